@@ -1,7 +1,7 @@
 """BitNet b1.58 BitLinear forward on MI355X (gfx950).
 
-A thin torch-facing binding over the C ABI in ``include/bitlinear.h``: these
-functions only check and marshal arguments (device pointers, sizes, the
+A thin torch-facing binding over the C ABI in ``include/bitlinear.h`` and
+``include/bitlinear_block.h``: these functions only check and marshal arguments (device pointers, sizes, the
 current HIP stream); every step of the computation runs in the HIP kernels of
 ``libbitlinear.so``.  There is no CPU fallback: without the built library or a
 GPU the calls raise.
@@ -34,6 +34,12 @@ __all__ = [
     "r3_decode_fits",
     "quantize_weights_r3",
     "forward_r3",
+    "save_activations",
+    "restore_activations",
+    "layer_norm",
+    "layer_norm_backward",
+    "relu2",
+    "relu2_backward",
 ]
 
 
@@ -480,3 +486,235 @@ def backward(dY, packedT, gamma, Xq, gamma_a, mask, K: int, need_dx: bool = True
                                      _ptr(mask), _ptr(dX), _ptr(dW), _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), _stream(dY)))
     return dX, dW
+
+
+# ---- the operators around BitLinear (include/bitlinear_block.h) -------------
+#
+# Activations saved in 8 bits are a pair (codes int8 [M, padded_k(K)], scales
+# float32 [M, padded_k(K) / 64]).  Every tensor of a call lies on one GPU, which
+# need not be the current one; the work goes to that GPU's current stream.
+
+_PLAIN = {}  # torch dtype -> abi dtype
+
+
+def _plain_dtype(dtype, name):
+    if not _PLAIN:
+        torch = _torch()
+        _PLAIN.update({torch.float32: abi.F32, torch.bfloat16: abi.BF16})
+    d = _PLAIN.get(dtype)
+    if d is None:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return d
+
+
+def _matrix(t, name, shape=None):
+    """Checks a contiguous GPU [M, K] tensor; its abi dtype."""
+    _require_cuda(t, name)
+    if t.dim() != 2 or t.numel() == 0:
+        raise ValueError(f"{name} must be [M, K] with at least one value")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return _plain_dtype(t.dtype, name)
+
+
+def _vector(t, n, device, name):
+    """The address of a float32 [n] tensor on `device` (None: 0)."""
+    if t is None:
+        return 0
+    torch = _torch()
+    _require_cuda(t, name)
+    if t.dtype != torch.float32 or t.numel() != n:
+        raise ValueError(f"{name} must hold {n} float32 values")
+    if t.device != device:
+        raise ValueError(f"{name} is on another device")
+    return t.data_ptr()
+
+
+def _whole_or_saved(x, K, name, M=None):
+    """(data address, scales address, abi dtype, M, K, device) of a [M, K] tensor or a saved pair."""
+    if not isinstance(x, (tuple, list)):
+        dt = _matrix(x, name)
+        m, k = x.shape
+        if (K is not None and k != K) or (M is not None and m != M):
+            raise ValueError(f"{name} does not have the other arrays' shape")
+        return x.data_ptr(), 0, dt, m, k, x.device
+    torch = _torch()
+    codes, scales = x
+    if K is None:
+        raise ValueError(f"K is needed where {name} is saved in 8 bits")
+    _require_cuda(codes, name + " codes")
+    _require_cuda(scales, name + " scales")
+    groups = (K + 63) // 64
+    m = codes.shape[0]
+    if codes.dtype != torch.int8 or codes.dim() != 2 or K < 1 or m < 1 or codes.shape[1] != 64 * groups:
+        raise ValueError(f"{name} codes must be int8 [M, padded_k(K)]")
+    if scales.dtype != torch.float32 or scales.shape != (m, groups):
+        raise ValueError(f"{name} scales must be float32 [M, padded_k(K) / 64]")
+    if scales.device != codes.device:
+        raise ValueError(f"{name} codes and scales are on different devices")
+    if M is not None and m != M:
+        raise ValueError(f"{name} does not have the other arrays' shape")
+    return codes.data_ptr(), scales.data_ptr(), abi.SAVED8, m, K, codes.device
+
+
+def _output(out, M, K, dtype, device, name="out"):
+    torch = _torch()
+    if out is None:
+        return torch.empty((M, K), dtype=dtype, device=device)
+    _require_cuda(out, name)
+    if out.shape != (M, K) or out.dtype != dtype or out.device != device:
+        raise ValueError(f"{name} must be {dtype} [{M}, {K}] on {device}")
+    return out
+
+
+def _empty_saved(M, K, device):
+    torch = _torch()
+    groups = (K + 63) // 64
+    return (torch.empty((M, 64 * groups), dtype=torch.int8, device=device),
+            torch.empty((M, groups), dtype=torch.float32, device=device))
+
+
+def _launch(name, device, *args):
+    """Calls a C function on `device`'s current stream, with that device current."""
+    torch = _torch()
+    fn = getattr(abi.load(), name)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    abi.check(name, status)
+
+
+def save_activations(X):
+    """X (float32 or bfloat16 [M, K]) in 8 bits: the pair (codes, scales)."""
+    dt = _matrix(X, "X")
+    M, K = X.shape
+    saved = _empty_saved(M, K, X.device)
+    _launch("bitlinear_save_activations", X.device, X.data_ptr(), dt, M, K, saved[0].data_ptr(),
+            saved[1].data_ptr())
+    return saved
+
+
+def restore_activations(saved, K: int, dtype=None, out=None):
+    """The [M, K] values that ``saved`` stands for, as float32 (default) or bfloat16."""
+    codes, scales, _, M, K, device = _whole_or_saved(tuple(saved), K, "saved")
+    dtype = _torch().float32 if dtype is None else dtype
+    dt = _plain_dtype(dtype, "dtype")
+    X = _output(out, M, K, dtype, device)
+    _launch("bitlinear_restore_activations", device, codes, scales, M, K, X.data_ptr(), dt)
+    return X
+
+
+def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, K: int | None = None, out_dtype=None,
+               return_stats: bool = False, save: bool = False, out=None):
+    """Layer norm over the rows of X: float32 or bfloat16 [M, K], or a saved pair (then K is needed).
+
+    ``weight``, ``bias``: float32 [K] or None.  Y is of ``out_dtype`` (default: X's; float32 for a saved
+    pair).  Returns Y; (Y, mean, rstd) with ``return_stats``, for :func:`layer_norm_backward`; and
+    (Y, mean, rstd, saved) with ``save``, X in 8 bits from the same pass.
+    """
+    torch = _torch()
+    x, xs, dt, M, K, device = _whole_or_saved(X, K, "X")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.float32 if dt == abi.SAVED8 else X.dtype
+    ydt = _plain_dtype(out_dtype, "out_dtype")
+    w, b = _vector(weight, K, device, "weight"), _vector(bias, K, device, "bias")
+    if save and dt == abi.SAVED8:
+        raise ValueError("X is saved already")
+    Y = _output(out, M, K, out_dtype, device)
+    mean = rstd = saved = None
+    mp = rp = cp = sp = 0
+    if return_stats or save:
+        mean, rstd = (torch.empty((M,), dtype=torch.float32, device=device) for _ in range(2))
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    if save:
+        saved = _empty_saved(M, K, device)
+        cp, sp = saved[0].data_ptr(), saved[1].data_ptr()
+    _launch("bitlinear_layer_norm", device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mp, rp, cp, sp)
+    return (Y, mean, rstd, saved) if save else (Y, mean, rstd) if return_stats else Y
+
+
+def layer_norm_backward(dY, X, mean, rstd, weight=None, out_dtype=None, need_dx: bool = True,
+                        need_dw: bool = True, workspace=None):
+    """Gradients (dX, dweight, dbias) of :func:`layer_norm` from dY (float32 or bfloat16 [M, K]).
+
+    ``X``: the forward's input, whole or as it was saved; ``mean``, ``rstd``: from the forward.  dX [M, K]
+    is of ``out_dtype`` (default: dY's), dweight and dbias are float32 [K]; None where not needed.
+    """
+    torch = _torch()
+    ddt = _matrix(dY, "dY")
+    M, K = dY.shape
+    device = dY.device
+    x, xs, dt, _, _, xdev = _whole_or_saved(X, K, "X", M)
+    if xdev != device:
+        raise ValueError("X is on another device")
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward are needed")
+    mp, rp = _vector(mean, M, device, "mean"), _vector(rstd, M, device, "rstd")
+    w = _vector(weight, K, device, "weight")
+    if not (need_dx or need_dw):
+        raise ValueError("nothing to compute")
+    out_dtype = dY.dtype if out_dtype is None else out_dtype
+    odt = _plain_dtype(out_dtype, "out_dtype")
+    dX = dw = db = None
+    dxp = dwp = dbp = wsp = ws_bytes = 0
+    if need_dx:
+        dX = torch.empty((M, K), dtype=out_dtype, device=device)
+        dxp = dX.data_ptr()
+    if need_dw:
+        dw, db = (torch.empty((K,), dtype=torch.float32, device=device) for _ in range(2))
+        dwp, dbp = dw.data_ptr(), db.data_ptr()
+        if workspace is None:
+            ws_bytes = abi.load().bitlinear_layer_norm_backward_workspace_bytes(M, K)
+            workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=device)
+        else:
+            _require_cuda(workspace, "workspace")
+            if workspace.device != device:
+                raise ValueError("workspace is on another device")
+            ws_bytes = workspace.numel() * workspace.element_size()
+        wsp = workspace.data_ptr()
+    _launch("bitlinear_layer_norm_backward", device, dY.data_ptr(), ddt, x, xs, dt, mp, rp, M, K, w, dxp, odt,
+            dwp, dbp, wsp, ws_bytes)
+    return dX, dw, db
+
+
+def relu2(H, K: int | None = None, out_dtype=None, save: bool = False, out=None):
+    """A = max(H, 0)^2 for H float32 or bfloat16 [M, K], or a saved pair (then K is needed).
+
+    A is of ``out_dtype`` (default: H's; float32 for a saved pair).  With ``save`` returns (A, saved), H in
+    8 bits from the same pass.
+    """
+    torch = _torch()
+    h, hs, dt, M, K, device = _whole_or_saved(H, K, "H")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.float32 if dt == abi.SAVED8 else H.dtype
+    adt = _plain_dtype(out_dtype, "out_dtype")
+    if save and dt == abi.SAVED8:
+        raise ValueError("H is saved already")
+    A = _output(out, M, K, out_dtype, device)
+    saved, cp, sp = None, 0, 0
+    if save:
+        saved = _empty_saved(M, K, device)
+        cp, sp = saved[0].data_ptr(), saved[1].data_ptr()
+    _launch("bitlinear_relu2", device, h, hs, dt, M, K, A.data_ptr(), adt, cp, sp)
+    return (A, saved) if save else A
+
+
+def relu2_backward(dA, H, out_dtype=None, out=None):
+    """dH = dA * 2 max(H, 0) from dA (float32 or bfloat16 [M, K]) and H, whole or as it was saved.
+
+    dH is of ``out_dtype`` (default: dA's; bfloat16 is what :func:`backward` takes).
+    """
+    adt = _matrix(dA, "dA")
+    M, K = dA.shape
+    h, hs, dt, _, _, hdev = _whole_or_saved(H, K, "H", M)
+    if hdev != dA.device:
+        raise ValueError("H is on another device")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else dA.dtype
+    odt = _plain_dtype(out_dtype, "out_dtype")
+    dH = _output(out, M, K, out_dtype, dA.device)
+    _launch("bitlinear_relu2_backward", dA.device, dA.data_ptr(), adt, h, hs, dt, M, K, dH.data_ptr(), odt)
+    return dH

@@ -1,5 +1,5 @@
-"""ctypes view of libbitlinear.so (the C ABI declared in include/bitlinear.h)
-and of the benchmark's probe library libbitlinear_probe.so
+"""ctypes view of libbitlinear.so (the C ABI declared in include/bitlinear.h and
+include/bitlinear_block.h) and of the benchmark's probe library libbitlinear_probe.so
 (include/bitlinear_probe.h).
 
 Loading is lazy and fails loudly: there is no fallback implementation.
@@ -22,6 +22,7 @@ ERR_ARG = -7
 
 F32 = 0
 BF16 = 1
+SAVED8 = 2  # an input saved in 8 bits (bitlinear_block.h)
 
 PATH_AUTO = 0
 PATH_DECODE = 1
@@ -29,6 +30,7 @@ PATH_PREFILL = 2
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 _p = ctypes.c_void_p
 
@@ -61,6 +63,19 @@ SIGNATURES = {
     "bitlinear_forward_lut": (_int, [_i64, _p, _int, _i64, _i64, _p, _i64, _p, _p, _p, _p, _sz, _p]),
     "bitlinear_forward_noalloc": (_int, [_p, _int, _i64, _i64, _p, _i64, _p, _p, _p]),
     "bitlinear_status_string": (ctypes.c_char_p, [_int]),
+}
+
+# the operators around BitLinear (include/bitlinear_block.h, same library)
+BLOCK_SIGNATURES = {
+    "bitlinear_saved_groups": (_i64, [_i64]),
+    "bitlinear_save_activations": (_int, [_p, _int, _i64, _i64, _p, _p, _p]),
+    "bitlinear_restore_activations": (_int, [_p, _p, _i64, _i64, _p, _int, _p]),
+    "bitlinear_layer_norm": (_int, [_p, _p, _int, _i64, _i64, _p, _p, _f32, _p, _int, _p, _p, _p, _p, _p]),
+    "bitlinear_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "bitlinear_layer_norm_backward": (_int, [_p, _int, _p, _p, _int, _p, _p, _i64, _i64, _p, _p, _int, _p, _p,
+                                             _p, _sz, _p]),
+    "bitlinear_relu2": (_int, [_p, _p, _int, _i64, _i64, _p, _int, _p, _p, _p]),
+    "bitlinear_relu2_backward": (_int, [_p, _int, _p, _p, _int, _i64, _i64, _p, _int, _p]),
 }
 
 NOALLOC_SCRATCH_BYTES = 80 * 1024 * 1024  # BITLINEAR_NOALLOC_SCRATCH_BYTES
@@ -106,7 +121,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the BitLinear HIP library (once).  Raises if it has not been built."""
     global _LIB
     if _LIB is None:
-        _LIB = _open(path, SIGNATURES)
+        _LIB = _open(path, {**SIGNATURES, **BLOCK_SIGNATURES})
     return _LIB
 
 

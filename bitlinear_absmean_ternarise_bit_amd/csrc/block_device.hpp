@@ -1,0 +1,203 @@
+// Device helpers of the operators around BitLinear: rows in chunks of eight
+// values, the 8-bit saved format, reductions.
+//
+// Every kernel works on chunks of 8 consecutive columns of a row, one lane to
+// a chunk whatever the type (32 bytes of float32, 16 of bfloat16, 8 codes), so
+// that a 64-column group of the saved format is 8 neighbouring lanes and its
+// largest magnitude comes from three DPP moves.  A row's start need only be
+// aligned to its element: gfx950 takes 16-byte accesses at any address, and
+// hipcc emits them for the under-aligned vector types below.  The last chunk
+// of a row may hold fewer than 8 values; it goes value by value.
+#pragma once
+
+#include "block_ops.hpp"
+#include "common.hpp"
+
+namespace bitlinear {
+
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef v4u v4u_by4 __attribute__((aligned(4)));
+typedef v4u v4u_by2 __attribute__((aligned(2)));
+
+template <int DT>
+constexpr int kBytes = DT == kF32 ? 4 : DT == kBf16 ? 2 : 1;
+
+// One chunk as it lies in memory.
+template <int DT>
+struct Raw;
+template <>
+struct Raw<kF32> {
+  v4u a, b;
+};
+template <>
+struct Raw<kBf16> {
+  v4u a;
+};
+template <>
+struct Raw<kSaved8> {
+  v2u a;
+  float scale;
+};
+
+// Values of chunk c that lie inside a row of K (0 to 8).
+__device__ __forceinline__ int chunk_values(int K, int c) { return max(0, min(8, K - 8 * c)); }
+
+// Chunk c (n values) of the row at `row`; `scales`: the row's scales (kSaved8,
+// whose rows are padded with zero codes, so every chunk below Kp / 8 is whole).
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_chunk(const char* row, const float* scales, int c, int n) {
+  Raw<DT> r;
+  if constexpr (DT == kSaved8) {
+    r.a = v2u{0u, 0u};
+    r.scale = 0.0f;
+    if (n > 0) {
+      r.a = *reinterpret_cast<const v2u*>(row + 8 * c);
+      r.scale = scales[c >> 3];
+    }
+  } else if constexpr (DT == kBf16) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + 8 * c;
+    r.a = v4u{0u, 0u, 0u, 0u};
+    if (n == 8) {
+      r.a = *reinterpret_cast<const v4u_by2*>(p);
+    } else if (n > 0) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n) r.a[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+    }
+  } else {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + 8 * c;
+    r.a = v4u{0u, 0u, 0u, 0u};
+    r.b = v4u{0u, 0u, 0u, 0u};
+    if (n == 8) {
+      r.a = *reinterpret_cast<const v4u_by4*>(p);
+      r.b = *reinterpret_cast<const v4u_by4*>(p + 4);
+    } else if (n > 0) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n) (i < 4 ? r.a : r.b)[i & 3] = p[i];
+    }
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void chunk_f32(const Raw<DT>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (DT == kF32) {
+      v[i] = __uint_as_float(i < 4 ? r.a[i & 3] : r.b[i & 3]);
+    } else if constexpr (DT == kBf16) {
+      v[i] = __uint_as_float((i & 1) ? r.a[i >> 1] & 0xffff0000u : r.a[i >> 1] << 16);
+    } else {
+      const int q = static_cast<int>(r.a[i >> 2] << (24 - 8 * (i & 3))) >> 24;
+      v[i] = __fmul_rn(r.scale, static_cast<float>(q));
+    }
+  }
+}
+
+// Two float32 as packed bfloat16, each rounded half to even.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+template <int DT>
+__device__ __forceinline__ void store_chunk(char* row, int c, int n, const float (&v)[8]) {
+  static_assert(DT != kSaved8, "saved rows are written by save_chunk");
+  if constexpr (DT == kBf16) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(row) + 8 * c;
+    const v4u w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    if (n == 8) {
+      *reinterpret_cast<v4u_by2*>(p) = w;
+    } else if (n > 0) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
+  } else {
+    uint32_t* p = reinterpret_cast<uint32_t*>(row) + 8 * c;
+    if (n == 8) {
+      *reinterpret_cast<v4u_by4*>(p) = v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                           __float_as_uint(v[3])};
+      *reinterpret_cast<v4u_by4*>(p + 4) = v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                                               __float_as_uint(v[7])};
+    } else if (n > 0) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n) p[i] = __float_as_uint(v[i]);
+    }
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_move(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
+}
+
+// Saves chunk c (v is 0 past the row's end): its codes at `codes` + 8 c and,
+// by the first lane of each group, the group's scale.  All 8 lanes of a group
+// take part.  |x| is compared as an integer, so a NaN is the largest.
+// x * s is rounded to an integer by one FMA with 1.5 * 2^23: the sum has unit
+// spacing and rounds the exact product half to even, and its low byte is the
+// code.  No step depends on the order of anything: the codes are the same
+// whichever kernel saves.
+__device__ __forceinline__ void save_chunk(const float (&v)[8], int8_t* codes, float* scales, int c) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  m = max(m, static_cast<unsigned>(dpp_move<0xb1>(static_cast<int>(m))));   // quad_perm 1,0,3,2
+  m = max(m, static_cast<unsigned>(dpp_move<0x4e>(static_cast<int>(m))));   // quad_perm 2,3,0,1
+  m = max(m, static_cast<unsigned>(dpp_move<0x141>(static_cast<int>(m))));  // row_half_mirror
+  const float amax = __uint_as_float(m);
+  const bool finite = m < 0x7f800000u;
+  const bool live = finite && amax >= 0x1p-100f;
+  const float s = live ? __fdiv_rn(127.0f, amax) : 0.0f;
+  const float scale = live ? __fmul_rn(amax, 1.0f / 127.0f) : finite ? 0.0f : __uint_as_float(0x7fc00000u);
+  v2u w = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i >> 2] |= (__float_as_uint(__fmaf_rn(v[i], s, 12582912.0f)) & 0xffu) << (8 * (i & 3));
+  if (!finite) w = v2u{0u, 0u};
+  *reinterpret_cast<v2u*>(codes + 8 * c) = w;
+  if ((c & 7) == 0) scales[c >> 3] = scale;
+}
+
+// Sum over a wave, in every lane: within each row of 16 lanes by DPP moves,
+// then the four rows' sums, always in the same order.
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  v += __int_as_float(dpp_move<0xb1>(__float_as_int(v)));
+  v += __int_as_float(dpp_move<0x4e>(__float_as_int(v)));
+  v += __int_as_float(dpp_move<0x141>(__float_as_int(v)));
+  v += __int_as_float(dpp_move<0x140>(__float_as_int(v)));
+  const int b = __float_as_int(v);
+  return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
+         (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
+}
+
+// Sums of NV values over a team of W waves of the workgroup, in every lane.
+// slot: this reduction's LDS area, W x NV floats of the team's own; two
+// consecutive reductions use different slots (a wave that is still reading one
+// has not passed the barrier of the next).  Every wave of the workgroup calls.
+template <int W, int NV>
+__device__ __forceinline__ void team_sum(float (&v)[NV], float* slot, int wave_in_team, int lane) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = wave_sum_f32(v[i]);
+  if constexpr (W > 1) {
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) slot[wave_in_team * NV + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) t += slot[w * NV + i];
+      v[i] = t;
+    }
+  }
+}
+
+}  // namespace bitlinear

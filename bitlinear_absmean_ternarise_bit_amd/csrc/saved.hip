@@ -1,0 +1,108 @@
+// 8-bit saved activations (save, restore) and ReLU^2 with its backward pass
+// (include/bitlinear_block.h): one read of each input, one write of each
+// output, chunk by chunk.
+#include "block_device.hpp"
+
+namespace bitlinear {
+
+namespace {
+
+// What a pass over [M, K] does with a chunk.
+enum Op { kSave, kRestore, kRelu2, kRelu2Backward };
+
+// max(h, 0), and a NaN for a NaN
+__device__ __forceinline__ float relu(float h) { return h <= 0.0f ? 0.0f : h; }
+
+// One thread per chunk; row m of the array is chunks m * cpr .. of the grid's
+// index (cpr = Kp / 8, so the 8 lanes of a group are neighbours).
+//   kSave:          in -> codes, scales
+//   kRestore:       in (saved) -> out
+//   kRelu2:         in -> out (and codes, scales when SAVE)
+//   kRelu2Backward: dA, in -> out
+template <int OP, int IT, int OT, int DT, bool SAVE>
+__global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in, const float* __restrict__ in_scales,
+                                                    const char* __restrict__ dA, int64_t M, int K, int cpr,
+                                                    char* __restrict__ out, int8_t* __restrict__ codes,
+                                                    float* __restrict__ scales) {
+  const int64_t total = M * cpr;
+  const int64_t G = cpr >> 3, Kp = int64_t(cpr) * 8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t m = i / cpr;
+    const int c = static_cast<int>(i - m * cpr);
+    const int n = chunk_values(K, c);
+    float v[8];
+    chunk_f32<IT>(load_chunk<IT>(in + (IT == kSaved8 ? m * Kp : m * K * kBytes<IT>), in_scales + m * G, c, n), v);
+    if constexpr (SAVE) save_chunk(v, codes + m * Kp, scales + m * G, c);
+    if constexpr (OP == kRelu2) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float r = relu(v[e]);
+        v[e] = __fmul_rn(r, r);
+      }
+    } else if constexpr (OP == kRelu2Backward) {
+      float d[8];
+      chunk_f32<DT>(load_chunk<DT>(dA + m * K * kBytes<DT>, nullptr, c, n), d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(d[e], 2.0f * relu(v[e]));
+    }
+    if constexpr (OP != kSave) store_chunk<OT>(out + m * K * kBytes<OT>, c, n, v);
+  }
+}
+
+template <int OP, int IT, int OT, int DT, bool SAVE>
+hipError_t launch(BlockIn in, const void* dA, int64_t M, int64_t K, void* out, int8_t* codes, float* scales,
+                  hipStream_t stream) {
+  const int cpr = static_cast<int>(padded_k(K) / 8);
+  int64_t blocks = (M * cpr + 255) / 256;
+  if (blocks > 1 << 20) blocks = 1 << 20;
+  chunk_kernel<OP, IT, OT, DT, SAVE><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+      static_cast<const char*>(in.p), in.scales, static_cast<const char*>(dA), M, static_cast<int>(K), cpr,
+      static_cast<char*>(out), codes, scales);
+  return hipGetLastError();
+}
+
+template <int OP, int OT, int DT>
+hipError_t launch_any(BlockIn in, const void* dA, int64_t M, int64_t K, void* out, hipStream_t s) {
+  if (in.dtype == kF32) return launch<OP, kF32, OT, DT, false>(in, dA, M, K, out, nullptr, nullptr, s);
+  if (in.dtype == kBf16) return launch<OP, kBf16, OT, DT, false>(in, dA, M, K, out, nullptr, nullptr, s);
+  return launch<OP, kSaved8, OT, DT, false>(in, dA, M, K, out, nullptr, nullptr, s);
+}
+
+template <int OT>
+hipError_t launch_relu2_to(BlockIn H, int64_t M, int64_t K, void* A, int8_t* codes, float* scales, hipStream_t s) {
+  if (codes && H.dtype == kF32) return launch<kRelu2, kF32, OT, kF32, true>(H, nullptr, M, K, A, codes, scales, s);
+  if (codes) return launch<kRelu2, kBf16, OT, kF32, true>(H, nullptr, M, K, A, codes, scales, s);
+  return launch_any<kRelu2, OT, kF32>(H, nullptr, M, K, A, s);
+}
+
+}  // namespace
+
+hipError_t launch_save(const void* X, int x_dtype, int64_t M, int64_t K, int8_t* codes, float* scales,
+                       hipStream_t s) {
+  const BlockIn in = {X, nullptr, x_dtype};
+  if (x_dtype == kF32) return launch<kSave, kF32, kF32, kF32, true>(in, nullptr, M, K, nullptr, codes, scales, s);
+  return launch<kSave, kBf16, kF32, kF32, true>(in, nullptr, M, K, nullptr, codes, scales, s);
+}
+
+hipError_t launch_restore(BlockIn in, int64_t M, int64_t K, void* X, int x_dtype, hipStream_t s) {
+  if (x_dtype == kF32) return launch<kRestore, kSaved8, kF32, kF32, false>(in, nullptr, M, K, X, nullptr, nullptr, s);
+  return launch<kRestore, kSaved8, kBf16, kF32, false>(in, nullptr, M, K, X, nullptr, nullptr, s);
+}
+
+hipError_t launch_relu2(BlockIn H, int64_t M, int64_t K, void* A, int a_dtype, int8_t* saved, float* saved_scales,
+                        hipStream_t s) {
+  if (a_dtype == kF32) return launch_relu2_to<kF32>(H, M, K, A, saved, saved_scales, s);
+  return launch_relu2_to<kBf16>(H, M, K, A, saved, saved_scales, s);
+}
+
+hipError_t launch_relu2_backward(const void* dA, int da_dtype, BlockIn H, int64_t M, int64_t K, void* dH,
+                                 int dh_dtype, hipStream_t s) {
+  if (da_dtype == kF32)
+    return dh_dtype == kF32 ? launch_any<kRelu2Backward, kF32, kF32>(H, dA, M, K, dH, s)
+                            : launch_any<kRelu2Backward, kBf16, kF32>(H, dA, M, K, dH, s);
+  return dh_dtype == kF32 ? launch_any<kRelu2Backward, kF32, kBf16>(H, dA, M, K, dH, s)
+                          : launch_any<kRelu2Backward, kBf16, kBf16>(H, dA, M, K, dH, s);
+}
+
+}  // namespace bitlinear
