@@ -7,7 +7,7 @@
 // largest magnitude comes from three DPP moves.  A row's start need only be
 // aligned to its element: gfx950 takes 16-byte accesses at any address, and
 // hipcc emits them for the under-aligned vector types below.  The last chunk
-// of a row may hold fewer than 8 values; it goes value by value.
+// of a row may hold fewer than 8 values.
 #pragma once
 
 #include "block_ops.hpp"
@@ -41,13 +41,36 @@ struct Raw<kSaved8> {
   float scale;
 };
 
+// The wave's number in its workgroup, as a scalar: row addresses and per-row
+// loads that follow from it stay out of the vector registers.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6)); }
+
 // Values of chunk c that lie inside a row of K (0 to 8).
 __device__ __forceinline__ int chunk_values(int K, int c) { return max(0, min(8, K - 8 * c)); }
 
-// Chunk c (n values) of the row at `row`; `scales`: the row's scales (kSaved8,
-// whose rows are padded with zero codes, so every chunk below Kp / 8 is whole).
+// The last n < 8 values of a row, moved down to the front of the chunk and
+// followed by zeros, from the row's last 8 values.
+__device__ __forceinline__ void move_down(v4u& a, v4u& b, int n) {  // 32-bit values in a, b
+  const int by = 8 - n;
+  if (by & 4) a = b, b = v4u{0u, 0u, 0u, 0u};
+  if (by & 2) a = v4u{a.z, a.w, b.x, b.y}, b = v4u{b.z, b.w, 0u, 0u};
+  if (by & 1) a = v4u{a.y, a.z, a.w, b.x}, b = v4u{b.y, b.z, b.w, 0u};
+}
+__device__ __forceinline__ void move_down(v4u& a, int n) {  // 16-bit values
+  const int by = 8 - n;
+  if (by & 4) a = v4u{a.z, a.w, 0u, 0u};
+  if (by & 2) a = v4u{a.y, a.z, a.w, 0u};
+  if (by & 1)
+    a = v4u{(a.x >> 16) | (a.y << 16), (a.y >> 16) | (a.z << 16), (a.z >> 16) | (a.w << 16), a.w >> 16};
+}
+
+// Chunk c (n values) of the row of K values at `row`; `scales`: the row's
+// scales (kSaved8, whose rows are padded with zero codes, so every chunk below
+// Kp / 8 is whole).  The row's end is read as its last 8 values (one load, like
+// every other chunk: value by value the loads would wait for one another, 4 us
+// a row) and moved into place; only a row of fewer than 8 goes value by value.
 template <int DT>
-__device__ __forceinline__ Raw<DT> load_chunk(const char* row, const float* scales, int c, int n) {
+__device__ __forceinline__ Raw<DT> load_chunk(const char* row, const float* scales, int K, int c, int n) {
   Raw<DT> r;
   if constexpr (DT == kSaved8) {
     r.a = v2u{0u, 0u};
@@ -57,26 +80,42 @@ __device__ __forceinline__ Raw<DT> load_chunk(const char* row, const float* scal
       r.scale = scales[c >> 3];
     }
   } else if constexpr (DT == kBf16) {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + 8 * c;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
     r.a = v4u{0u, 0u, 0u, 0u};
-    if (n == 8) {
-      r.a = *reinterpret_cast<const v4u_by2*>(p);
+    if (K >= 8) {
+      if (n > 0) r.a = *reinterpret_cast<const v4u_by2*>(p + (n == 8 ? 8 * c : K - 8));
+      if (n > 0 && n < 8) move_down(r.a, n);
     } else if (n > 0) {
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (i < n) r.a[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+      for (int i = 0; i < n; ++i) {
+        const uint32_t v = static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+        if (i < 2) r.a.x |= v;
+        else if (i < 4) r.a.y |= v;
+        else if (i < 6) r.a.z |= v;
+        else r.a.w |= v;
+      }
     }
   } else {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + 8 * c;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
     r.a = v4u{0u, 0u, 0u, 0u};
     r.b = v4u{0u, 0u, 0u, 0u};
-    if (n == 8) {
-      r.a = *reinterpret_cast<const v4u_by4*>(p);
-      r.b = *reinterpret_cast<const v4u_by4*>(p + 4);
+    if (K >= 8) {
+      if (n > 0) {
+        p += n == 8 ? 8 * c : K - 8;
+        r.a = *reinterpret_cast<const v4u_by4*>(p);
+        r.b = *reinterpret_cast<const v4u_by4*>(p + 4);
+        if (n < 8) move_down(r.a, r.b, n);
+      }
     } else if (n > 0) {
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (i < n) (i < 4 ? r.a : r.b)[i & 3] = p[i];
+      for (int i = 0; i < n; ++i) {
+        const uint32_t v = p[i];
+        if (i == 0) r.a.x = v;
+        else if (i == 1) r.a.y = v;
+        else if (i == 2) r.a.z = v;
+        else if (i == 3) r.a.w = v;
+        else if (i == 4) r.b.x = v;
+        else if (i == 5) r.b.y = v;
+        else r.b.z = v;
+      }
     }
   }
   return r;
@@ -91,8 +130,10 @@ __device__ __forceinline__ void chunk_f32(const Raw<DT>& r, float (&v)[8]) {
     } else if constexpr (DT == kBf16) {
       v[i] = __uint_as_float((i & 1) ? r.a[i >> 1] & 0xffff0000u : r.a[i >> 1] << 16);
     } else {
-      const int q = static_cast<int>(r.a[i >> 2] << (24 - 8 * (i & 3))) >> 24;
-      v[i] = __fmul_rn(r.scale, static_cast<float>(q));
+      // code + 128 is a byte, one conversion; 128 scale is exact, so the FMA
+      // rounds scale * code once
+      const uint32_t u = ((r.a[i >> 2] ^ 0x80808080u) >> (8 * (i & 3))) & 0xffu;
+      v[i] = __fmaf_rn(r.scale, static_cast<float>(u), -128.0f * r.scale);
     }
   }
 }
@@ -180,8 +221,10 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
 // slot: this reduction's LDS area, W x NV floats of the team's own; two
 // consecutive reductions use different slots (a wave that is still reading one
 // has not passed the barrier of the next).  Every wave of the workgroup calls.
+// Lane i reads wave i % W's sum, and DPP moves add them in every lane.
 template <int W, int NV>
 __device__ __forceinline__ void team_sum(float (&v)[NV], float* slot, int wave_in_team, int lane) {
+  static_assert(W == 1 || W == 2 || W == 4 || W == 8 || W == 16, "waves of a team");
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i] = wave_sum_f32(v[i]);
   if constexpr (W > 1) {
@@ -192,10 +235,12 @@ __device__ __forceinline__ void team_sum(float (&v)[NV], float* slot, int wave_i
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float t = 0.0f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) t += slot[w * NV + i];
-      v[i] = t;
+      float t = slot[(lane & (W - 1)) * NV + i];
+      t += __int_as_float(dpp_move<0xb1>(__float_as_int(t)));
+      if constexpr (W >= 4) t += __int_as_float(dpp_move<0x4e>(__float_as_int(t)));
+      if constexpr (W >= 8) t += __int_as_float(dpp_move<0x141>(__float_as_int(t)));
+      if constexpr (W >= 16) t += __int_as_float(dpp_move<0x140>(__float_as_int(t)));
+      v[i] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(t)));
     }
   }
 }

@@ -21,19 +21,55 @@ struct BlockIn {
   int dtype;
 };
 
-// Sets of rows whose dweight / dbias sums are formed apart, for rows that the
-// column kernel sums: 32 columns of 8 to a workgroup, about 1024 workgroups.
-inline int64_t ln_param_slabs(int64_t M, int64_t K) {
-  const int64_t col_blocks = (padded_k(K) / 8 + 31) / 32;
-  int64_t s = 1024 / col_blocks;
-  if (s > 256) s = 256;
-  if (s > (M + 7) / 8) s = (M + 7) / 8;
-  return s < 1 ? 1 : s;
+// How layer norm's backward pass is cut up.  Rows of at most kLnBwdMaxChunks
+// chunks of 8 (K <= 32768) go through one kernel: `waves` waves to a row,
+// `chunks` chunks to a lane, `teams` rows at a time in a workgroup, `groups`
+// workgroups.  K <= 8192: one chunk to a lane, as many waves as that takes, 16
+// in a workgroup.  Longer: 8 waves with 3, 4 or 8 chunks to a lane, alone in the
+// workgroup, which leaves each lane 256 registers; with 8 the row is not held
+// between its two passes.
+// About one workgroup to each of the 256 CUs: the parameter gradients leave as
+// one partial row from each, and more of them would cost more than they hide.
+// So few rows that one workgroup takes them in two turns are left to one: it
+// writes the gradients itself, and the second launch (about as long as a turn)
+// is saved.
+// Longer rows still (waves = 0): `groups` sets of rows for the column kernel,
+// 32 chunks of columns to a workgroup, about 1024 workgroups.
+struct LnBwdPlan {
+  int waves, chunks, teams, groups;
+};
+constexpr int64_t kLnBwdMaxChunks = 2048;
+
+inline LnBwdPlan ln_bwd_plan(int64_t M, int64_t K, bool params) {
+  const int64_t cpr = padded_k(K) / 8;
+  LnBwdPlan p = {0, 1, 1, 1};
+  if (cpr > kLnBwdMaxChunks) {
+    int64_t s = 1024 / ((cpr + 31) / 32);
+    if (s > 256) s = 256;
+    if (s > (M + 7) / 8) s = (M + 7) / 8;
+    p.groups = static_cast<int>(s < 1 ? 1 : s);
+    return p;
+  }
+  int64_t most = 1;  // teams of a workgroup
+  if (cpr <= 1024) {
+    p.waves = 1;
+    while (64 * p.waves < cpr) p.waves *= 2;
+    most = 16 / p.waves;
+  } else {
+    p.waves = 8;
+    p.chunks = cpr <= 1536 ? 3 : 4;
+  }
+  const bool alone = params && M <= 2 * most;
+  const int64_t teams = alone ? M : (M + 255) / 256;
+  p.teams = static_cast<int>(teams < most ? teams : most);
+  const int64_t groups = (M + p.teams - 1) / p.teams;
+  p.groups = static_cast<int>(alone ? 1 : groups < 256 ? groups : 256);
+  return p;
 }
 
 inline size_t ln_bwd_workspace_bytes(int64_t M, int64_t K) {
   if (!size_args_ok(M) || !size_args_ok(K)) return 0;
-  return align256(size_mul(size_t(ln_param_slabs(M, K)), size_mul(size_t(K), 8)));
+  return align256(size_mul(size_t(ln_bwd_plan(M, K, true).groups), size_mul(size_t(K), 8)));
 }
 
 hipError_t launch_save(const void* X, int x_dtype, int64_t M, int64_t K, int8_t* codes, float* scales,

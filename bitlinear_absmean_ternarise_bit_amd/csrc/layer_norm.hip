@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     float sum[1] = {0.0f};
     for (int c = tid; c < cpr; c += 256) {
       float v[8];
-      chunk_f32<XT>(load_chunk<XT>(row, rs, c, chunk_values(K, c)), v);
+      chunk_f32<XT>(load_chunk<XT>(row, rs, K, c, chunk_values(K, c)), v);
       if constexpr (SAVE) save_chunk(v, codes + m * Kp, scales + m * G, c);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[0] += v[e];
@@ -36,7 +36,7 @@ __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     for (int c = tid; c < cpr; c += 256) {
       const int n = chunk_values(K, c);
       float v[8];
-      chunk_f32<XT>(load_chunk<XT>(row, rs, c, n), v);
+      chunk_f32<XT>(load_chunk<XT>(row, rs, K, c, n), v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = e < n ? v[e] - mean : 0.0f;
@@ -48,9 +48,9 @@ __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     for (int c = tid; c < cpr; c += 256) {
       const int n = chunk_values(K, c);
       float v[8], w[8], b[8];
-      chunk_f32<XT>(load_chunk<XT>(row, rs, c, n), v);
-      if (weight) chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, c, n), w);
-      if (bias) chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(bias), nullptr, c, n), b);
+      chunk_f32<XT>(load_chunk<XT>(row, rs, K, c, n), v);
+      if (weight) chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, K, c, n), w);
+      if (bias) chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(bias), nullptr, K, c, n), b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float xh = (v[e] - mean) * rstd;

@@ -2,14 +2,161 @@
 // xhat = (x - mean) rstd and g = dy w:
 //   dx = rstd (g - sum_k g / K - xhat sum_k (g xhat) / K)
 //   dw = sum_m dy xhat,  db = sum_m dy
-// in float32, from x as it was or from its 8-bit copy.
+// in float32, from x as it was or from its 8-bit copy.  Bound by the bytes of
+// x, dy and dx: ln_backward_kernel reads each row once and keeps it in
+// registers between the row's sums and its dx, with the columns' dw and db in
+// registers across all of a workgroup's rows.  Rows over kLnBwdMaxChunks chunks
+// take the two kernels below it, which read the rows twice each.
 #include "block_device.hpp"
 
 namespace bitlinear {
 
 namespace {
 
-// dx: one workgroup per row, rows gridDim.x apart; the row is read for the two
+// dx, dw and db in one pass.  A team of W waves holds a row, NC chunks of 8
+// columns to a lane; a workgroup is T = blockDim.x / (64 W) teams.  Team t of
+// workgroup b takes rows (i G + b) T + t, i = 0, 1, ...  (G workgroups).  A row
+// is converted to xhat and g in registers, and the next one's loads are issued
+// before the sums are formed, so that they are in flight through the reduction,
+// its barrier and the stores.  A team past the last row works on zeros.  At the
+// end the teams' dw and db are added through LDS and the workgroup writes one
+// partial row of each (the gradients themselves where it is the only one), so
+// no sum depends on the order in which anything runs.
+//
+// The vector ALU is the second bound: about 180 instructions for a wave's 512
+// columns are 7 TB/s at float32 dy and bfloat16 dx.  So dx is two FMAs,
+//   dx = rstd g - rstd c1 - xhat (rstd c2),   c1, c2 the sums over K,
+// and a value is converted once.
+template <int XT, int DT, int OT, int W, int NC, int THREADS>
+__global__ __launch_bounds__(THREADS) void ln_backward_kernel(
+    const char* __restrict__ dY, const char* __restrict__ X, const float* __restrict__ x_scales,
+    const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t M, int K, int cpr,
+    const float* __restrict__ weight, char* __restrict__ dX, float* __restrict__ dw_out, float* __restrict__ db_out,
+    int64_t out_stride) {
+  constexpr bool kWeightInLds = NC > 1;  // else in registers
+  constexpr int kMaxT = THREADS / (64 * W);
+  constexpr int kTeamFloats = 64 * W * NC * 8;                     // one row
+  constexpr int kLds = kTeamFloats * (kMaxT > 2 ? kMaxT / 2 : 1);  // the weight; later half the teams' sums
+  __shared__ float slots[2][kMaxT * W * 2];
+  __shared__ __align__(16) float lds[kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  const int team = wave / W, wt = wave % W, T = blockDim.x / (64 * W);
+  const int64_t G = cpr >> 3, Kp = int64_t(cpr) * 8;
+  const float inv_k = 1.0f / static_cast<float>(K);
+  // lane's place in a team's area, chunk j: 8 floats in two halves, so that a
+  // wave's 16-byte accesses are consecutive
+  auto place = [&](int t, int j, int half) { return t * kTeamFloats + ((j * 2 + half) * 64 * W + wt * 64 + lane) * 4; };
+  int c[NC], n[NC];
+  float dw[NC][8], db[NC][8], held_w[8];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    c[j] = wt * 64 + lane + j * 64 * W;
+    n[j] = c[j] < cpr ? chunk_values(K, c[j]) : 0;
+    float w[8];
+    if (weight) {
+      chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, K, c[j], n[j]), w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dw[j][e] = db[j][e] = 0.0f;
+      if constexpr (kWeightInLds) lds[place(0, j, e >> 2) + (e & 3)] = w[e];
+      else held_w[e] = w[e];
+    }
+  }
+  auto weight_of = [&](int j, int e) {
+    if constexpr (kWeightInLds) return lds[place(0, j, e >> 2) + (e & 3)];
+    else return held_w[e];
+  };
+  Raw<XT> rx[NC];
+  Raw<DT> rd[NC];
+  float next_mean, next_rstd;
+  auto load_row = [&](int64_t m) {
+    const bool ok = m < M;
+    if (!ok) m = 0;
+    next_mean = ok ? mean_in[m] : 0.0f;
+    next_rstd = ok ? rstd_in[m] : 0.0f;
+    const char* row = X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>);
+    const char* drow = dY + m * K * kBytes<DT>;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      rx[j] = load_chunk<XT>(row, x_scales + m * G, K, c[j], ok ? n[j] : 0);
+      rd[j] = load_chunk<DT>(drow, nullptr, K, c[j], ok ? n[j] : 0);
+    }
+  };
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * T;
+  int64_t m = static_cast<int64_t>(blockIdx.x) * T + team;
+  const int64_t iters = (M + stride - 1) / stride;
+  load_row(m);
+  for (int64_t it = 0; it < iters; ++it, m += stride) {
+    const float mu = next_mean, rs = next_rstd;
+    float xh[NC][8], g[NC][8], s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      chunk_f32<XT>(rx[j], xh[j]);
+      chunk_f32<DT>(rd[j], g[j]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xh[j][e] = (xh[j][e] - mu) * rs;
+    }
+    if (it + 1 < iters) load_row(m + stride);
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        db[j][e] += g[j][e];
+        dw[j][e] = __fmaf_rn(g[j][e], xh[j][e], dw[j][e]);
+        g[j][e] *= weight_of(j, e);
+        s[0] += g[j][e];
+        s[1] = __fmaf_rn(g[j][e], xh[j][e], s[1]);
+      }
+    team_sum<W>(s, slots[it & 1] + team * W * 2, wt, lane);
+    if (!dX || m >= M) continue;
+    const float k1 = rs * (s[0] * inv_k), k2 = rs * (s[1] * inv_k);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[j][e] = __fmaf_rn(-k2, xh[j][e], __fmaf_rn(rs, g[j][e], -k1));
+      store_chunk<OT>(dX + m * K * kBytes<OT>, c[j], n[j], g[j]);
+    }
+  }
+  if (!dw_out && !db_out) return;
+  // add the upper half of the teams to the lower half until one is left
+  auto combine = [&](float (&v)[NC][8]) {
+    for (int left = T; left > 1;) {
+      const int half = (left + 1) / 2;
+      __syncthreads();
+      if (team >= half && team < left) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) lds[place(team - half, j, e >> 2) + (e & 3)] = v[j][e];
+      }
+      __syncthreads();
+      if (team < left - half) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[j][e] += lds[place(team, j, e >> 2) + (e & 3)];
+      }
+      left = half;
+    }
+  };
+  auto finish = [&](float (&v)[NC][8], float* out) {
+    if (!out) return;
+    combine(v);
+    if (team == 0) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        store_chunk<kF32>(reinterpret_cast<char*>(out + blockIdx.x * out_stride), c[j], n[j], v[j]);
+    }
+  };
+  finish(dw, dw_out);
+  finish(db, db_out);
+}
+
+// dx of long rows: one workgroup per row, rows gridDim.x apart; the row is read for the two
 // sums and again for the output.
 template <int XT, int DT, int OT>
 __global__ __launch_bounds__(256) void ln_dx_rows_kernel(
@@ -26,11 +173,11 @@ __global__ __launch_bounds__(256) void ln_dx_rows_kernel(
     const char* drow = dY + m * K * kBytes<DT>;
     const float mean = mean_in[m], rstd = rstd_in[m];
     auto chunk = [&](int c, int n, float (&g)[8], float (&xh)[8]) {
-      chunk_f32<XT>(load_chunk<XT>(row, x_scales + m * G, c, n), xh);
-      chunk_f32<DT>(load_chunk<DT>(drow, nullptr, c, n), g);
+      chunk_f32<XT>(load_chunk<XT>(row, x_scales + m * G, K, c, n), xh);
+      chunk_f32<DT>(load_chunk<DT>(drow, nullptr, K, c, n), g);
       if (weight) {
         float w[8];
-        chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, c, n), w);
+        chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, K, c, n), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] *= w[e];
       }
@@ -75,8 +222,8 @@ __global__ __launch_bounds__(256) void ln_param_cols_kernel(
   float dw[8] = {}, db[8] = {};
   for (int64_t m = blockIdx.y * 8 + r; m < M; m += int64_t(gridDim.y) * 8) {
     float xh[8], d[8];
-    chunk_f32<XT>(load_chunk<XT>(X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>), x_scales + m * G, c, n), xh);
-    chunk_f32<DT>(load_chunk<DT>(dY + m * K * kBytes<DT>, nullptr, c, n), d);
+    chunk_f32<XT>(load_chunk<XT>(X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>), x_scales + m * G, K, c, n), xh);
+    chunk_f32<DT>(load_chunk<DT>(dY + m * K * kBytes<DT>, nullptr, K, c, n), d);
     const float mean = mean_in[m], rstd = rstd_in[m];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -101,16 +248,27 @@ __global__ __launch_bounds__(256) void ln_param_cols_kernel(
   }
 }
 
-// dw[k] = sum over the slabs of partial[slab][0][k], db likewise from [1].
-__global__ __launch_bounds__(256) void ln_param_sum_kernel(const float* __restrict__ partial, int slabs, int K,
-                                                           float* __restrict__ dw, float* __restrict__ db) {
-  const int k = blockIdx.x * 256 + threadIdx.x;
+// dw[k] = sum over the partial rows of partial[row][0][k], db likewise from
+// [1]: 64 columns to a workgroup, 16 rows at a time, then the 16 sums in order.
+__global__ __launch_bounds__(1024) void ln_param_sum_kernel(const float* __restrict__ partial, int rows, int K,
+                                                            float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float sums[16][64];
   float* out = blockIdx.y ? db : dw;
-  if (k >= K || !out) return;
-  const float* p = partial + static_cast<int64_t>(blockIdx.y) * K + k;
+  if (!out) return;
+  const int kl = threadIdx.x & 63, r = threadIdx.x >> 6;
+  const int k = blockIdx.x * 64 + kl;
+  const float* p = partial + static_cast<int64_t>(blockIdx.y) * K + min(k, K - 1);
   float t = 0.0f;
-  for (int s = 0; s < slabs; ++s) t += p[static_cast<int64_t>(s) * 2 * K];
-  out[k] = t;
+#pragma unroll 8
+  for (int s = r; s < rows; s += 16) t += p[static_cast<int64_t>(s) * 2 * K];
+  sums[r][kl] = t;
+  __syncthreads();
+  if (r == 0 && k < K) {
+    t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += sums[i][kl];
+    out[k] = t;
+  }
 }
 
 struct Args {
@@ -124,34 +282,51 @@ struct Args {
   float* partial;
 };
 
-template <int XT, int DT>
-hipError_t launch(const Args& a, int dx_dtype, hipStream_t stream) {
+template <int XT, int DT, int OT, int W, int NC, int THREADS = 1024>
+void launch_one(const Args& a, const LnBwdPlan& p, hipStream_t stream) {
+  const int64_t K = a.K;
+  const bool only = p.groups == 1;  // its sums are the gradients
+  ln_backward_kernel<XT, DT, OT, W, NC, THREADS><<<p.groups, 64 * W * p.teams, 0, stream>>>(
+      static_cast<const char*>(a.dY), static_cast<const char*>(a.X.p), a.X.scales, a.mean, a.rstd, a.M,
+      static_cast<int>(K), static_cast<int>(padded_k(K) / 8), a.weight, static_cast<char*>(a.dX),
+      !a.dweight ? nullptr : only ? a.dweight : a.partial, !a.dbias ? nullptr : only ? a.dbias : a.partial + K, 2 * K);
+}
+
+template <int XT, int DT, int OT>
+hipError_t launch(const Args& a, hipStream_t stream) {
   const int cpr = static_cast<int>(padded_k(a.K) / 8), K = static_cast<int>(a.K);
-  const char* dY = static_cast<const char*>(a.dY);
-  const char* X = static_cast<const char*>(a.X.p);
-  if (a.dX) {
-    const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
-    if (dx_dtype == kF32)
-      ln_dx_rows_kernel<XT, DT, kF32><<<blocks, 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr,
-                                                                 a.weight, static_cast<char*>(a.dX));
-    else
-      ln_dx_rows_kernel<XT, DT, kBf16><<<blocks, 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr,
-                                                                  a.weight, static_cast<char*>(a.dX));
+  const LnBwdPlan p = ln_bwd_plan(a.M, a.K, a.dweight || a.dbias);
+  if (p.waves == 0) {  // long rows
+    const char* dY = static_cast<const char*>(a.dY);
+    const char* X = static_cast<const char*>(a.X.p);
+    if (a.dX) {
+      const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
+      ln_dx_rows_kernel<XT, DT, OT><<<blocks, 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr,
+                                                               a.weight, static_cast<char*>(a.dX));
+    }
+    if (a.dweight || a.dbias)
+      ln_param_cols_kernel<XT, DT><<<dim3((cpr + 31) / 32, p.groups), 256, 0, stream>>>(
+          dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr, a.partial);
+  } else if (p.chunks == 1) {
+    if (p.waves == 1) launch_one<XT, DT, OT, 1, 1>(a, p, stream);
+    else if (p.waves == 2) launch_one<XT, DT, OT, 2, 1>(a, p, stream);
+    else if (p.waves == 4) launch_one<XT, DT, OT, 4, 1>(a, p, stream);
+    else if (p.waves == 8) launch_one<XT, DT, OT, 8, 1>(a, p, stream);
+    else launch_one<XT, DT, OT, 16, 1>(a, p, stream);
+  } else {
+    if (p.chunks == 3) launch_one<XT, DT, OT, 8, 3, 512>(a, p, stream);
+    else launch_one<XT, DT, OT, 8, 4, 512>(a, p, stream);
   }
-  if (a.dweight || a.dbias) {
-    const int slabs = static_cast<int>(ln_param_slabs(a.M, a.K));
-    ln_param_cols_kernel<XT, DT><<<dim3((cpr + 31) / 32, slabs), 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd,
-                                                                                  a.M, K, cpr, a.partial);
-    ln_param_sum_kernel<<<dim3((K + 255) / 256, 2), 256, 0, stream>>>(a.partial, slabs, K, a.dweight, a.dbias);
-  }
+  if ((a.dweight || a.dbias) && (p.groups > 1 || p.waves == 0))
+    ln_param_sum_kernel<<<dim3((K + 63) / 64, 2), 1024, 0, stream>>>(a.partial, p.groups, K, a.dweight, a.dbias);
   return hipGetLastError();
 }
 
-template <int DT>
-hipError_t launch_from(const Args& a, int dx_dtype, hipStream_t s) {
-  if (a.X.dtype == kF32) return launch<kF32, DT>(a, dx_dtype, s);
-  if (a.X.dtype == kBf16) return launch<kBf16, DT>(a, dx_dtype, s);
-  return launch<kSaved8, DT>(a, dx_dtype, s);
+template <int DT, int OT>
+hipError_t launch_from(const Args& a, hipStream_t s) {
+  if (a.X.dtype == kF32) return launch<kF32, DT, OT>(a, s);
+  if (a.X.dtype == kBf16) return launch<kBf16, DT, OT>(a, s);
+  return launch<kSaved8, DT, OT>(a, s);
 }
 
 }  // namespace
@@ -160,7 +335,10 @@ hipError_t launch_layer_norm_backward(const void* dY, int dy_dtype, BlockIn X, c
                                       int64_t M, int64_t K, const float* weight, void* dX, int dx_dtype,
                                       float* dweight, float* dbias, void* workspace, hipStream_t stream) {
   const Args a = {dY, X, mean, rstd, M, K, weight, dX, dweight, dbias, static_cast<float*>(workspace)};
-  return dy_dtype == kF32 ? launch_from<kF32>(a, dx_dtype, stream) : launch_from<kBf16>(a, dx_dtype, stream);
+  if (!dX) dx_dtype = kF32;  // not written
+  if (dy_dtype == kF32)
+    return dx_dtype == kF32 ? launch_from<kF32, kF32>(a, stream) : launch_from<kF32, kBf16>(a, stream);
+  return dx_dtype == kF32 ? launch_from<kBf16, kF32>(a, stream) : launch_from<kBf16, kBf16>(a, stream);
 }
 
 }  // namespace bitlinear

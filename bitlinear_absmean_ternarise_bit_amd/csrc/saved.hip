@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in,
     const int c = static_cast<int>(i - m * cpr);
     const int n = chunk_values(K, c);
     float v[8];
-    chunk_f32<IT>(load_chunk<IT>(in + (IT == kSaved8 ? m * Kp : m * K * kBytes<IT>), in_scales + m * G, c, n), v);
+    chunk_f32<IT>(load_chunk<IT>(in + (IT == kSaved8 ? m * Kp : m * K * kBytes<IT>), in_scales + m * G, K, c, n), v);
     if constexpr (SAVE) save_chunk(v, codes + m * Kp, scales + m * G, c);
     if constexpr (OP == kRelu2) {
 #pragma unroll
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in,
       }
     } else if constexpr (OP == kRelu2Backward) {
       float d[8];
-      chunk_f32<DT>(load_chunk<DT>(dA + m * K * kBytes<DT>, nullptr, c, n), d);
+      chunk_f32<DT>(load_chunk<DT>(dA + m * K * kBytes<DT>, nullptr, K, c, n), d);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(d[e], 2.0f * relu(v[e]));
     }
