@@ -196,10 +196,15 @@ __device__ __forceinline__ void save_chunk(const float (&v)[8], int8_t* codes, f
   const bool live = finite && amax >= 0x1p-100f;
   const float s = live ? __fdiv_rn(127.0f, amax) : 0.0f;
   const float scale = live ? __fmul_rn(amax, 1.0f / 127.0f) : finite ? 0.0f : __uint_as_float(0x7fc00000u);
-  v2u w = {0u, 0u};
+  v2u w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i >> 2] |= (__float_as_uint(__fmaf_rn(v[i], s, 12582912.0f)) & 0xffu) << (8 * (i & 3));
+  for (int h = 0; h < 2; ++h) {
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(__fmaf_rn(v[4 * h + i], s, 12582912.0f));
+    // low bytes of q[0], q[1] and q[2], q[3]; selector 12 gives a zero byte
+    w[h] = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400u) | __builtin_amdgcn_perm(q[3], q[2], 0x04000c0cu);
+  }
   if (!finite) w = v2u{0u, 0u};
   *reinterpret_cast<v2u*>(codes + 8 * c) = w;
   if ((c & 7) == 0) scales[c >> 3] = scale;

@@ -1,14 +1,118 @@
 // Layer norm's forward pass (include/bitlinear_block.h):
 //   mean = sum x / K, var = sum (x - mean)^2 / K, rstd = 1 / sqrt(var + eps)
 //   y = (x - mean) rstd w + b
-// in float32, with the row's 8-bit copy written from the same read.
+// in float32, with the row's 8-bit copy written from the same read.  Bound by
+// the bytes of x and y (and the copy): layer_norm_kernel reads a row once and
+// keeps it in registers; rows over kLnMaxChunks chunks take the kernel below it,
+// which reads them three times.
 #include "block_device.hpp"
 
 namespace bitlinear {
 
 namespace {
 
-// One workgroup per row, rows gridDim.x apart; the row is read from memory
+constexpr int kLnMaxChunks = 4096;  // K <= 32768
+
+// Waves that a SIMD holds at once: 64 or 128 registers to a lane.  As many
+// waves as the row needs with one chunk to a lane and all eight resident beat
+// half the waves with two chunks and six resident (8192 rows of 1024 to 8192,
+// bfloat16: equal to 4% slower; float32 with the 8-bit copy, where the two
+// chunks spill: 23% to 67% slower).
+template <int NC>
+constexpr int kLnWavesPerSimd = NC == 1 ? 8 : 4;
+
+// A team of W waves holds a row, NC chunks of 8 columns to a lane, between the
+// mean, the variance and the output.  W > 1: a team is a workgroup; W = 1: four
+// teams to a workgroup, without barriers.  Rows are gridDim.x T apart, about as
+// many teams as the card holds at once; each loads its next row before it works
+// on the current one, and keeps weight and bias in registers (NC <= 2), so that
+// nothing but that load is waited for.
+template <int XT, int YT, bool SAVE, int W, int NC>
+__global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void layer_norm_kernel(
+    const char* __restrict__ X, const float* __restrict__ x_scales, int64_t M, int K, int cpr,
+    const float* __restrict__ weight, const float* __restrict__ bias, float eps, char* __restrict__ Y,
+    float* __restrict__ mean_out, float* __restrict__ rstd_out, int8_t* __restrict__ codes,
+    float* __restrict__ scales) {
+  constexpr bool kHoldWeights = NC <= 2;
+  constexpr int T = W > 1 ? 1 : 4;
+  __shared__ float slots[2][W];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int team = W > 1 ? 0 : wave, wt = W > 1 ? wave : 0;
+  const int64_t G = cpr >> 3, Kp = int64_t(cpr) * 8;
+  const float inv_k = 1.0f / static_cast<float>(K);
+  int c[NC], n[NC];
+  float w[kHoldWeights ? NC : 1][8], b[kHoldWeights ? NC : 1][8];
+  auto load_weights = [&](int j, float (&wj)[8], float (&bj)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wj[e] = 1.0f, bj[e] = 0.0f;
+    if (weight) chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, K, c[j], n[j]), wj);
+    if (bias) chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(bias), nullptr, K, c[j], n[j]), bj);
+  };
+  Raw<XT> r[NC];
+  auto load_row = [&](int64_t m) {
+    const char* row = X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) r[j] = load_chunk<XT>(row, x_scales + m * G, K, c[j], n[j]);
+  };
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    c[j] = wt * 64 + lane + j * 64 * W;
+    n[j] = c[j] < cpr ? chunk_values(K, c[j]) : 0;
+  }
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * T;
+  int64_t m = static_cast<int64_t>(blockIdx.x) * T + team;
+  if (m >= M) return;  // W = 1 only: a grid has no more workgroups than rows
+  load_row(m);
+  if constexpr (kHoldWeights) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) load_weights(j, w[j], b[j]);
+  }
+  for (; m < M; m += stride) {
+    float v[NC][8], sum[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NC; ++j) chunk_f32<XT>(r[j], v[j]);
+    if (m + stride < M) load_row(m + stride);
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[0] += v[j][e];
+    team_sum<W>(sum, slots[0], wt, lane);
+    const float mean = sum[0] * inv_k;
+    if constexpr (SAVE) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        if (c[j] < cpr) save_chunk(v[j], codes + m * Kp, scales + m * G, c[j]);
+    }
+    float sq[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] -= mean;
+      if (n[j] < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = e < n[j] ? v[j][e] : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq[0] = __fmaf_rn(v[j][e], v[j][e], sq[0]);
+    }
+    team_sum<W>(sq, slots[1], wt, lane);
+    const float rstd = 1.0f / sqrtf(sq[0] * inv_k + eps);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int held = kHoldWeights ? j : 0;
+      if constexpr (!kHoldWeights) load_weights(j, w[0], b[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] = __fmaf_rn(v[j][e] * rstd, w[held][e], b[held][e]);
+      store_chunk<YT>(Y + m * K * kBytes<YT>, c[j], n[j], v[j]);
+    }
+    if (mean_out && wt == 0 && lane == 0) {
+      mean_out[m] = mean;
+      rstd_out[m] = rstd;
+    }
+  }
+}
+
+// Long rows: one workgroup per row, rows gridDim.x apart; the row is read from memory
 // (the caches after the first time) for the mean, the variance and the output.
 template <int XT, int YT, bool SAVE>
 __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
@@ -76,13 +180,40 @@ struct Args {
   float* saved_scales;
 };
 
+template <int XT, int YT, bool SAVE, int W, int NC>
+void launch_held(const Args& a, hipStream_t stream) {
+  constexpr int64_t T = W > 1 ? 1 : 4;  // rows at a time of a workgroup
+  constexpr int64_t most = 256 * (4 * kLnWavesPerSimd<NC> / (W > 1 ? W : 4));  // workgroups that 256 CUs hold
+  const int64_t wgs = (a.M + T - 1) / T, turns = (wgs + most - 1) / most;
+  const int64_t blocks = (wgs + turns - 1) / turns;  // as many turns for each
+  layer_norm_kernel<XT, YT, SAVE, W, NC><<<static_cast<unsigned>(blocks), W > 1 ? 64 * W : 256, 0, stream>>>(
+      static_cast<const char*>(a.X.p), a.X.scales, a.M, static_cast<int>(a.K), static_cast<int>(padded_k(a.K) / 8),
+      a.weight, a.bias, a.eps, static_cast<char*>(a.Y), a.mean, a.rstd, a.saved, a.saved_scales);
+}
+
 template <int XT, int YT, bool SAVE>
 hipError_t launch(const Args& a, hipStream_t stream) {
   const int cpr = static_cast<int>(padded_k(a.K) / 8);
-  const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
-  layer_norm_rows_kernel<XT, YT, SAVE><<<blocks, 256, 0, stream>>>(
-      static_cast<const char*>(a.X.p), a.X.scales, a.M, static_cast<int>(a.K), cpr, a.weight, a.bias, a.eps,
-      static_cast<char*>(a.Y), a.mean, a.rstd, a.saved, a.saved_scales);
+  if (cpr <= 64) {
+    launch_held<XT, YT, SAVE, 1, 1>(a, stream);
+  } else if (cpr <= 128) {
+    launch_held<XT, YT, SAVE, 2, 1>(a, stream);
+  } else if (cpr <= 256) {
+    launch_held<XT, YT, SAVE, 4, 1>(a, stream);
+  } else if (cpr <= 512) {
+    launch_held<XT, YT, SAVE, 8, 1>(a, stream);
+  } else if (cpr <= 1024) {
+    launch_held<XT, YT, SAVE, 16, 1>(a, stream);
+  } else if (cpr <= 2048) {
+    launch_held<XT, YT, SAVE, 16, 2>(a, stream);
+  } else if (cpr <= kLnMaxChunks) {
+    launch_held<XT, YT, SAVE, 16, 4>(a, stream);
+  } else {
+    const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
+    layer_norm_rows_kernel<XT, YT, SAVE><<<blocks, 256, 0, stream>>>(
+        static_cast<const char*>(a.X.p), a.X.scales, a.M, static_cast<int>(a.K), cpr, a.weight, a.bias, a.eps,
+        static_cast<char*>(a.Y), a.mean, a.rstd, a.saved, a.saved_scales);
+  }
   return hipGetLastError();
 }
 
