@@ -493,37 +493,70 @@ def backward(dY, packedT, gamma, Xq, gamma_a, mask, K: int, need_dx: bool = True
 # Activations saved in 8 bits are a pair (codes int8 [M, padded_k(K)], scales
 # float32 [M, padded_k(K) / 64]).  Every tensor of a call lies on one GPU, which
 # need not be the current one; the work goes to that GPU's current stream.
+#
+# The calls of a decode step last about as long as this file's own work for
+# them, so it is kept short: addresses go to ctypes as they are, what is looked
+# up once is kept, and arrays shaped like another are made like it.
 
-_PLAIN = {}  # torch dtype -> abi dtype
+_BLOCK = None
+
+
+class _BlockCalls:
+    """What every call below needs, looked up once: torch, its dtypes and the C functions."""
+
+    def __init__(self):
+        torch = _torch()
+        lib = abi.load()
+        self.torch, self.f32, self.i8 = torch, torch.float32, torch.int8
+        self.plain = {torch.float32: abi.F32, torch.bfloat16: abi.BF16}
+        self.device_now = torch.cuda.current_device
+        # the stream's address without a Stream object, where torch has that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream_of = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        for name in abi.BLOCK_SIGNATURES:
+            setattr(self, name[len("bitlinear_"):], getattr(lib, name))
+
+    def launch(self, name, device, *args):
+        """Calls a C function on `device`'s current stream, with that device current."""
+        fn, index = getattr(self, name), device.index
+        if index == self.device_now():
+            status = fn(*args, self.stream_of(index))
+        else:
+            with self.torch.cuda.device(index):
+                status = fn(*args, self.stream_of(index))
+        if status:
+            abi.check("bitlinear_" + name, status)
+
+
+def _block():
+    global _BLOCK
+    if _BLOCK is None:
+        _BLOCK = _BlockCalls()
+    return _BLOCK
 
 
 def _plain_dtype(dtype, name):
-    if not _PLAIN:
-        torch = _torch()
-        _PLAIN.update({torch.float32: abi.F32, torch.bfloat16: abi.BF16})
-    d = _PLAIN.get(dtype)
+    d = _block().plain.get(dtype)
     if d is None:
         raise ValueError(f"{name} must be float32 or bfloat16")
     return d
 
 
-def _matrix(t, name, shape=None):
-    """Checks a contiguous GPU [M, K] tensor; its abi dtype."""
+def _matrix(t, name):
+    """Checks a contiguous GPU [M, K] tensor; its abi dtype, M and K."""
     _require_cuda(t, name)
     if t.dim() != 2 or t.numel() == 0:
         raise ValueError(f"{name} must be [M, K] with at least one value")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    return _plain_dtype(t.dtype, name)
+    M, K = t.shape
+    return _plain_dtype(t.dtype, name), M, K
 
 
 def _vector(t, n, device, name):
-    """The address of a float32 [n] tensor on `device` (None: 0)."""
+    """The address of a float32 tensor of n values on `device` (None: 0)."""
     if t is None:
         return 0
-    torch = _torch()
     _require_cuda(t, name)
-    if t.dtype != torch.float32 or t.numel() != n:
+    if t.dtype != _block().f32 or t.numel() != n:
         raise ValueError(f"{name} must hold {n} float32 values")
     if t.device != device:
         raise ValueError(f"{name} is on another device")
@@ -533,22 +566,21 @@ def _vector(t, n, device, name):
 def _whole_or_saved(x, K, name, M=None):
     """(data address, scales address, abi dtype, M, K, device) of a [M, K] tensor or a saved pair."""
     if not isinstance(x, (tuple, list)):
-        dt = _matrix(x, name)
-        m, k = x.shape
+        dt, m, k = _matrix(x, name)
         if (K is not None and k != K) or (M is not None and m != M):
             raise ValueError(f"{name} does not have the other arrays' shape")
         return x.data_ptr(), 0, dt, m, k, x.device
-    torch = _torch()
     codes, scales = x
     if K is None:
         raise ValueError(f"K is needed where {name} is saved in 8 bits")
     _require_cuda(codes, name + " codes")
     _require_cuda(scales, name + " scales")
+    B = _block()
     groups = (K + 63) // 64
     m = codes.shape[0]
-    if codes.dtype != torch.int8 or codes.dim() != 2 or K < 1 or m < 1 or codes.shape[1] != 64 * groups:
+    if codes.dtype != B.i8 or codes.dim() != 2 or K < 1 or m < 1 or codes.shape[1] != 64 * groups:
         raise ValueError(f"{name} codes must be int8 [M, padded_k(K)]")
-    if scales.dtype != torch.float32 or scales.shape != (m, groups):
+    if scales.dtype != B.f32 or scales.shape != (m, groups):
         raise ValueError(f"{name} scales must be float32 [M, padded_k(K) / 64]")
     if scales.device != codes.device:
         raise ValueError(f"{name} codes and scales are on different devices")
@@ -557,53 +589,43 @@ def _whole_or_saved(x, K, name, M=None):
     return codes.data_ptr(), scales.data_ptr(), abi.SAVED8, m, K, codes.device
 
 
-def _output(out, M, K, dtype, device, name="out"):
-    torch = _torch()
+def _output(out, M, K, dtype, device, like=None):
+    """`out`, checked, or a new [M, K] tensor (`like`: one of that shape on that device)."""
     if out is None:
-        return torch.empty((M, K), dtype=dtype, device=device)
-    _require_cuda(out, name)
+        if like is not None and like.dtype == dtype:
+            return _block().torch.empty_like(like)
+        return _block().torch.empty((M, K), dtype=dtype, device=device)
+    _require_cuda(out, "out")
     if out.shape != (M, K) or out.dtype != dtype or out.device != device:
-        raise ValueError(f"{name} must be {dtype} [{M}, {K}] on {device}")
+        raise ValueError(f"out must be {dtype} [{M}, {K}] on {device}")
     return out
 
 
 def _empty_saved(M, K, device):
-    torch = _torch()
+    B = _block()
     groups = (K + 63) // 64
-    return (torch.empty((M, 64 * groups), dtype=torch.int8, device=device),
-            torch.empty((M, groups), dtype=torch.float32, device=device))
-
-
-def _launch(name, device, *args):
-    """Calls a C function on `device`'s current stream, with that device current."""
-    torch = _torch()
-    fn = getattr(abi.load(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, stream)
-    abi.check(name, status)
+    return (B.torch.empty((M, 64 * groups), dtype=B.i8, device=device),
+            B.torch.empty((M, groups), dtype=B.f32, device=device))
 
 
 def save_activations(X):
     """X (float32 or bfloat16 [M, K]) in 8 bits: the pair (codes, scales)."""
-    dt = _matrix(X, "X")
-    M, K = X.shape
-    saved = _empty_saved(M, K, X.device)
-    _launch("bitlinear_save_activations", X.device, X.data_ptr(), dt, M, K, saved[0].data_ptr(),
-            saved[1].data_ptr())
+    dt, M, K = _matrix(X, "X")
+    device = X.device
+    codes, scales = saved = _empty_saved(M, K, device)
+    _block().launch("save_activations", device, X.data_ptr(), dt, M, K, codes.data_ptr(), scales.data_ptr())
     return saved
 
 
 def restore_activations(saved, K: int, dtype=None, out=None):
     """The [M, K] values that ``saved`` stands for, as float32 (default) or bfloat16."""
+    B = _block()
     codes, scales, _, M, K, device = _whole_or_saved(tuple(saved), K, "saved")
-    dtype = _torch().float32 if dtype is None else dtype
+    if dtype is None:
+        dtype = B.f32 if out is None else out.dtype
     dt = _plain_dtype(dtype, "dtype")
     X = _output(out, M, K, dtype, device)
-    _launch("bitlinear_restore_activations", device, codes, scales, M, K, X.data_ptr(), dt)
+    B.launch("restore_activations", device, codes, scales, M, K, X.data_ptr(), dt)
     return X
 
 
@@ -615,25 +637,29 @@ def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, K: int | None = Non
     pair).  Returns Y; (Y, mean, rstd) with ``return_stats``, for :func:`layer_norm_backward`; and
     (Y, mean, rstd, saved) with ``save``, X in 8 bits from the same pass.
     """
-    torch = _torch()
+    B = _block()
     x, xs, dt, M, K, device = _whole_or_saved(X, K, "X")
+    like = None if xs else X
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.float32 if dt == abi.SAVED8 else X.dtype
+        out_dtype = out.dtype if out is not None else B.f32 if xs else X.dtype
     ydt = _plain_dtype(out_dtype, "out_dtype")
     w, b = _vector(weight, K, device, "weight"), _vector(bias, K, device, "bias")
-    if save and dt == abi.SAVED8:
+    if save and xs:
         raise ValueError("X is saved already")
-    Y = _output(out, M, K, out_dtype, device)
-    mean = rstd = saved = None
-    mp = rp = cp = sp = 0
-    if return_stats or save:
-        mean, rstd = (torch.empty((M,), dtype=torch.float32, device=device) for _ in range(2))
-        mp, rp = mean.data_ptr(), rstd.data_ptr()
-    if save:
-        saved = _empty_saved(M, K, device)
-        cp, sp = saved[0].data_ptr(), saved[1].data_ptr()
-    _launch("bitlinear_layer_norm", device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mp, rp, cp, sp)
-    return (Y, mean, rstd, saved) if save else (Y, mean, rstd) if return_stats else Y
+    Y = _output(out, M, K, out_dtype, device, like)
+    if not (return_stats or save):
+        B.launch("layer_norm", device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, 0, 0, 0, 0)
+        return Y
+    mean = B.torch.empty(M, dtype=B.f32, device=device)
+    rstd = B.torch.empty_like(mean)
+    if not save:
+        B.launch("layer_norm", device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mean.data_ptr(),
+                 rstd.data_ptr(), 0, 0)
+        return Y, mean, rstd
+    codes, scales = saved = _empty_saved(M, K, device)
+    B.launch("layer_norm", device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mean.data_ptr(),
+             rstd.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return Y, mean, rstd, saved
 
 
 def layer_norm_backward(dY, X, mean, rstd, weight=None, out_dtype=None, need_dx: bool = True,
@@ -643,9 +669,8 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, out_dtype=None, need_dx:
     ``X``: the forward's input, whole or as it was saved; ``mean``, ``rstd``: from the forward.  dX [M, K]
     is of ``out_dtype`` (default: dY's), dweight and dbias are float32 [K]; None where not needed.
     """
-    torch = _torch()
-    ddt = _matrix(dY, "dY")
-    M, K = dY.shape
+    B = _block()
+    ddt, M, K = _matrix(dY, "dY")
     device = dY.device
     x, xs, dt, _, _, xdev = _whole_or_saved(X, K, "X", M)
     if xdev != device:
@@ -656,27 +681,30 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, out_dtype=None, need_dx:
     w = _vector(weight, K, device, "weight")
     if not (need_dx or need_dw):
         raise ValueError("nothing to compute")
-    out_dtype = dY.dtype if out_dtype is None else out_dtype
+    if out_dtype is None:
+        out_dtype = dY.dtype
     odt = _plain_dtype(out_dtype, "out_dtype")
     dX = dw = db = None
     dxp = dwp = dbp = wsp = ws_bytes = 0
     if need_dx:
-        dX = torch.empty((M, K), dtype=out_dtype, device=device)
+        dX = _output(None, M, K, out_dtype, device, dY)
         dxp = dX.data_ptr()
     if need_dw:
-        dw, db = (torch.empty((K,), dtype=torch.float32, device=device) for _ in range(2))
+        dw = B.torch.empty(K, dtype=B.f32, device=device)
+        db = B.torch.empty_like(dw)
         dwp, dbp = dw.data_ptr(), db.data_ptr()
         if workspace is None:
-            ws_bytes = abi.load().bitlinear_layer_norm_backward_workspace_bytes(M, K)
-            workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=device)
+            ws_bytes = B.layer_norm_backward_workspace_bytes(M, K)
+            if ws_bytes:
+                workspace = B.torch.empty(ws_bytes, dtype=B.i8, device=device)
+                wsp = workspace.data_ptr()
         else:
             _require_cuda(workspace, "workspace")
             if workspace.device != device:
                 raise ValueError("workspace is on another device")
-            ws_bytes = workspace.numel() * workspace.element_size()
-        wsp = workspace.data_ptr()
-    _launch("bitlinear_layer_norm_backward", device, dY.data_ptr(), ddt, x, xs, dt, mp, rp, M, K, w, dxp, odt,
-            dwp, dbp, wsp, ws_bytes)
+            wsp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    B.launch("layer_norm_backward", device, dY.data_ptr(), ddt, x, xs, dt, mp, rp, M, K, w, dxp, odt, dwp, dbp,
+             wsp, ws_bytes)
     return dX, dw, db
 
 
@@ -686,20 +714,20 @@ def relu2(H, K: int | None = None, out_dtype=None, save: bool = False, out=None)
     A is of ``out_dtype`` (default: H's; float32 for a saved pair).  With ``save`` returns (A, saved), H in
     8 bits from the same pass.
     """
-    torch = _torch()
+    B = _block()
     h, hs, dt, M, K, device = _whole_or_saved(H, K, "H")
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.float32 if dt == abi.SAVED8 else H.dtype
+        out_dtype = out.dtype if out is not None else B.f32 if hs else H.dtype
     adt = _plain_dtype(out_dtype, "out_dtype")
-    if save and dt == abi.SAVED8:
+    if save and hs:
         raise ValueError("H is saved already")
-    A = _output(out, M, K, out_dtype, device)
-    saved, cp, sp = None, 0, 0
-    if save:
-        saved = _empty_saved(M, K, device)
-        cp, sp = saved[0].data_ptr(), saved[1].data_ptr()
-    _launch("bitlinear_relu2", device, h, hs, dt, M, K, A.data_ptr(), adt, cp, sp)
-    return (A, saved) if save else A
+    A = _output(out, M, K, out_dtype, device, None if hs else H)
+    if not save:
+        B.launch("relu2", device, h, hs, dt, M, K, A.data_ptr(), adt, 0, 0)
+        return A
+    codes, scales = saved = _empty_saved(M, K, device)
+    B.launch("relu2", device, h, hs, dt, M, K, A.data_ptr(), adt, codes.data_ptr(), scales.data_ptr())
+    return A, saved
 
 
 def relu2_backward(dA, H, out_dtype=None, out=None):
@@ -707,14 +735,14 @@ def relu2_backward(dA, H, out_dtype=None, out=None):
 
     dH is of ``out_dtype`` (default: dA's; bfloat16 is what :func:`backward` takes).
     """
-    adt = _matrix(dA, "dA")
-    M, K = dA.shape
+    adt, M, K = _matrix(dA, "dA")
+    device = dA.device
     h, hs, dt, _, _, hdev = _whole_or_saved(H, K, "H", M)
-    if hdev != dA.device:
+    if hdev != device:
         raise ValueError("H is on another device")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else dA.dtype
     odt = _plain_dtype(out_dtype, "out_dtype")
-    dH = _output(out, M, K, out_dtype, dA.device)
-    _launch("bitlinear_relu2_backward", dA.device, dA.data_ptr(), adt, h, hs, dt, M, K, dH.data_ptr(), odt)
+    dH = _output(out, M, K, out_dtype, device, dA)
+    _block().launch("relu2_backward", device, dA.data_ptr(), adt, h, hs, dt, M, K, dH.data_ptr(), odt)
     return dH
