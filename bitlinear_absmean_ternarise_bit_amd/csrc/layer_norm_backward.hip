@@ -5,8 +5,9 @@
 // in float32, from x as it was or from its 8-bit copy.  Bound by the bytes of
 // x, dy and dx: ln_backward_kernel reads each row once and keeps it in
 // registers between the row's sums and its dx, with the columns' dw and db in
-// registers across all of a workgroup's rows.  Rows over kLnBwdMaxChunks chunks
-// take the two kernels below it, which read the rows twice each.
+// registers across all of a workgroup's rows.  For rows over kLnBwdMaxChunks
+// chunks it gives dx alone, and a column kernel reads x and dy again for dw and
+// db; over kLnDxMaxChunks dx comes from a kernel that reads each row twice.
 #include "block_device.hpp"
 
 namespace bitlinear {
@@ -27,7 +28,9 @@ namespace {
 // columns are 7 TB/s at float32 dy and bfloat16 dx.  So dx is two FMAs,
 //   dx = rstd g - rstd c1 - xhat (rstd c2),   c1, c2 the sums over K,
 // and a value is converted once.
-template <int XT, int DT, int OT, int W, int NC, int THREADS>
+//
+// PARAMS false: dx alone, for rows whose dw and db do not fit beside them.
+template <int XT, int DT, int OT, int W, int NC, int THREADS, bool PARAMS>
 __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
     const char* __restrict__ dY, const char* __restrict__ X, const float* __restrict__ x_scales,
     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t M, int K, int cpr,
@@ -47,7 +50,7 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
   // wave's 16-byte accesses are consecutive
   auto place = [&](int t, int j, int half) { return t * kTeamFloats + ((j * 2 + half) * 64 * W + wt * 64 + lane) * 4; };
   int c[NC], n[NC];
-  float dw[NC][8], db[NC][8], held_w[8];
+  float dw[PARAMS ? NC : 1][8], db[PARAMS ? NC : 1][8], held_w[8];
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     c[j] = wt * 64 + lane + j * 64 * W;
@@ -61,7 +64,7 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      dw[j][e] = db[j][e] = 0.0f;
+      if constexpr (PARAMS) dw[j][e] = db[j][e] = 0.0f;
       if constexpr (kWeightInLds) lds[place(0, j, e >> 2) + (e & 3)] = w[e];
       else held_w[e] = w[e];
     }
@@ -105,8 +108,10 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        db[j][e] += g[j][e];
-        dw[j][e] = __fmaf_rn(g[j][e], xh[j][e], dw[j][e]);
+        if constexpr (PARAMS) {
+          db[j][e] += g[j][e];
+          dw[j][e] = __fmaf_rn(g[j][e], xh[j][e], dw[j][e]);
+        }
         g[j][e] *= weight_of(j, e);
         s[0] += g[j][e];
         s[1] = __fmaf_rn(g[j][e], xh[j][e], s[1]);
@@ -121,9 +126,9 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
       store_chunk<OT>(dX + m * K * kBytes<OT>, c[j], n[j], g[j]);
     }
   }
-  if (!dw_out && !db_out) return;
+  if (!PARAMS || (!dw_out && !db_out)) return;
   // add the upper half of the teams to the lower half until one is left
-  auto combine = [&](float (&v)[NC][8]) {
+  auto combine = [&](auto& v) {
     for (int left = T; left > 1;) {
       const int half = (left + 1) / 2;
       __syncthreads();
@@ -143,7 +148,7 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
       left = half;
     }
   };
-  auto finish = [&](float (&v)[NC][8], float* out) {
+  auto finish = [&](auto& v, float* out) {
     if (!out) return;
     combine(v);
     if (team == 0) {
@@ -152,8 +157,10 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
         store_chunk<kF32>(reinterpret_cast<char*>(out + blockIdx.x * out_stride), c[j], n[j], v[j]);
     }
   };
-  finish(dw, dw_out);
-  finish(db, db_out);
+  if constexpr (PARAMS) {
+    finish(dw, dw_out);
+    finish(db, db_out);
+  }
 }
 
 // dx of long rows: one workgroup per row, rows gridDim.x apart; the row is read for the two
@@ -271,6 +278,8 @@ __global__ __launch_bounds__(1024) void ln_param_sum_kernel(const float* __restr
   }
 }
 
+constexpr int kLnDxMaxChunks = 7 * 512;  // K <= 28672: 8 waves hold a row for dx alone
+
 struct Args {
   const void* dY;
   BlockIn X;
@@ -282,11 +291,11 @@ struct Args {
   float* partial;
 };
 
-template <int XT, int DT, int OT, int W, int NC, int THREADS = 1024>
+template <int XT, int DT, int OT, int W, int NC, int THREADS = 1024, bool PARAMS = true>
 void launch_one(const Args& a, const LnBwdPlan& p, hipStream_t stream) {
   const int64_t K = a.K;
   const bool only = p.groups == 1;  // its sums are the gradients
-  ln_backward_kernel<XT, DT, OT, W, NC, THREADS><<<p.groups, 64 * W * p.teams, 0, stream>>>(
+  ln_backward_kernel<XT, DT, OT, W, NC, THREADS, PARAMS><<<p.groups, 64 * W * p.teams, 0, stream>>>(
       static_cast<const char*>(a.dY), static_cast<const char*>(a.X.p), a.X.scales, a.mean, a.rstd, a.M,
       static_cast<int>(K), static_cast<int>(padded_k(K) / 8), a.weight, static_cast<char*>(a.dX),
       !a.dweight ? nullptr : only ? a.dweight : a.partial, !a.dbias ? nullptr : only ? a.dbias : a.partial + K, 2 * K);
@@ -299,7 +308,10 @@ hipError_t launch(const Args& a, hipStream_t stream) {
   if (p.waves == 0) {  // long rows
     const char* dY = static_cast<const char*>(a.dY);
     const char* X = static_cast<const char*>(a.X.p);
-    if (a.dX) {
+    if (a.dX && cpr <= kLnDxMaxChunks) {
+      const LnBwdPlan dx = {8, 7, 1, static_cast<int>(a.M < 256 ? a.M : 256)};
+      launch_one<XT, DT, OT, 8, 7, 512, false>(a, dx, stream);
+    } else if (a.dX) {
       const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
       ln_dx_rows_kernel<XT, DT, OT><<<blocks, 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr,
                                                                a.weight, static_cast<char*>(a.dX));
