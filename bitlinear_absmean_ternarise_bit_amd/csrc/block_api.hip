@@ -155,14 +155,14 @@ int bitlinear_layer_norm_backward(const void* dY, int dy_dtype, const void* X, c
   if (!aligned_to(dY, dy_dtype) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(weight, 4) ||
       (dX && !aligned_to(dX, dx_dtype)) || !aligned(dweight, 4) || !aligned(dbias, 4))
     return BITLINEAR_ERR_ALIGN;
-  const bool params = dweight || dbias;
-  if (params) {
-    if (!workspace || workspace_bytes < ln_bwd_workspace_bytes(M, K)) return BITLINEAR_ERR_WORKSPACE;
+  const size_t need = dweight || dbias ? ln_bwd_workspace_bytes(M, K) : 0;
+  if (need) {
+    if (!workspace || workspace_bytes < need) return BITLINEAR_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return BITLINEAR_ERR_ALIGN;
   }
   const BlockIn x = block_in(X, x_scales, x_dtype);
   const Range out[] = {array(dX, dx_dtype, M, K), floats(dweight, K), floats(dbias, K),
-                       {params ? workspace : nullptr, ln_bwd_workspace_bytes(M, K)}};
+                       {need ? workspace : nullptr, need}};
   const Range in[] = {array(dY, dy_dtype, M, K), array(X, x_dtype, M, K), scale_range(x.scales, M, K),
                       floats(mean, M), floats(rstd, M), floats(weight, K)};
   if (any_overlap(out, in)) return BITLINEAR_ERR_ARG;

@@ -67,9 +67,13 @@ inline LnBwdPlan ln_bwd_plan(int64_t M, int64_t K, bool params) {
   return p;
 }
 
+// Partial rows of dweight and dbias; none where one workgroup writes the
+// gradients themselves.
 inline size_t ln_bwd_workspace_bytes(int64_t M, int64_t K) {
   if (!size_args_ok(M) || !size_args_ok(K)) return 0;
-  return align256(size_mul(size_t(ln_bwd_plan(M, K, true).groups), size_mul(size_t(K), 8)));
+  const LnBwdPlan p = ln_bwd_plan(M, K, true);
+  if (p.waves > 0 && p.groups == 1) return 0;
+  return align256(size_mul(size_t(p.groups), size_mul(size_t(K), 8)));
 }
 
 hipError_t launch_save(const void* X, int x_dtype, int64_t M, int64_t K, int8_t* codes, float* scales,

@@ -108,7 +108,7 @@ int bitlinear_layer_norm(const void* X, const float* x_scales, int x_dtype, int6
                          float* mean, float* rstd, int8_t* saved, float* saved_scales, void* stream);
 
 /* Workspace bytes of bitlinear_layer_norm_backward: partial sums of dweight
- * and dbias (at most 256 rows of 2 K float32). */
+ * and dbias (at most 256 rows of 2 K float32; 0 for few rows). */
 size_t bitlinear_layer_norm_backward_workspace_bytes(int64_t M, int64_t K);
 
 /*
@@ -127,7 +127,8 @@ size_t bitlinear_layer_norm_backward_workspace_bytes(int64_t M, int64_t K);
  * dweight, dbias: device float32 [K], each may be NULL (of dX, dweight and
  *         dbias at least one is given).
  * workspace: >= bitlinear_layer_norm_backward_workspace_bytes(M, K), 256-byte
- *         aligned, when dweight or dbias is given, else it may be NULL/0.
+ *         aligned; may be NULL/0 where that is 0, or without dweight and dbias.
+ *         Scratch only: two calls that may overlap need one each.
  *
  * Arithmetic in float32; the sums over m run over fixed sets of rows, one
  * after the other, and over the sets in a fixed order (no atomics).

@@ -54,8 +54,9 @@ def test_sizes(lib):
         assert lib.bitlinear_layer_norm_backward_workspace_bytes(bad, 64) == 0
         assert lib.bitlinear_layer_norm_backward_workspace_bytes(64, bad) == 0
     f = lib.bitlinear_layer_norm_backward_workspace_bytes
-    for M, K in ((1, 1), (1, 1 << 20), (3, 100), (2048, 4096), (1 << 31, 64), (100, 28672)):
+    for M, K in ((1, 1 << 20), (40, 100), (2048, 4096), (1 << 31, 64), (100, 28672), (3, 8192)):
         assert f(M, K) % 256 == 0 and 0 < f(M, K) <= 256 * 2 * 4 * K + 256
+    assert f(1, 1) == f(3, 100) == f(2, 8192) == 0  # one workgroup writes the gradients
 
 
 SHAPES = [(0, 8), (8, 0), (-1, 8), (8, -1), ((1 << 31) + 1, 1), (8, (1 << 20) + 1), (1 << 20, 1 << 20),
@@ -133,6 +134,8 @@ def test_layer_norm_backward_refusals(lib):
         assert call(**{nm: at(names.index(nm) + 20) + off}) == abi.ERR_ALIGN
     assert call(ws=None) == abi.ERR_WORKSPACE and call(wsb=need - 1) == abi.ERR_WORKSPACE
     assert call(ws=None, wsb=0, db=None) == abi.ERR_WORKSPACE
+    # a workspace that is not needed is not looked at
+    assert call(M=3, ws=None, wsb=0, dw=at(0)) == abi.ERR_ARG
     for nm in ("dX", "dw", "db", "ws"):
         for other in (at(0), at(1), at(2), at(3), at(4)):
             assert call(**{nm: other}) == abi.ERR_ARG

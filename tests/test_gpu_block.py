@@ -320,7 +320,7 @@ def test_odd_addresses_and_guards():
         t = torch.full((n + 64,), 77, dtype=dtype, device=DEV)
         return t, t[off:off + n]
 
-    for M, K, off in ((5, 67, 1), (3, 1003, 3), (4, 640, 5), (2, 4096, 7)):
+    for M, K, off in ((5, 67, 1), (90, 1003, 3), (4, 640, 5), (2, 4096, 7), (3, 20001, 3)):
         say(f"guards M={M} K={K} off={off}")
         Kp = bl.padded_k(K)
         X = values(rng, (M, K), "bf16")
@@ -475,8 +475,10 @@ def test_binding_refusals():
     with pytest.raises(bl.BitLinearError):
         bl.layer_norm(X, eps=-1.0)
     st = X[:, 0].contiguous()
+    Z = torch.zeros((400, 100), device=DEV)
+    st = Z[:, 0].contiguous()
     with pytest.raises(bl.BitLinearError):
-        bl.layer_norm_backward(X, X, st, st.clone(), workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+        bl.layer_norm_backward(Z, Z.clone(), st, st.clone(), workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
 
 
 # ---- together, as a block trains ------------------------------------------------------
