@@ -390,6 +390,53 @@ def test_offsets_past_32_bits():
     check_backward(np_of(dA[-40:]), xk, np_of(m), np_of(r), None, None, np_of(dw), np_of(db), "f32")
 
 
+def test_more_rows_than_one_launch_takes():
+    """2^28 rows of 8 chunks are one launch of the element-wise kernels; the rows behind it are the next."""
+    M = (1 << 28) + 1000
+    say(f"rows M={M} K=1")
+    g = torch.Generator(device=DEV).manual_seed(2)
+    tail = torch.randn((2000, 1), generator=g, device=DEV).to(torch.bfloat16)
+    X = torch.zeros((M, 1), dtype=torch.bfloat16, device=DEV)
+    X[-2000:] = tail
+    A, saved = bl.relu2(X, save=True)
+    a, s = bl.relu2(tail, save=True)
+    assert torch.equal(A[-2000:], a) and not bool(A[:-2000].any())
+    assert torch.equal(saved[0][-2000:], s[0]) and torch.equal(saved[1][-2000:], s[1])
+    assert not bool(saved[1][:-2000].any())
+    back = bl.restore_activations(saved, 1, torch.bfloat16)
+    assert torch.equal(back[-2000:], bl.restore_activations(s, 1, torch.bfloat16)) and not bool(back[:-2000].any())
+    del A, saved, back
+    # every row is one value: its norm is the bias, its mean the value, and dbias is the sum of dY
+    bias = torch.full((1,), 0.5, device=DEV)
+    Y, mean, rstd = bl.layer_norm(X, None, bias, return_stats=True)
+    assert bool((Y == 0.5).all()) and torch.equal(mean, X.view(-1).float())
+    dX, dw, db = bl.layer_norm_backward(X, X, mean, rstd)
+    # dX = rstd g - rstd c1 with c1 = g: the exact product less the rounded one, at most u rstd |g|
+    # (and u of that again for the second rounding), of either sign
+    assert bool((dX.float().abs() <= 2 * U * rstd[0] * X.float().abs()).all()) and float(dw) == 0
+    assert abs(float(db) - float(tail.double().sum())) <= 2000 * U * float(tail.double().abs().sum())
+
+
+@pytest.mark.parametrize("M,K", [(3, 100), (400, 520), (90, 9000), (40, 20000)])
+def test_gradients_one_at_a_time(M, K):
+    """dX, dweight and dbias each alone, through the C ABI, equal the call for all three."""
+    lib, g = abi.load(), torch.Generator(device=DEV).manual_seed(M)
+    X, dY = (torch.randn((M, K), generator=g, device=DEV) for _ in range(2))
+    _, mean, rstd = bl.layer_norm(X, return_stats=True)
+    ref = bl.layer_norm_backward(dY, X, mean, rstd)
+    need = lib.bitlinear_layer_norm_backward_workspace_bytes(M, K)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=DEV)
+    stream = torch.cuda.current_stream(DEV).cuda_stream
+    for i in range(3):
+        out = torch.full_like(ref[i], float("nan"))
+        p = [out.data_ptr() if i == j else None for j in range(3)]
+        assert lib.bitlinear_layer_norm_backward(
+            dY.data_ptr(), 0, X.data_ptr(), None, 0, mean.data_ptr(), rstd.data_ptr(), M, K, None, p[0], 0, p[1], p[2],
+            ws.data_ptr() if i and need else None, need if i else 0, stream) == abi.OK
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref[i])
+
+
 # ---- streams, graphs, refusals ------------------------------------------------------
 
 def test_other_stream():
@@ -405,6 +452,26 @@ def test_other_stream():
     s.synchronize()
     for a, b in zip((*ref[:3], *ref[3], *refb), (*got[:3], *got[3], *gotb)):
         assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    g = torch.Generator(device=DEV).manual_seed(9)
+    jobs = []
+    for M, K in ((3000, 1000), (700, 9000)):
+        X, dY = (torch.randn((M, K), generator=g, device=DEV) for _ in range(2))
+        st = bl.layer_norm(X, save=True)
+        jobs.append((X, dY, st, bl.layer_norm_backward(dY, st[3], st[1], st[2]), torch.cuda.Stream(DEV)))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, (X, dY, st, ref, s) in enumerate(jobs):
+            with torch.cuda.stream(s):
+                y = bl.layer_norm(X, save=True)
+                got[i].append((y, bl.layer_norm_backward(dY, y[3], y[1], y[2])))
+    torch.cuda.synchronize()
+    for i, (X, dY, st, ref, s) in enumerate(jobs):
+        for y, b in got[i]:
+            assert all(torch.equal(u, v) for u, v in zip((*y[:3], *y[3], *b), (*st[:3], *st[3], *ref)))
 
 
 def test_graph_replays_equal_eager():
@@ -426,14 +493,18 @@ def test_graph_replays_equal_eager():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out = step(X, dY, ws)
+    other = torch.cuda.CUDAGraph()  # one more of the same calls, with a workspace of its own pool
+    with torch.cuda.graph(other):
+        out2 = step(X, dY)
     for seed in range(4):
         g2 = torch.Generator(device=DEV).manual_seed(100 + seed)
         X.copy_(torch.randn((M, K), generator=g2, device=DEV))
         dY.copy_(torch.randn((M, K), generator=g2, device=DEV))
         graph.replay()
+        other.replay()
         torch.cuda.synchronize()
-        for a, r in zip(out, step(X.clone(), dY.clone())):
-            assert torch.equal(a, r)
+        for one, two, eager in zip(out, out2, step(X.clone(), dY.clone())):
+            assert torch.equal(one, eager) and torch.equal(two, eager)
         torch.cuda.synchronize()
 
 
