@@ -502,30 +502,31 @@ _BLOCK = None
 
 
 class _BlockCalls:
-    """What every call below needs, looked up once: torch, its dtypes and the C functions."""
+    """What every call below needs, looked up once: torch's functions and dtypes and the C functions."""
 
     def __init__(self):
         torch = _torch()
         lib = abi.load()
-        self.torch, self.f32, self.i8 = torch, torch.float32, torch.int8
+        self.f32, self.i8, self.empty, self.empty_like = torch.float32, torch.int8, torch.empty, torch.empty_like
         self.plain = {torch.float32: abi.F32, torch.bfloat16: abi.BF16}
-        self.device_now = torch.cuda.current_device
-        # the stream's address without a Stream object, where torch has that
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.stream_of = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self.on_device = torch.cuda.device
+        # the current device and a stream's address without torch's objects for them, where it has that
+        self.device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        self.stream_of = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                 lambda index: torch.cuda.current_stream(index).cuda_stream)
         for name in abi.BLOCK_SIGNATURES:
             setattr(self, name[len("bitlinear_"):], getattr(lib, name))
 
-    def launch(self, name, device, *args):
+    def launch(self, fn, device, *args):
         """Calls a C function on `device`'s current stream, with that device current."""
-        fn, index = getattr(self, name), device.index
+        index = device.index
         if index == self.device_now():
             status = fn(*args, self.stream_of(index))
         else:
-            with self.torch.cuda.device(index):
+            with self.on_device(index):
                 status = fn(*args, self.stream_of(index))
         if status:
-            abi.check("bitlinear_" + name, status)
+            abi.check(fn.__name__, status)
 
 
 def _block():
@@ -593,8 +594,8 @@ def _output(out, M, K, dtype, device, like=None):
     """`out`, checked, or a new [M, K] tensor (`like`: one of that shape on that device)."""
     if out is None:
         if like is not None and like.dtype == dtype:
-            return _block().torch.empty_like(like)
-        return _block().torch.empty((M, K), dtype=dtype, device=device)
+            return _block().empty_like(like)
+        return _block().empty((M, K), dtype=dtype, device=device)
     _require_cuda(out, "out")
     if out.shape != (M, K) or out.dtype != dtype or out.device != device:
         raise ValueError(f"out must be {dtype} [{M}, {K}] on {device}")
@@ -604,16 +605,17 @@ def _output(out, M, K, dtype, device, like=None):
 def _empty_saved(M, K, device):
     B = _block()
     groups = (K + 63) // 64
-    return (B.torch.empty((M, 64 * groups), dtype=B.i8, device=device),
-            B.torch.empty((M, groups), dtype=B.f32, device=device))
+    return (B.empty((M, 64 * groups), dtype=B.i8, device=device),
+            B.empty((M, groups), dtype=B.f32, device=device))
 
 
 def save_activations(X):
     """X (float32 or bfloat16 [M, K]) in 8 bits: the pair (codes, scales)."""
+    B = _block()
     dt, M, K = _matrix(X, "X")
     device = X.device
     codes, scales = saved = _empty_saved(M, K, device)
-    _block().launch("save_activations", device, X.data_ptr(), dt, M, K, codes.data_ptr(), scales.data_ptr())
+    B.launch(B.save_activations, device, X.data_ptr(), dt, M, K, codes.data_ptr(), scales.data_ptr())
     return saved
 
 
@@ -625,7 +627,7 @@ def restore_activations(saved, K: int, dtype=None, out=None):
         dtype = B.f32 if out is None else out.dtype
     dt = _plain_dtype(dtype, "dtype")
     X = _output(out, M, K, dtype, device)
-    B.launch("restore_activations", device, codes, scales, M, K, X.data_ptr(), dt)
+    B.launch(B.restore_activations, device, codes, scales, M, K, X.data_ptr(), dt)
     return X
 
 
@@ -648,16 +650,16 @@ def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, K: int | None = Non
         raise ValueError("X is saved already")
     Y = _output(out, M, K, out_dtype, device, like)
     if not (return_stats or save):
-        B.launch("layer_norm", device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, 0, 0, 0, 0)
+        B.launch(B.layer_norm, device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, 0, 0, 0, 0)
         return Y
-    mean = B.torch.empty(M, dtype=B.f32, device=device)
-    rstd = B.torch.empty_like(mean)
+    mean = B.empty(M, dtype=B.f32, device=device)
+    rstd = B.empty_like(mean)
     if not save:
-        B.launch("layer_norm", device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mean.data_ptr(),
+        B.launch(B.layer_norm, device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mean.data_ptr(),
                  rstd.data_ptr(), 0, 0)
         return Y, mean, rstd
     codes, scales = saved = _empty_saved(M, K, device)
-    B.launch("layer_norm", device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mean.data_ptr(),
+    B.launch(B.layer_norm, device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mean.data_ptr(),
              rstd.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return Y, mean, rstd, saved
 
@@ -690,20 +692,20 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, out_dtype=None, need_dx:
         dX = _output(None, M, K, out_dtype, device, dY)
         dxp = dX.data_ptr()
     if need_dw:
-        dw = B.torch.empty(K, dtype=B.f32, device=device)
-        db = B.torch.empty_like(dw)
+        dw = B.empty(K, dtype=B.f32, device=device)
+        db = B.empty_like(dw)
         dwp, dbp = dw.data_ptr(), db.data_ptr()
         if workspace is None:
             ws_bytes = B.layer_norm_backward_workspace_bytes(M, K)
             if ws_bytes:
-                workspace = B.torch.empty(ws_bytes, dtype=B.i8, device=device)
+                workspace = B.empty(ws_bytes, dtype=B.i8, device=device)
                 wsp = workspace.data_ptr()
         else:
             _require_cuda(workspace, "workspace")
             if workspace.device != device:
                 raise ValueError("workspace is on another device")
             wsp, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    B.launch("layer_norm_backward", device, dY.data_ptr(), ddt, x, xs, dt, mp, rp, M, K, w, dxp, odt, dwp, dbp,
+    B.launch(B.layer_norm_backward, device, dY.data_ptr(), ddt, x, xs, dt, mp, rp, M, K, w, dxp, odt, dwp, dbp,
              wsp, ws_bytes)
     return dX, dw, db
 
@@ -723,10 +725,10 @@ def relu2(H, K: int | None = None, out_dtype=None, save: bool = False, out=None)
         raise ValueError("H is saved already")
     A = _output(out, M, K, out_dtype, device, None if hs else H)
     if not save:
-        B.launch("relu2", device, h, hs, dt, M, K, A.data_ptr(), adt, 0, 0)
+        B.launch(B.relu2, device, h, hs, dt, M, K, A.data_ptr(), adt, 0, 0)
         return A
     codes, scales = saved = _empty_saved(M, K, device)
-    B.launch("relu2", device, h, hs, dt, M, K, A.data_ptr(), adt, codes.data_ptr(), scales.data_ptr())
+    B.launch(B.relu2, device, h, hs, dt, M, K, A.data_ptr(), adt, codes.data_ptr(), scales.data_ptr())
     return A, saved
 
 
@@ -735,6 +737,7 @@ def relu2_backward(dA, H, out_dtype=None, out=None):
 
     dH is of ``out_dtype`` (default: dA's; bfloat16 is what :func:`backward` takes).
     """
+    B = _block()
     adt, M, K = _matrix(dA, "dA")
     device = dA.device
     h, hs, dt, _, _, hdev = _whole_or_saved(H, K, "H", M)
@@ -744,5 +747,5 @@ def relu2_backward(dA, H, out_dtype=None, out=None):
         out_dtype = out.dtype if out is not None else dA.dtype
     odt = _plain_dtype(out_dtype, "out_dtype")
     dH = _output(out, M, K, out_dtype, device, dA)
-    _block().launch("relu2_backward", device, dA.data_ptr(), adt, h, hs, dt, M, K, dH.data_ptr(), odt)
+    B.launch(B.relu2_backward, device, dA.data_ptr(), adt, h, hs, dt, M, K, dH.data_ptr(), odt)
     return dH

@@ -180,3 +180,27 @@ def test_binding_refuses_host_tensors_and_bad_types():
             call()
     with pytest.raises(ValueError, match="K is needed"):
         bl.layer_norm((x.to(torch.int8), x))
+
+
+def test_binding_launches_on_the_tensors_device():
+    """A call for another device than the current one makes it current and uses that device's stream."""
+    from contextlib import contextmanager
+    from types import SimpleNamespace
+    B = object.__new__(bl._BlockCalls)
+    now, seen = [0], []
+
+    @contextmanager
+    def on_device(index):
+        before, now[0] = now[0], index
+        yield
+        now[0] = before
+
+    B.on_device, B.device_now, B.stream_of = on_device, lambda: now[0], lambda index: 1000 + index
+
+    def fn(*args):
+        seen.append((now[0], args))
+        return abi.OK
+
+    B.launch(fn, SimpleNamespace(index=0), 7)
+    B.launch(fn, SimpleNamespace(index=3), 8)
+    assert seen == [(0, (7, 1000)), (3, (8, 1003))] and now == [0]
