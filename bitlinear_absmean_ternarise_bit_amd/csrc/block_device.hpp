@@ -64,59 +64,91 @@ __device__ __forceinline__ void move_down(v4u& a, int n) {  // 16-bit values
     a = v4u{(a.x >> 16) | (a.y << 16), (a.y >> 16) | (a.z << 16), (a.z >> 16) | (a.w << 16), a.w >> 16};
 }
 
-// Chunk c (n values) of the row of K values at `row`; `scales`: the row's
-// scales (kSaved8, whose rows are padded with zero codes, so every chunk below
-// Kp / 8 is whole).  The row's end is read as its last 8 values (one load, like
-// every other chunk: value by value the loads would wait for one another, 4 us
-// a row) and moved into place; only a row of fewer than 8 goes value by value.
+// A row as a buffer resource of `bytes` bytes: what lies behind its end reads as
+// zeros and is not written, and an empty one (a row or an array that is not
+// there) takes a whole loop's stores without a branch (see fetch_chunk).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_resource(const void* row, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(row), 0, bytes, 0x00020000);
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every resource
+
+// Chunk c of the row of K >= 8 values at `row` as it lies in memory, for any c.
+// `scales`: the row's scales (kSaved8, whose rows are padded with zero codes).
+// Nothing is conditional, so a loop that loads its next row ahead waits for
+// those loads alone: around a branch with memory operations the compiler waits
+// for all that is outstanding, the last row's stores among them.
+// WHOLE: K is a multiple of 8; chunks behind the row are zeros.  Else the row's
+// end is read as its last 8 values (value by value the loads would wait for one
+// another, 4 us a row), and so is a chunk behind it: settle_chunk() before use.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ Raw<DT> fetch_chunk(const char* row, const float* scales, int K, int cpr, int c) {
+  Raw<DT> r;
+  if constexpr (WHOLE) {
+    const __amdgpu_buffer_rsrc_t from = row_resource(row, DT == kSaved8 ? cpr * 8 : K * kBytes<DT>);
+    if constexpr (DT == kSaved8) {
+      r.a = __builtin_amdgcn_raw_buffer_load_b64(from, 8 * c, 0, 0);
+      r.scale = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row_resource(scales, cpr / 2), c >> 3 << 2, 0, 0));
+    } else if constexpr (DT == kBf16) {
+      r.a = __builtin_amdgcn_raw_buffer_load_b128(from, 16 * c, 0, 0);
+    } else {
+      r.a = __builtin_amdgcn_raw_buffer_load_b128(from, 32 * c, 0, 0);
+      r.b = __builtin_amdgcn_raw_buffer_load_b128(from, 32 * c + 16, 0, 0);
+    }
+  } else if constexpr (DT == kSaved8) {
+    const uint32_t at = static_cast<uint32_t>(min(c, cpr - 1));
+    r.a = *reinterpret_cast<const v2u*>(row + 8u * at);
+    r.scale = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(scales) + 4u * (at >> 3));
+  } else if constexpr (DT == kBf16) {
+    r.a = *reinterpret_cast<const v4u_by2*>(row + 2u * static_cast<uint32_t>(min(8 * c, K - 8)));
+  } else {
+    const char* p = row + 4u * static_cast<uint32_t>(min(8 * c, K - 8));
+    r.a = *reinterpret_cast<const v4u_by4*>(p);
+    r.b = *reinterpret_cast<const v4u_by4*>(p + 16);
+  }
+  return r;
+}
+
+// Waits for a chunk's loads.  Called before a loop that loads ahead: with loads
+// outstanding on entry, each turn would wait for everything (the loop's head is
+// reached from outside with no stores behind the loads).
+__device__ __forceinline__ void arrive(Raw<kF32>& r) { asm volatile("" : "+v"(r.a), "+v"(r.b)); }
+__device__ __forceinline__ void arrive(Raw<kBf16>& r) { asm volatile("" : "+v"(r.a)); }
+__device__ __forceinline__ void arrive(Raw<kSaved8>& r) { asm volatile("" : "+v"(r.a), "+v"(r.scale)); }
+
+// Puts a fetched chunk's n values in place, zeros behind them.
 template <int DT>
+__device__ __forceinline__ void settle_chunk(Raw<DT>& r, int n) {
+  if (n == 8) return;
+  if constexpr (DT == kSaved8) {
+    if (n == 0) r.a = v2u{0u, 0u}, r.scale = 0.0f;
+  } else if constexpr (DT == kBf16) {
+    if (n > 0) move_down(r.a, n);
+    else r.a = v4u{0u, 0u, 0u, 0u};
+  } else {
+    if (n > 0) move_down(r.a, r.b, n);
+    else r.a = r.b = v4u{0u, 0u, 0u, 0u};
+  }
+}
+
+// Chunk c (n values) of the row of K values at `row`, in place.  SHORT: rows of
+// fewer than 8 values, which go value by value.
+template <int DT, bool SHORT = false>
 __device__ __forceinline__ Raw<DT> load_chunk(const char* row, const float* scales, int K, int c, int n) {
   Raw<DT> r;
-  if constexpr (DT == kSaved8) {
-    r.a = v2u{0u, 0u};
-    r.scale = 0.0f;
-    if (n > 0) {
-      r.a = *reinterpret_cast<const v2u*>(row + 8 * c);
-      r.scale = scales[c >> 3];
-    }
-  } else if constexpr (DT == kBf16) {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-    r.a = v4u{0u, 0u, 0u, 0u};
-    if (K >= 8) {
-      if (n > 0) r.a = *reinterpret_cast<const v4u_by2*>(p + (n == 8 ? 8 * c : K - 8));
-      if (n > 0 && n < 8) move_down(r.a, n);
-    } else if (n > 0) {
-      for (int i = 0; i < n; ++i) {
-        const uint32_t v = static_cast<uint32_t>(p[i]) << (16 * (i & 1));
-        if (i < 2) r.a.x |= v;
-        else if (i < 4) r.a.y |= v;
-        else if (i < 6) r.a.z |= v;
-        else r.a.w |= v;
-      }
-    }
+  if constexpr (DT == kSaved8 || !SHORT) {
+    if (n > 0) r = fetch_chunk<DT, false>(row, scales, K, 1 << 30, c);
+    settle_chunk<DT>(r, n);
   } else {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
     r.a = v4u{0u, 0u, 0u, 0u};
-    r.b = v4u{0u, 0u, 0u, 0u};
-    if (K >= 8) {
-      if (n > 0) {
-        p += n == 8 ? 8 * c : K - 8;
-        r.a = *reinterpret_cast<const v4u_by4*>(p);
-        r.b = *reinterpret_cast<const v4u_by4*>(p + 4);
-        if (n < 8) move_down(r.a, r.b, n);
+    if constexpr (DT == kF32) r.b = v4u{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) {
+        if constexpr (DT == kBf16)
+          r.a[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[i]) << (16 * (i & 1));
+        else
+          (i < 4 ? r.a : r.b)[i & 3] = reinterpret_cast<const uint32_t*>(row)[i];
       }
-    } else if (n > 0) {
-      for (int i = 0; i < n; ++i) {
-        const uint32_t v = p[i];
-        if (i == 0) r.a.x = v;
-        else if (i == 1) r.a.y = v;
-        else if (i == 2) r.a.z = v;
-        else if (i == 3) r.a.w = v;
-        else if (i == 4) r.b.x = v;
-        else if (i == 5) r.b.y = v;
-        else r.b.z = v;
-      }
-    }
   }
   return r;
 }
@@ -172,19 +204,46 @@ __device__ __forceinline__ void store_chunk(char* row, int c, int n, const float
   }
 }
 
+// Chunk c (n values) of a row.  WHOLE: chunks are whole or behind the row; else
+// a chunk that the row's end cuts goes value by value, the only branch.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void put_chunk(__amdgpu_buffer_rsrc_t row, int c, int n, const float (&v)[8]) {
+  const uint32_t at = WHOLE || n == 8 ? 8u * kBytes<DT> * c : kNowhere;
+  if constexpr (DT == kBf16) {
+    const v4u w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    __builtin_amdgcn_raw_buffer_store_b128(w, row, at, 0, 0);
+    if (!WHOLE && n > 0 && n < 8) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n)
+          __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(w[i >> 1] >> (16 * (i & 1))), row, 16u * c + 2u * i,
+                                                0, 0);
+    }
+  } else {
+    const v4u lo = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    const v4u hi = {__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    __builtin_amdgcn_raw_buffer_store_b128(lo, row, at, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(hi, row, at + 16u, 0, 0);
+    if (!WHOLE && n > 0 && n < 8) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (i < n) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), row, 32u * c + 4u * i, 0, 0);
+    }
+  }
+}
+
 template <int CTRL>
 __device__ __forceinline__ int dpp_move(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
 }
 
-// Saves chunk c (v is 0 past the row's end): its codes at `codes` + 8 c and,
-// by the first lane of each group, the group's scale.  All 8 lanes of a group
-// take part.  |x| is compared as an integer, so a NaN is the largest.
-// x * s is rounded to an integer by one FMA with 1.5 * 2^23: the sum has unit
-// spacing and rounds the exact product half to even, and its low byte is the
-// code.  No step depends on the order of anything: the codes are the same
-// whichever kernel saves.
-__device__ __forceinline__ void save_chunk(const float (&v)[8], int8_t* codes, float* scales, int c) {
+// The 8-bit form of a chunk (v is 0 past the row's end): its codes and its
+// group's scale.  All 8 lanes of a group take part.  |x| is compared as an
+// integer, so a NaN is the largest.  x * s is rounded to an integer by one FMA
+// with 1.5 * 2^23: the sum has unit spacing and rounds the exact product half to
+// even, and its low byte is the code.  No step depends on the order of
+// anything: the codes are the same whichever kernel saves.
+__device__ __forceinline__ void codes_of(const float (&v)[8], v2u& w, float& scale) {
   unsigned m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
@@ -195,8 +254,7 @@ __device__ __forceinline__ void save_chunk(const float (&v)[8], int8_t* codes, f
   const bool finite = m < 0x7f800000u;
   const bool live = finite && amax >= 0x1p-100f;
   const float s = live ? __fdiv_rn(127.0f, amax) : 0.0f;
-  const float scale = live ? __fmul_rn(amax, 1.0f / 127.0f) : finite ? 0.0f : __uint_as_float(0x7fc00000u);
-  v2u w;
+  scale = live ? __fmul_rn(amax, 1.0f / 127.0f) : finite ? 0.0f : __uint_as_float(0x7fc00000u);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t q[4];
@@ -206,8 +264,25 @@ __device__ __forceinline__ void save_chunk(const float (&v)[8], int8_t* codes, f
     w[h] = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400u) | __builtin_amdgcn_perm(q[3], q[2], 0x04000c0cu);
   }
   if (!finite) w = v2u{0u, 0u};
+}
+
+// Saves chunk c of a row: its codes, and by the first lane of each group the
+// group's scale.
+__device__ __forceinline__ void save_chunk(const float (&v)[8], int8_t* codes, float* scales, int c) {
+  v2u w;
+  float scale;
+  codes_of(v, w, scale);
   *reinterpret_cast<v2u*>(codes + 8 * c) = w;
   if ((c & 7) == 0) scales[c >> 3] = scale;
+}
+// The same into a row's resources; chunks behind the row fall outside them.
+__device__ __forceinline__ void save_chunk(const float (&v)[8], __amdgpu_buffer_rsrc_t codes,
+                                           __amdgpu_buffer_rsrc_t scales, int c) {
+  v2u w;
+  float scale;
+  codes_of(v, w, scale);
+  __builtin_amdgcn_raw_buffer_store_b64(w, codes, 8u * c, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(scale), scales, (c & 7) == 0 ? c >> 1 : kNowhere, 0, 0);
 }
 
 // Sum over a wave, in every lane: within each row of 16 lanes by DPP moves,

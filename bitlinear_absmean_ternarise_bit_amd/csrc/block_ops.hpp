@@ -33,8 +33,9 @@ struct BlockIn {
 // So few rows that one workgroup takes them in two turns are left to one: it
 // writes the gradients itself, and the second launch (about as long as a turn)
 // is saved.
-// Longer rows still (waves = 0): `groups` sets of rows for the column kernel,
-// 32 chunks of columns to a workgroup, about 1024 workgroups.
+// Longer rows still, and rows of fewer than 8 values (waves = 0): `groups` sets
+// of rows for the column kernel, 32 chunks of columns to a workgroup, about
+// 1024 workgroups.
 struct LnBwdPlan {
   int waves, chunks, teams, groups;
 };
@@ -43,7 +44,7 @@ constexpr int64_t kLnBwdMaxChunks = 2048;
 inline LnBwdPlan ln_bwd_plan(int64_t M, int64_t K, bool params) {
   const int64_t cpr = padded_k(K) / 8;
   LnBwdPlan p = {0, 1, 1, 1};
-  if (cpr > kLnBwdMaxChunks) {
+  if (cpr > kLnBwdMaxChunks || K < 8) {
     int64_t s = 1024 / ((cpr + 31) / 32);
     if (s > 256) s = 256;
     if (s > (M + 7) / 8) s = (M + 7) / 8;

@@ -26,8 +26,8 @@ constexpr int kLnWavesPerSimd = NC == 1 ? 8 : 4;
 // teams to a workgroup, without barriers.  Rows are gridDim.x T apart, about as
 // many teams as the card holds at once; each loads its next row before it works
 // on the current one, and keeps weight and bias in registers (NC <= 2), so that
-// nothing but that load is waited for.
-template <int XT, int YT, bool SAVE, int W, int NC>
+// nothing but that load is waited for.  WHOLE: K is a multiple of 8.
+template <int XT, int YT, bool SAVE, int W, int NC, bool WHOLE>
 __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void layer_norm_kernel(
     const char* __restrict__ X, const float* __restrict__ x_scales, int64_t M, int K, int cpr,
     const float* __restrict__ weight, const float* __restrict__ bias, float eps, char* __restrict__ Y,
@@ -50,9 +50,10 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void lay
   };
   Raw<XT> r[NC];
   auto load_row = [&](int64_t m) {
+    m = m < M ? m : 0;  // behind the last row: any row, not used
     const char* row = X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) r[j] = load_chunk<XT>(row, x_scales + m * G, K, c[j], n[j]);
+    for (int j = 0; j < NC; ++j) r[j] = fetch_chunk<XT, WHOLE>(row, x_scales + m * G, K, cpr, c[j]);
   };
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
@@ -67,11 +68,16 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void lay
 #pragma unroll
     for (int j = 0; j < NC; ++j) load_weights(j, w[j], b[j]);
   }
+#pragma unroll
+  for (int j = 0; j < NC; ++j) arrive(r[j]);
   for (; m < M; m += stride) {
     float v[NC][8], sum[1] = {0.0f};
 #pragma unroll
-    for (int j = 0; j < NC; ++j) chunk_f32<XT>(r[j], v[j]);
-    if (m + stride < M) load_row(m + stride);
+    for (int j = 0; j < NC; ++j) {
+      if constexpr (!WHOLE) settle_chunk<XT>(r[j], n[j]);
+      chunk_f32<XT>(r[j], v[j]);
+    }
+    load_row(m + stride);
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -79,9 +85,10 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void lay
     team_sum<W>(sum, slots[0], wt, lane);
     const float mean = sum[0] * inv_k;
     if constexpr (SAVE) {
+      const __amdgpu_buffer_rsrc_t to_codes = row_resource(codes + m * Kp, static_cast<int>(Kp));
+      const __amdgpu_buffer_rsrc_t to_scales = row_resource(scales + m * G, static_cast<int>(4 * G));
 #pragma unroll
-      for (int j = 0; j < NC; ++j)
-        if (c[j] < cpr) save_chunk(v[j], codes + m * Kp, scales + m * G, c[j]);
+      for (int j = 0; j < NC; ++j) save_chunk(v[j], to_codes, to_scales, c[j]);
     }
     float sq[1] = {0.0f};
 #pragma unroll
@@ -90,31 +97,32 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void lay
       for (int e = 0; e < 8; ++e) v[j][e] -= mean;
       if (n[j] < 8) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = e < n[j] ? v[j][e] : 0.0f;
+        for (int e = 0; e < 8; ++e) v[j][e] = (WHOLE ? n[j] > 0 : e < n[j]) ? v[j][e] : 0.0f;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sq[0] = __fmaf_rn(v[j][e], v[j][e], sq[0]);
     }
     team_sum<W>(sq, slots[1], wt, lane);
     const float rstd = 1.0f / sqrtf(sq[0] * inv_k + eps);
+    const __amdgpu_buffer_rsrc_t to_y = row_resource(Y + m * K * kBytes<YT>, K * kBytes<YT>);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int held = kHoldWeights ? j : 0;
       if constexpr (!kHoldWeights) load_weights(j, w[0], b[0]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] = __fmaf_rn(v[j][e] * rstd, w[held][e], b[held][e]);
-      store_chunk<YT>(Y + m * K * kBytes<YT>, c[j], n[j], v[j]);
+      put_chunk<YT, WHOLE>(to_y, c[j], n[j], v[j]);
     }
-    if (mean_out && wt == 0 && lane == 0) {
-      mean_out[m] = mean;
-      rstd_out[m] = rstd;
-    }
+    // by the team's first lane: the others fall behind 4 bytes
+    const int stats = mean_out && wt == 0 ? 4 : 0;
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(mean), row_resource(mean_out + m, stats), 4u * lane, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rstd), row_resource(rstd_out + m, stats), 4u * lane, 0, 0);
   }
 }
 
-// Long rows: one workgroup per row, rows gridDim.x apart; the row is read from memory
+// Long rows, and rows of fewer than 8 (SHORT): one workgroup per row, rows gridDim.x apart; the row is read from memory
 // (the caches after the first time) for the mean, the variance and the output.
-template <int XT, int YT, bool SAVE>
+template <int XT, int YT, bool SAVE, bool SHORT>
 __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     const char* __restrict__ X, const float* __restrict__ x_scales, int64_t M, int K, int cpr,
     const float* __restrict__ weight, const float* __restrict__ bias, float eps, char* __restrict__ Y,
@@ -129,7 +137,7 @@ __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     float sum[1] = {0.0f};
     for (int c = tid; c < cpr; c += 256) {
       float v[8];
-      chunk_f32<XT>(load_chunk<XT>(row, rs, K, c, chunk_values(K, c)), v);
+      chunk_f32<XT>(load_chunk<XT, SHORT>(row, rs, K, c, chunk_values(K, c)), v);
       if constexpr (SAVE) save_chunk(v, codes + m * Kp, scales + m * G, c);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[0] += v[e];
@@ -140,7 +148,7 @@ __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     for (int c = tid; c < cpr; c += 256) {
       const int n = chunk_values(K, c);
       float v[8];
-      chunk_f32<XT>(load_chunk<XT>(row, rs, K, c, n), v);
+      chunk_f32<XT>(load_chunk<XT, SHORT>(row, rs, K, c, n), v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = e < n ? v[e] - mean : 0.0f;
@@ -152,9 +160,9 @@ __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     for (int c = tid; c < cpr; c += 256) {
       const int n = chunk_values(K, c);
       float v[8], w[8], b[8];
-      chunk_f32<XT>(load_chunk<XT>(row, rs, K, c, n), v);
-      if (weight) chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, K, c, n), w);
-      if (bias) chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(bias), nullptr, K, c, n), b);
+      chunk_f32<XT>(load_chunk<XT, SHORT>(row, rs, K, c, n), v);
+      if (weight) chunk_f32<kF32>(load_chunk<kF32, SHORT>(reinterpret_cast<const char*>(weight), nullptr, K, c, n), w);
+      if (bias) chunk_f32<kF32>(load_chunk<kF32, SHORT>(reinterpret_cast<const char*>(bias), nullptr, K, c, n), b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float xh = (v[e] - mean) * rstd;
@@ -186,7 +194,8 @@ void launch_held(const Args& a, hipStream_t stream) {
   constexpr int64_t most = 256 * (4 * kLnWavesPerSimd<NC> / (W > 1 ? W : 4));  // workgroups that 256 CUs hold
   const int64_t wgs = (a.M + T - 1) / T, turns = (wgs + most - 1) / most;
   const int64_t blocks = (wgs + turns - 1) / turns;  // as many turns for each
-  layer_norm_kernel<XT, YT, SAVE, W, NC><<<static_cast<unsigned>(blocks), W > 1 ? 64 * W : 256, 0, stream>>>(
+  auto kernel = a.K % 8 == 0 ? layer_norm_kernel<XT, YT, SAVE, W, NC, true> : layer_norm_kernel<XT, YT, SAVE, W, NC, false>;
+  kernel<<<static_cast<unsigned>(blocks), W > 1 ? 64 * W : 256, 0, stream>>>(
       static_cast<const char*>(a.X.p), a.X.scales, a.M, static_cast<int>(a.K), static_cast<int>(padded_k(a.K) / 8),
       a.weight, a.bias, a.eps, static_cast<char*>(a.Y), a.mean, a.rstd, a.saved, a.saved_scales);
 }
@@ -194,7 +203,13 @@ void launch_held(const Args& a, hipStream_t stream) {
 template <int XT, int YT, bool SAVE>
 hipError_t launch(const Args& a, hipStream_t stream) {
   const int cpr = static_cast<int>(padded_k(a.K) / 8);
-  if (cpr <= 64) {
+  if (a.K < 8 || cpr > kLnMaxChunks) {
+    const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
+    auto kernel = a.K < 8 ? layer_norm_rows_kernel<XT, YT, SAVE, true> : layer_norm_rows_kernel<XT, YT, SAVE, false>;
+    kernel<<<blocks, 256, 0, stream>>>(static_cast<const char*>(a.X.p), a.X.scales, a.M, static_cast<int>(a.K), cpr,
+                                       a.weight, a.bias, a.eps, static_cast<char*>(a.Y), a.mean, a.rstd, a.saved,
+                                       a.saved_scales);
+  } else if (cpr <= 64) {
     launch_held<XT, YT, SAVE, 1, 1>(a, stream);
   } else if (cpr <= 128) {
     launch_held<XT, YT, SAVE, 2, 1>(a, stream);
@@ -206,13 +221,8 @@ hipError_t launch(const Args& a, hipStream_t stream) {
     launch_held<XT, YT, SAVE, 16, 1>(a, stream);
   } else if (cpr <= 2048) {
     launch_held<XT, YT, SAVE, 16, 2>(a, stream);
-  } else if (cpr <= kLnMaxChunks) {
-    launch_held<XT, YT, SAVE, 16, 4>(a, stream);
   } else {
-    const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
-    layer_norm_rows_kernel<XT, YT, SAVE><<<blocks, 256, 0, stream>>>(
-        static_cast<const char*>(a.X.p), a.X.scales, a.M, static_cast<int>(a.K), cpr, a.weight, a.bias, a.eps,
-        static_cast<char*>(a.Y), a.mean, a.rstd, a.saved, a.saved_scales);
+    launch_held<XT, YT, SAVE, 16, 4>(a, stream);
   }
   return hipGetLastError();
 }

@@ -30,7 +30,8 @@ namespace {
 // and a value is converted once.
 //
 // PARAMS false: dx alone, for rows whose dw and db do not fit beside them.
-template <int XT, int DT, int OT, int W, int NC, int THREADS, bool PARAMS>
+// WHOLE: K is a multiple of 8.
+template <int XT, int DT, int OT, int W, int NC, int THREADS, bool PARAMS, bool WHOLE>
 __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
     const char* __restrict__ dY, const char* __restrict__ X, const float* __restrict__ x_scales,
     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t M, int K, int cpr,
@@ -77,33 +78,45 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
   Raw<DT> rd[NC];
   float next_mean, next_rstd;
   auto load_row = [&](int64_t m) {
-    const bool ok = m < M;
-    if (!ok) m = 0;
-    next_mean = ok ? mean_in[m] : 0.0f;
-    next_rstd = ok ? rstd_in[m] : 0.0f;
+    // behind the last row: any row, whose loads (WHOLE) or values are zeros
+    const int behind = m < M ? 0 : cpr;
+    m = m < M ? m : 0;
+    next_mean = mean_in[m];
+    next_rstd = rstd_in[m];
     const char* row = X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>);
     const char* drow = dY + m * K * kBytes<DT>;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      rx[j] = load_chunk<XT>(row, x_scales + m * G, K, c[j], ok ? n[j] : 0);
-      rd[j] = load_chunk<DT>(drow, nullptr, K, c[j], ok ? n[j] : 0);
+      rx[j] = fetch_chunk<XT, WHOLE>(row, x_scales + m * G, K, cpr, c[j] + behind);
+      rd[j] = fetch_chunk<DT, WHOLE>(drow, nullptr, K, cpr, c[j] + behind);
     }
   };
   const int64_t stride = static_cast<int64_t>(gridDim.x) * T;
   int64_t m = static_cast<int64_t>(blockIdx.x) * T + team;
   const int64_t iters = (M + stride - 1) / stride;
   load_row(m);
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    arrive(rx[j]);
+    arrive(rd[j]);
+  }
   for (int64_t it = 0; it < iters; ++it, m += stride) {
+    const bool ok = m < M;
     const float mu = next_mean, rs = next_rstd;
     float xh[NC][8], g[NC][8], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
+      if constexpr (!WHOLE) {
+        const int nj = ok ? n[j] : 0;
+        settle_chunk<XT>(rx[j], nj);
+        settle_chunk<DT>(rd[j], nj);
+      }
       chunk_f32<XT>(rx[j], xh[j]);
       chunk_f32<DT>(rd[j], g[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) xh[j][e] = (xh[j][e] - mu) * rs;
     }
-    if (it + 1 < iters) load_row(m + stride);
+    load_row(m + stride);
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -117,13 +130,13 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
         s[1] = __fmaf_rn(g[j][e], xh[j][e], s[1]);
       }
     team_sum<W>(s, slots[it & 1] + team * W * 2, wt, lane);
-    if (!dX || m >= M) continue;
+    const __amdgpu_buffer_rsrc_t to = row_resource(dX + (ok ? m * K * kBytes<OT> : 0), dX && ok ? K * kBytes<OT> : 0);
     const float k1 = rs * (s[0] * inv_k), k2 = rs * (s[1] * inv_k);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[j][e] = __fmaf_rn(-k2, xh[j][e], __fmaf_rn(rs, g[j][e], -k1));
-      store_chunk<OT>(dX + m * K * kBytes<OT>, c[j], n[j], g[j]);
+      put_chunk<OT, WHOLE>(to, c[j], n[j], g[j]);
     }
   }
   if (!PARAMS || (!dw_out && !db_out)) return;
@@ -163,9 +176,9 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
   }
 }
 
-// dx of long rows: one workgroup per row, rows gridDim.x apart; the row is read for the two
+// dx of long rows, and of rows of fewer than 8 (SHORT): one workgroup per row, rows gridDim.x apart; the row is read for the two
 // sums and again for the output.
-template <int XT, int DT, int OT>
+template <int XT, int DT, int OT, bool SHORT>
 __global__ __launch_bounds__(256) void ln_dx_rows_kernel(
     const char* __restrict__ dY, const char* __restrict__ X, const float* __restrict__ x_scales,
     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t M, int K, int cpr,
@@ -180,11 +193,11 @@ __global__ __launch_bounds__(256) void ln_dx_rows_kernel(
     const char* drow = dY + m * K * kBytes<DT>;
     const float mean = mean_in[m], rstd = rstd_in[m];
     auto chunk = [&](int c, int n, float (&g)[8], float (&xh)[8]) {
-      chunk_f32<XT>(load_chunk<XT>(row, x_scales + m * G, K, c, n), xh);
-      chunk_f32<DT>(load_chunk<DT>(drow, nullptr, K, c, n), g);
+      chunk_f32<XT>(load_chunk<XT, SHORT>(row, x_scales + m * G, K, c, n), xh);
+      chunk_f32<DT>(load_chunk<DT, SHORT>(drow, nullptr, K, c, n), g);
       if (weight) {
         float w[8];
-        chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, K, c, n), w);
+        chunk_f32<kF32>(load_chunk<kF32, SHORT>(reinterpret_cast<const char*>(weight), nullptr, K, c, n), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] *= w[e];
       }
@@ -216,7 +229,7 @@ __global__ __launch_bounds__(256) void ln_dx_rows_kernel(
 
 // Partial dw and db of slab blockIdx.y (rows slab, slab + slabs, ... in groups
 // of 8): 32 chunks of columns by 8 rows at a time.
-template <int XT, int DT>
+template <int XT, int DT, bool SHORT>
 __global__ __launch_bounds__(256) void ln_param_cols_kernel(
     const char* __restrict__ dY, const char* __restrict__ X, const float* __restrict__ x_scales,
     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t M, int K, int cpr,
@@ -229,8 +242,8 @@ __global__ __launch_bounds__(256) void ln_param_cols_kernel(
   float dw[8] = {}, db[8] = {};
   for (int64_t m = blockIdx.y * 8 + r; m < M; m += int64_t(gridDim.y) * 8) {
     float xh[8], d[8];
-    chunk_f32<XT>(load_chunk<XT>(X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>), x_scales + m * G, K, c, n), xh);
-    chunk_f32<DT>(load_chunk<DT>(dY + m * K * kBytes<DT>, nullptr, K, c, n), d);
+    chunk_f32<XT>(load_chunk<XT, SHORT>(X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>), x_scales + m * G, K, c, n), xh);
+    chunk_f32<DT>(load_chunk<DT, SHORT>(dY + m * K * kBytes<DT>, nullptr, K, c, n), d);
     const float mean = mean_in[m], rstd = rstd_in[m];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -295,7 +308,9 @@ template <int XT, int DT, int OT, int W, int NC, int THREADS = 1024, bool PARAMS
 void launch_one(const Args& a, const LnBwdPlan& p, hipStream_t stream) {
   const int64_t K = a.K;
   const bool only = p.groups == 1;  // its sums are the gradients
-  ln_backward_kernel<XT, DT, OT, W, NC, THREADS, PARAMS><<<p.groups, 64 * W * p.teams, 0, stream>>>(
+  auto kernel = K % 8 == 0 ? ln_backward_kernel<XT, DT, OT, W, NC, THREADS, PARAMS, true>
+                           : ln_backward_kernel<XT, DT, OT, W, NC, THREADS, PARAMS, false>;
+  kernel<<<p.groups, 64 * W * p.teams, 0, stream>>>(
       static_cast<const char*>(a.dY), static_cast<const char*>(a.X.p), a.X.scales, a.mean, a.rstd, a.M,
       static_cast<int>(K), static_cast<int>(padded_k(K) / 8), a.weight, static_cast<char*>(a.dX),
       !a.dweight ? nullptr : only ? a.dweight : a.partial, !a.dbias ? nullptr : only ? a.dbias : a.partial + K, 2 * K);
@@ -305,20 +320,23 @@ template <int XT, int DT, int OT>
 hipError_t launch(const Args& a, hipStream_t stream) {
   const int cpr = static_cast<int>(padded_k(a.K) / 8), K = static_cast<int>(a.K);
   const LnBwdPlan p = ln_bwd_plan(a.M, a.K, a.dweight || a.dbias);
-  if (p.waves == 0) {  // long rows
+  if (p.waves == 0) {
     const char* dY = static_cast<const char*>(a.dY);
     const char* X = static_cast<const char*>(a.X.p);
-    if (a.dX && cpr <= kLnDxMaxChunks) {
+    if (a.dX && K >= 8 && cpr <= kLnDxMaxChunks) {
       const LnBwdPlan dx = {8, 7, 1, static_cast<int>(a.M < 256 ? a.M : 256)};
       launch_one<XT, DT, OT, 8, 7, 512, false>(a, dx, stream);
     } else if (a.dX) {
       const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
-      ln_dx_rows_kernel<XT, DT, OT><<<blocks, 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr,
-                                                               a.weight, static_cast<char*>(a.dX));
+      auto kernel = K < 8 ? ln_dx_rows_kernel<XT, DT, OT, true> : ln_dx_rows_kernel<XT, DT, OT, false>;
+      kernel<<<blocks, 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr, a.weight,
+                                         static_cast<char*>(a.dX));
     }
-    if (a.dweight || a.dbias)
-      ln_param_cols_kernel<XT, DT><<<dim3((cpr + 31) / 32, p.groups), 256, 0, stream>>>(
-          dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr, a.partial);
+    if (a.dweight || a.dbias) {
+      auto kernel = K < 8 ? ln_param_cols_kernel<XT, DT, true> : ln_param_cols_kernel<XT, DT, false>;
+      kernel<<<dim3((cpr + 31) / 32, p.groups), 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr,
+                                                                  a.partial);
+    }
   } else if (p.chunks == 1) {
     if (p.waves == 1) launch_one<XT, DT, OT, 1, 1>(a, p, stream);
     else if (p.waves == 2) launch_one<XT, DT, OT, 2, 1>(a, p, stream);

@@ -19,12 +19,13 @@ __device__ __forceinline__ float relu(float h) { return h <= 0.0f ? 0.0f : h; }
 //   kRestore:       in (saved) -> out
 //   kRelu2:         in -> out (and codes, scales when SAVE)
 //   kRelu2Backward: dA, in -> out
+// SHORT: rows of fewer than 8 values.
 // Bound by HBM: 5.7 to 6.1 TB/s over arrays of 2048x11008 and larger (a copy of
 // 2 GiB reaches 4.9).  Two or four chunks to a thread, loaded first, are 1% to
 // 35% slower there and slower still on small arrays; total is 32 bits (at most
 // 2^31 chunks to a launch) because a 64-bit division takes about as many
 // instructions as the rest of a chunk (2048x4096 bf16: 3% to 8% slower).
-template <int OP, int IT, int OT, int DT, bool SAVE>
+template <int OP, int IT, int OT, int DT, bool SAVE, bool SHORT>
 __global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in, const float* __restrict__ in_scales,
                                                     const char* __restrict__ dA, uint32_t total, int K, int cpr,
                                                     char* __restrict__ out, int8_t* __restrict__ codes,
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in,
   const int c = static_cast<int>(i - row * static_cast<uint32_t>(cpr)), n = chunk_values(K, c);
   const int64_t m = row;
   float v[8];
-  chunk_f32<IT>(load_chunk<IT>(in + (IT == kSaved8 ? m * Kp : m * K * kBytes<IT>), in_scales + m * G, K, c, n), v);
+  chunk_f32<IT>(load_chunk<IT, SHORT>(in + (IT == kSaved8 ? m * Kp : m * K * kBytes<IT>), in_scales + m * G, K, c, n), v);
   if constexpr (SAVE) save_chunk(v, codes + m * Kp, scales + m * G, c);
   if constexpr (OP == kRelu2) {
 #pragma unroll
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in,
     }
   } else if constexpr (OP == kRelu2Backward) {
     float d[8];
-    chunk_f32<DT>(load_chunk<DT>(dA + m * K * kBytes<DT>, nullptr, K, c, n), d);
+    chunk_f32<DT>(load_chunk<DT, SHORT>(dA + m * K * kBytes<DT>, nullptr, K, c, n), d);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(d[e], 2.0f * relu(v[e]));
   }
@@ -64,7 +65,8 @@ hipError_t launch(BlockIn in, const void* dA, int64_t M, int64_t K, void* out, i
   for (int64_t m = 0; m < M; m += most) {
     const int64_t total = (M - m < most ? M - m : most) * cpr;
     // arrays that the operation does not have stay NULL
-    chunk_kernel<OP, IT, OT, DT, SAVE><<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(
+    auto kernel = K < 8 ? chunk_kernel<OP, IT, OT, DT, SAVE, true> : chunk_kernel<OP, IT, OT, DT, SAVE, false>;
+    kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(
         src + (IT == kSaved8 ? m * Kp : m * K * kBytes<IT>), in.scales ? in.scales + m * G : nullptr,
         d ? d + m * K * kBytes<DT> : nullptr, static_cast<uint32_t>(total), static_cast<int>(K),
         static_cast<int>(cpr), dst ? dst + m * K * kBytes<OT> : nullptr, codes ? codes + m * Kp : nullptr,
