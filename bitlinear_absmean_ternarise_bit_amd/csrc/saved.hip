@@ -10,6 +10,8 @@ namespace {
 // What a pass over [M, K] does with a chunk.
 enum Op { kSave, kRestore, kRelu2, kRelu2Backward };
 
+constexpr uint32_t kRun = 256;  // consecutive workgroups of an XCD
+
 // max(h, 0), and a NaN for a NaN
 __device__ __forceinline__ float relu(float h) { return h <= 0.0f ? 0.0f : h; }
 
@@ -20,8 +22,12 @@ __device__ __forceinline__ float relu(float h) { return h <= 0.0f ? 0.0f : h; }
 //   kRelu2:         in -> out (and codes, scales when SAVE)
 //   kRelu2Backward: dA, in -> out
 // SHORT: rows of fewer than 8 values.
-// Bound by HBM: 5.7 to 6.1 TB/s over arrays of 2048x11008 and larger (a copy of
-// 2 GiB reaches 4.9).  Two or four chunks to a thread, loaded first, are 1% to
+// Bound by HBM: 5.7 to 6.2 TB/s over arrays of 2048x11008 and larger (a copy of
+// 2 GiB reaches 4.9).  Workgroups are dealt round-robin to the 8 XCDs; each XCD
+// takes runs of kRun consecutive workgroups, 2 MiB of float32, so that it
+// streams through memory: 8192x28672, save 203 -> 192 us, ReLU^2 325 -> 315, its
+// backward 284 -> 274; nothing on arrays below 2048x11008; runs of 4, 1024 or
+// 4096 are slower than none.  Two or four chunks to a thread, loaded first, are 1% to
 // 35% slower there and slower still on small arrays; total is 32 bits (at most
 // 2^31 chunks to a launch) because a 64-bit division takes about as many
 // instructions as the rest of a chunk (2048x4096 bf16: 3% to 8% slower).
@@ -31,7 +37,9 @@ __global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in,
                                                     char* __restrict__ out, int8_t* __restrict__ codes,
                                                     float* __restrict__ scales) {
   const int64_t G = cpr >> 3, Kp = int64_t(cpr) * 8;
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t b = blockIdx.x, in_turn = b % (8 * kRun);
+  const uint32_t wg = b - in_turn + 8 * kRun <= gridDim.x ? b - in_turn + (in_turn & 7) * kRun + (in_turn >> 3) : b;
+  const uint32_t i = wg * 256u + threadIdx.x;
   if (i >= total) return;  // total is a multiple of 8: whole groups leave
   const uint32_t row = i / static_cast<uint32_t>(cpr);
   const int c = static_cast<int>(i - row * static_cast<uint32_t>(cpr)), n = chunk_values(K, c);
