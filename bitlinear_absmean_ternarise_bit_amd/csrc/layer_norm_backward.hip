@@ -58,7 +58,9 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
     n[j] = c[j] < cpr ? chunk_values(K, c[j]) : 0;
     float w[8];
     if (weight) {
-      chunk_f32<kF32>(load_chunk<kF32>(reinterpret_cast<const char*>(weight), nullptr, K, c[j], n[j]), w);
+      Raw<kF32> rw = fetch_chunk<kF32, WHOLE>(reinterpret_cast<const char*>(weight), nullptr, K, cpr, c[j]);
+      if constexpr (!WHOLE) settle_chunk<kF32>(rw, n[j]);
+      chunk_f32<kF32>(rw, w);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = 1.0f;
