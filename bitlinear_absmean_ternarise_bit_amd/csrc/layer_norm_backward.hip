@@ -274,7 +274,8 @@ __global__ __launch_bounds__(256) void ln_param_cols_kernel(
 }
 
 // dw[k] = sum over the partial rows of partial[row][0][k], db likewise from
-// [1]: 64 columns to a workgroup, 16 rows at a time, then the 16 sums in order.
+// [1]: 64 columns to a workgroup, a wave to every 16th row (at most 256 rows, so
+// 16 loads, all in flight), then the 16 waves' sums in order.
 __global__ __launch_bounds__(1024) void ln_param_sum_kernel(const float* __restrict__ partial, int rows, int K,
                                                             float* __restrict__ dw, float* __restrict__ db) {
   __shared__ float sums[16][64];
@@ -284,8 +285,11 @@ __global__ __launch_bounds__(1024) void ln_param_sum_kernel(const float* __restr
   const int k = blockIdx.x * 64 + kl;
   const float* p = partial + static_cast<int64_t>(blockIdx.y) * K + min(k, K - 1);
   float t = 0.0f;
-#pragma unroll 8
-  for (int s = r; s < rows; s += 16) t += p[static_cast<int64_t>(s) * 2 * K];
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = r + 16 * i < rows ? p[static_cast<int64_t>(r + 16 * i) * 2 * K] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t += v[i];
   sums[r][kl] = t;
   __syncthreads();
   if (r == 0 && k < K) {
