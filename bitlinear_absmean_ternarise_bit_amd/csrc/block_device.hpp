@@ -162,10 +162,7 @@ __device__ __forceinline__ void chunk_f32(const Raw<DT>& r, float (&v)[8]) {
     } else if constexpr (DT == kBf16) {
       v[i] = __uint_as_float((i & 1) ? r.a[i >> 1] & 0xffff0000u : r.a[i >> 1] << 16);
     } else {
-      // code + 128 is a byte, one conversion; 128 scale is exact, so the FMA
-      // rounds scale * code once
-      const uint32_t u = ((r.a[i >> 2] ^ 0x80808080u) >> (8 * (i & 3))) & 0xffu;
-      v[i] = __fmaf_rn(r.scale, static_cast<float>(u), -128.0f * r.scale);
+      v[i] = r.scale * static_cast<float>(static_cast<int8_t>(r.a[i >> 2] >> (8 * (i & 3))));
     }
   }
 }

@@ -119,6 +119,23 @@ def test_save_special_values():
     assert np.isnan(dH[1, :64]).all() and np.isnan(dH[2, 64:128]).all() and np.isfinite(dH[0]).all()
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_restore_of_the_largest_values(out):
+    """Groups whose scale times 128 is past the largest float32."""
+    top = np.float32(3.4028235e38)
+    X = np.zeros((4, 130), np.float32)
+    X[0, :6] = [top, -top, top / 2, -top / 3, 1e36, -3e35]
+    X[1, 64:68] = [-3.3895314e38, 1e38, 3.37e38, -3.3e38]
+    X[2, 128:] = [-3.38e38, 3.38e38]
+    X[3, :64] = np.float32(3.375e38)
+    codes, scales = B.save8(X)
+    with np.errstate(over="ignore"):
+        ref = to_type(B.restore8(codes, scales, 130), out)
+    saved = bl.save_activations(on_gpu(X, "f32"))
+    assert np.array_equal(saved[0].cpu().numpy(), codes) and same_bits(saved[1].cpu().numpy(), scales)
+    assert same_bits(np_of(bl.restore_activations(saved, 130, dtype=DT[out])), ref)
+
+
 # ---- ReLU^2 -------------------------------------------------------------------
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
