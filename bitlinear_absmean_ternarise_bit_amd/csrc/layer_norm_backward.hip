@@ -107,7 +107,9 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
   }
   for (int64_t it = 0; it < iters; ++it, m += stride) {
     const bool ok = m < M;
-    const float mu = next_mean, rs = next_rstd;
+    // a team past the last row has x = dy = 0; with xhat 0 too, whatever the
+    // first row's statistics are
+    const float mu = ok ? next_mean : 0.0f, rs = ok ? next_rstd : 0.0f;
     float xh[NC][8], g[NC][8], s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NC; ++j) {

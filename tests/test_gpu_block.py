@@ -304,6 +304,19 @@ def test_layer_norm_non_finite_rows_stay_apart():
     assert np.isnan(dX[1]).all() and np.isfinite(dX[[0, 3]]).all()
 
 
+@pytest.mark.parametrize("K", [100, 104, 4100])
+def test_statistics_stay_with_their_row(K):
+    """Infinite statistics of the first row, with teams behind the last one: dweight has that row's
+    infinities and no NaN of another team's making."""
+    M = 257
+    g = torch.Generator(device=DEV).manual_seed(K)
+    X, dY = torch.randn((M, K), generator=g, device=DEV), torch.ones((M, K), device=DEV)
+    _, mean, rstd = bl.layer_norm(X, return_stats=True)
+    mean[0], rstd[0] = 100.0, float("inf")  # every difference to the mean is negative
+    dX, dw, db = bl.layer_norm_backward(dY, X, mean, rstd)
+    assert bool((dw == -float("inf")).all()) and bool((db == M).all()) and bool(torch.isfinite(dX[1:]).all())
+
+
 def test_layer_norm_gradient_by_differences():
     rng = np.random.default_rng(5)
     M, K, h = 3, 96, 2.0 ** -6
