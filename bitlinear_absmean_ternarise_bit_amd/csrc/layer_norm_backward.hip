@@ -121,7 +121,11 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
       chunk_f32<XT>(rx[j], xh[j]);
       chunk_f32<DT>(rd[j], g[j]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) xh[j][e] = (xh[j][e] - mu) * rs;
+      for (int e = 0; e < 8; ++e) {
+        // behind the row x is 0, and mean rstd may be infinite and meet dy = 0
+        const float mean = (WHOLE ? n[j] > 0 : e < n[j]) ? mu : 0.0f;
+        xh[j][e] = (xh[j][e] - mean) * rs;
+      }
     }
     load_row(m + stride);
 #pragma unroll
@@ -209,7 +213,7 @@ __global__ __launch_bounds__(256) void ln_dx_rows_kernel(
         for (int e = 0; e < 8; ++e) g[e] *= w[e];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) xh[e] = (xh[e] - mean) * rstd;
+      for (int e = 0; e < 8; ++e) xh[e] = e < n ? (xh[e] - mean) * rstd : 0.0f;
     };
     float s[2] = {0.0f, 0.0f};
     for (int c = tid; c < cpr; c += 256) {

@@ -317,6 +317,20 @@ def test_statistics_stay_with_their_row(K):
     assert bool((dw == -float("inf")).all()) and bool((db == M).all()) and bool(torch.isfinite(dX[1:]).all())
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [6, 10, 100, 104, 4100, 5000, 20000, 20004, 33000])
+def test_layer_norm_backward_large_constant_rows(K, dt):
+    """mean * rstd past the largest float32, xhat = 0: dX = rstd (dY - mean of dY), here rstd dY.
+    Nothing rounds: the sums over dY = +1, -1, ... are sums of small integers."""
+    M, top, rs = 3, 2.0 ** 118, 2.0 ** 17
+    X = torch.full((M, K), top, device=DEV, dtype=DT[dt])
+    dY = torch.ones((M, K), device=DEV)
+    dY[:, 1::2] = -1
+    mean, rstd = torch.full((M,), top, device=DEV), torch.full((M,), rs, device=DEV)
+    dX, dw, db = bl.layer_norm_backward(dY, X, mean, rstd, out_dtype=torch.float32)
+    assert torch.equal(dX, rs * dY) and not bool(dw.any()) and torch.equal(db, M * dY[0])
+
+
 def test_layer_norm_gradient_by_differences():
     rng = np.random.default_rng(5)
     M, K, h = 3, 96, 2.0 ** -6
