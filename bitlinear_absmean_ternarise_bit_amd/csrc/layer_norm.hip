@@ -3,8 +3,8 @@
 //   y = (x - mean) rstd w + b
 // in float32, with the row's 8-bit copy written from the same read.  Bound by
 // the bytes of x and y (and the copy): layer_norm_kernel reads a row once and
-// keeps it in registers; rows over kLnMaxChunks chunks take the kernel below it,
-// which reads them three times.
+// keeps it in registers; rows over kLnMaxChunks chunks, and rows of fewer than 8
+// values, take the kernel below it, which reads them three times.
 #include "block_device.hpp"
 
 namespace bitlinear {
@@ -28,7 +28,9 @@ constexpr int kLnWavesPerSimd = NC == 1 ? 8 : 4;
 // on the current one, and keeps weight and bias in registers (NC <= 2), so that
 // nothing but that load is waited for; with NC = 4 the weight lies in LDS and the
 // bias is read again (2048x28672, against both read again: float32 106 -> 97 us,
-// bfloat16 52 -> 46; 5% slower where a team has one row).  WHOLE: K is a multiple of 8.
+// bfloat16 52 -> 46; 5% slower where a team has one row).  8192x8192 bfloat16:
+// 43 us, 6.3 TB/s; with the 8-bit copy 61 us, 5.6 TB/s.
+// WHOLE: K is a multiple of 8.
 template <int XT, int YT, bool SAVE, int W, int NC, bool WHOLE>
 __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void layer_norm_kernel(
     const char* __restrict__ X, const float* __restrict__ x_scales, int64_t M, int K, int cpr,
@@ -140,8 +142,9 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void lay
   }
 }
 
-// Long rows, and rows of fewer than 8 (SHORT): one workgroup per row, rows gridDim.x apart; the row is read from memory
-// (the caches after the first time) for the mean, the variance and the output.
+// Long rows, and rows of fewer than 8 values (SHORT): one workgroup per row,
+// rows gridDim.x apart; the row is read from memory (the caches after the first
+// time) for the mean, the variance and the output.
 template <int XT, int YT, bool SAVE, bool SHORT>
 __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     const char* __restrict__ X, const float* __restrict__ x_scales, int64_t M, int K, int cpr,
@@ -214,7 +217,8 @@ void launch_held(const Args& a, hipStream_t stream) {
   constexpr int64_t most = 256 * (4 * kLnWavesPerSimd<NC> / (W > 1 ? W : 4));  // workgroups that 256 CUs hold
   const int64_t wgs = (a.M + T - 1) / T, turns = (wgs + most - 1) / most;
   const int64_t blocks = (wgs + turns - 1) / turns;  // as many turns for each
-  auto kernel = a.K % 8 == 0 ? layer_norm_kernel<XT, YT, SAVE, W, NC, true> : layer_norm_kernel<XT, YT, SAVE, W, NC, false>;
+  auto kernel = a.K % 8 == 0 ? layer_norm_kernel<XT, YT, SAVE, W, NC, true>
+                             : layer_norm_kernel<XT, YT, SAVE, W, NC, false>;
   kernel<<<static_cast<unsigned>(blocks), W > 1 ? 64 * W : 256, 0, stream>>>(
       static_cast<const char*>(a.X.p), a.X.scales, a.M, static_cast<int>(a.K), static_cast<int>(padded_k(a.K) / 8),
       a.weight, a.bias, a.eps, static_cast<char*>(a.Y), a.mean, a.rstd, a.saved, a.saved_scales);

@@ -27,9 +27,9 @@ __device__ __forceinline__ float relu(float h) { return h <= 0.0f ? 0.0f : h; }
 // takes runs of kRun consecutive workgroups, 2 MiB of float32, so that it
 // streams through memory: 8192x28672, save 203 -> 192 us, ReLU^2 325 -> 315, its
 // backward 284 -> 274; nothing on arrays below 2048x11008; runs of 4, 1024 or
-// 4096 are slower than none.  Two or four chunks to a thread, loaded first, are 1% to
-// 35% slower there and slower still on small arrays; total is 32 bits (at most
-// 2^31 chunks to a launch) because a 64-bit division takes about as many
+// 4096 are slower than none.  Two or four chunks to a thread, loaded first, are
+// 1% to 35% slower there and slower still on small arrays.  total is 32 bits (at
+// most 2^31 chunks to a launch) because a 64-bit division takes about as many
 // instructions as the rest of a chunk (2048x4096 bf16: 3% to 8% slower).
 template <int OP, int IT, int OT, int DT, bool SAVE, bool SHORT>
 __global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in, const float* __restrict__ in_scales,
@@ -45,7 +45,8 @@ __global__ __launch_bounds__(256) void chunk_kernel(const char* __restrict__ in,
   const int c = static_cast<int>(i - row * static_cast<uint32_t>(cpr)), n = chunk_values(K, c);
   const int64_t m = row;
   float v[8];
-  chunk_f32<IT>(load_chunk<IT, SHORT>(in + (IT == kSaved8 ? m * Kp : m * K * kBytes<IT>), in_scales + m * G, K, c, n), v);
+  const char* from = in + (IT == kSaved8 ? m * Kp : m * K * kBytes<IT>);
+  chunk_f32<IT>(load_chunk<IT, SHORT>(from, in_scales + m * G, K, c, n), v);
   if constexpr (SAVE) save_chunk(v, codes + m * Kp, scales + m * G, c);
   if constexpr (OP == kRelu2) {
 #pragma unroll

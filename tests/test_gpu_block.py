@@ -168,6 +168,19 @@ def test_relu2_nan_stays():
     assert np.isnan(A[0]) and A[1:].tolist() == [0.0, 4.0, 0.0, np.inf, 0.0, 0.0]
 
 
+def test_relu2_small_and_large_values():
+    """Results below the normal range and above the largest value."""
+    H = np.array([[1e-19, 3e-20, 1e-22, 2e19, 1.5e19, 1e-30, 4e-21, 1.7e-19, 9e-20]], np.float32)
+    H = bf16_bits_to_f32(f32_to_bf16_bits(H))
+    with np.errstate(over="ignore", under="ignore"):
+        sq = H * H
+    for dt in ("f32", "bf16"):
+        for out in ("f32", "bf16"):
+            with np.errstate(over="ignore"):
+                ref = to_type(sq, out)
+            assert same_bits(np_of(bl.relu2(on_gpu(H, dt), out_dtype=DT[out])), ref), (dt, out)
+
+
 # ---- layer norm ---------------------------------------------------------------
 
 def depth(K):
@@ -208,7 +221,8 @@ def check_backward(dY, X, mean, rstd, w, dX, dw, db, odt):
         axh = np.abs(xh)
         tol = np.abs(rs) * (e1 + axh * e2 + 6 * U * (np.abs(g) + axh * c2 + c1)) + 2 * U * np.abs(rdx)
         inside(dX, rdx, tol + half_step(np.abs(rdx) + tol, odt), "dX")
-    for got, ref, mag, nm in ((dw, rdw, np.abs(dY * xh).sum(axis=0), "dweight"), (db, rdb, np.abs(dY).sum(axis=0), "dbias")):
+    for got, ref, mag, nm in ((dw, rdw, np.abs(dY * xh).sum(axis=0), "dweight"),
+                              (db, rdb, np.abs(dY).sum(axis=0), "dbias")):
         if got is None:
             continue
         inside(got, ref, (M + 16) * U * mag, nm)
