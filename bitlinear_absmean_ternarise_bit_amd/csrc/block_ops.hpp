@@ -68,12 +68,15 @@ inline LnBwdPlan ln_bwd_plan(int64_t M, int64_t K, bool params) {
   return p;
 }
 
-// Partial rows of dweight and dbias; none where one workgroup writes the
-// gradients themselves.
+// One workgroup goes through all rows (rows of fewer than 8 values are one
+// workgroup of the column kernel): it writes the gradients themselves.
+inline bool ln_bwd_alone(const LnBwdPlan& p, int64_t K) { return p.groups == 1 && (p.waves > 0 || K < 8); }
+
+// Partial rows of dweight and dbias.
 inline size_t ln_bwd_workspace_bytes(int64_t M, int64_t K) {
   if (!size_args_ok(M) || !size_args_ok(K)) return 0;
   const LnBwdPlan p = ln_bwd_plan(M, K, true);
-  if (p.waves > 0 && p.groups == 1) return 0;
+  if (ln_bwd_alone(p, K)) return 0;
   return align256(size_mul(size_t(p.groups), size_mul(size_t(K), 8)));
 }
 

@@ -247,7 +247,7 @@ template <int XT, int DT, bool SHORT>
 __global__ __launch_bounds__(256) void ln_param_cols_kernel(
     const char* __restrict__ dY, const char* __restrict__ X, const float* __restrict__ x_scales,
     const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t M, int K, int cpr,
-    float* __restrict__ partial) {
+    float* __restrict__ dw_out, float* __restrict__ db_out, int64_t out_stride) {
   __shared__ float sums[8][32 * 8];
   const int tid = threadIdx.x, cl = tid & 31, r = tid >> 5;
   const int c = blockIdx.x * 32 + cl;
@@ -266,9 +266,10 @@ __global__ __launch_bounds__(256) void ln_param_cols_kernel(
       dw[e] = __fmaf_rn(d[e], (xh[e] - mean) * rstd, dw[e]);
     }
   }
-  float* out = partial + static_cast<int64_t>(blockIdx.y) * 2 * K;
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
+    float* out = a ? db_out : dw_out;
+    if (!out) continue;
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[r][cl * 8 + e] = a ? db[e] : dw[e];
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(256) void ln_param_cols_kernel(
       float t = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) t += sums[i][tid];
-      out[a * K + k] = t;
+      out[blockIdx.y * out_stride + k] = t;
     }
   }
 }
@@ -323,16 +324,23 @@ struct Args {
   float* partial;
 };
 
+// Where a kernel's sums go: the partial rows, or the gradients themselves.
+float* dweight_to(const Args& a, const LnBwdPlan& p) {
+  return !a.dweight ? nullptr : ln_bwd_alone(p, a.K) ? a.dweight : a.partial;
+}
+float* dbias_to(const Args& a, const LnBwdPlan& p) {
+  return !a.dbias ? nullptr : ln_bwd_alone(p, a.K) ? a.dbias : a.partial + a.K;
+}
+
 template <int XT, int DT, int OT, int W, int NC, int THREADS = 1024, bool PARAMS = true>
 void launch_one(const Args& a, const LnBwdPlan& p, hipStream_t stream) {
   const int64_t K = a.K;
-  const bool only = p.groups == 1;  // its sums are the gradients
   auto kernel = K % 8 == 0 ? ln_backward_kernel<XT, DT, OT, W, NC, THREADS, PARAMS, true>
                            : ln_backward_kernel<XT, DT, OT, W, NC, THREADS, PARAMS, false>;
   kernel<<<p.groups, 64 * W * p.teams, 0, stream>>>(
       static_cast<const char*>(a.dY), static_cast<const char*>(a.X.p), a.X.scales, a.mean, a.rstd, a.M,
       static_cast<int>(K), static_cast<int>(padded_k(K) / 8), a.weight, static_cast<char*>(a.dX),
-      !a.dweight ? nullptr : only ? a.dweight : a.partial, !a.dbias ? nullptr : only ? a.dbias : a.partial + K, 2 * K);
+      dweight_to(a, p), dbias_to(a, p), 2 * K);
 }
 
 template <int XT, int DT, int OT>
@@ -354,7 +362,7 @@ hipError_t launch(const Args& a, hipStream_t stream) {
     if (a.dweight || a.dbias) {
       auto kernel = K < 8 ? ln_param_cols_kernel<XT, DT, true> : ln_param_cols_kernel<XT, DT, false>;
       kernel<<<dim3((cpr + 31) / 32, p.groups), 256, 0, stream>>>(dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr,
-                                                                  a.partial);
+                                                                  dweight_to(a, p), dbias_to(a, p), 2 * a.K);
     }
   } else if (p.chunks == 1) {
     if (p.waves == 1) launch_one<XT, DT, OT, 1, 1>(a, p, stream);
@@ -366,7 +374,7 @@ hipError_t launch(const Args& a, hipStream_t stream) {
     if (p.chunks == 3) launch_one<XT, DT, OT, 8, 3, 512>(a, p, stream);
     else launch_one<XT, DT, OT, 8, 4, 512>(a, p, stream);
   }
-  if ((a.dweight || a.dbias) && (p.groups > 1 || p.waves == 0))
+  if ((a.dweight || a.dbias) && !ln_bwd_alone(p, a.K))
     ln_param_sum_kernel<<<dim3((K + 63) / 64, 2), 1024, 0, stream>>>(a.partial, p.groups, K, a.dweight, a.dbias);
   return hipGetLastError();
 }

@@ -174,7 +174,7 @@ int main() {
                p.teams >= 1 && (p.groups == 256 || int64_t(p.groups) * p.teams * (params ? 2 : 1) >= M);
         CHECK(ok);
         const size_t w = bitlinear_layer_norm_backward_workspace_bytes(M, K);
-        if (params) CHECK(p.waves > 0 && p.groups == 1 ? w == 0 : w >= size_t(p.groups) * 8 * K);
+        if (params) CHECK(ln_bwd_alone(p, K) ? w == 0 : w >= size_t(p.groups) * 8 * K);
       }
   printf("%d checks, %d failed\n", g_run, g_failed);
   return g_failed != 0;
