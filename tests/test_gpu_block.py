@@ -610,6 +610,17 @@ def test_binding_refusals():
         bl.layer_norm_backward(Z, Z.clone(), st, st.clone(), workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
 
 
+def test_saved_pair_refusals():
+    codes, scales = saved = bl.save_activations(torch.zeros((4, 100), device=DEV))
+    for pair, K in (((codes[0, 0].clone(), scales), 100), ((codes[0], scales), 100), ((codes[:0], scales[:0]), 100),
+                    (saved, 0), (saved, -10), (saved, 64), ((codes.float(), scales), 100), ((codes, scales.double()), 100),
+                    ((codes, scales[0]), 100), ((codes.cpu(), scales), 100), ((codes, scales.cpu()), 100),
+                    ((codes,), 100), ((codes, scales, scales), 100), ((codes[:, :64], scales[:, :1]), 64)):
+        for call in (bl.restore_activations, bl.relu2, lambda x, K: bl.layer_norm(x, K=K)):
+            with pytest.raises(ValueError):
+                call(pair, K)
+
+
 # ---- together, as a block trains ------------------------------------------------------
 
 def test_block_training_step():
