@@ -72,6 +72,27 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_resource(const void* row, 
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every resource
 
+// Chunk first + c of a row of a multiple of 8 values, zeros behind it.  `first`
+// is the same for a wave's lanes: it moves the resource, and chunks at several
+// of them share a lane's offset.
+template <int DT>
+__device__ __forceinline__ Raw<DT> fetch_whole(const char* row, const float* scales, int K, int cpr, int first, int c) {
+  Raw<DT> r;
+  const int bytes = (DT == kSaved8 ? cpr * 8 : K * kBytes<DT>) - first * 8 * kBytes<DT>;
+  const __amdgpu_buffer_rsrc_t from = row_resource(row + first * 8 * kBytes<DT>, max(bytes, 0));
+  if constexpr (DT == kSaved8) {
+    r.a = __builtin_amdgcn_raw_buffer_load_b64(from, 8 * c, 0, 0);
+    const __amdgpu_buffer_rsrc_t sc = row_resource(scales + (first >> 3), max(cpr - first, 0) / 2);
+    r.scale = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sc, c >> 3 << 2, 0, 0));
+  } else if constexpr (DT == kBf16) {
+    r.a = __builtin_amdgcn_raw_buffer_load_b128(from, 16 * c, 0, 0);
+  } else {
+    r.a = __builtin_amdgcn_raw_buffer_load_b128(from, 32 * c, 0, 0);
+    r.b = __builtin_amdgcn_raw_buffer_load_b128(from, 32 * c + 16, 0, 0);
+  }
+  return r;
+}
+
 // Chunk c of the row of K >= 8 values at `row` as it lies in memory, for any c.
 // `scales`: the row's scales (kSaved8, whose rows are padded with zero codes).
 // Nothing is conditional, so a loop that loads its next row ahead waits for
@@ -84,16 +105,7 @@ template <int DT, bool WHOLE>
 __device__ __forceinline__ Raw<DT> fetch_chunk(const char* row, const float* scales, int K, int cpr, int c) {
   Raw<DT> r;
   if constexpr (WHOLE) {
-    const __amdgpu_buffer_rsrc_t from = row_resource(row, DT == kSaved8 ? cpr * 8 : K * kBytes<DT>);
-    if constexpr (DT == kSaved8) {
-      r.a = __builtin_amdgcn_raw_buffer_load_b64(from, 8 * c, 0, 0);
-      r.scale = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row_resource(scales, cpr / 2), c >> 3 << 2, 0, 0));
-    } else if constexpr (DT == kBf16) {
-      r.a = __builtin_amdgcn_raw_buffer_load_b128(from, 16 * c, 0, 0);
-    } else {
-      r.a = __builtin_amdgcn_raw_buffer_load_b128(from, 32 * c, 0, 0);
-      r.b = __builtin_amdgcn_raw_buffer_load_b128(from, 32 * c + 16, 0, 0);
-    }
+    r = fetch_whole<DT>(row, scales, K, cpr, 0, c);
   } else if constexpr (DT == kSaved8) {
     const uint32_t at = static_cast<uint32_t>(min(c, cpr - 1));
     r.a = *reinterpret_cast<const v2u*>(row + 8u * at);

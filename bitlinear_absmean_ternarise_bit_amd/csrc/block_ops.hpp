@@ -22,28 +22,36 @@ struct BlockIn {
 };
 
 // How layer norm's backward pass is cut up.  Rows of at most kLnBwdMaxChunks
-// chunks of 8 (K <= 32768) go through one kernel: `waves` waves to a row,
+// chunks of 8 (K <= 16384) go through one kernel: `waves` waves to a row,
 // `chunks` chunks to a lane, `teams` rows at a time in a workgroup, `groups`
 // workgroups.  K <= 8192: one chunk to a lane, as many waves as that takes, 16
-// in a workgroup.  Longer: 8 waves with 3, 4 or 8 chunks to a lane, alone in the
-// workgroup, which leaves each lane 256 registers; with 8 the row is not held
-// between its two passes.
+// in a workgroup.  Longer: 8 waves with 3 or 4 chunks to a lane, alone in the
+// workgroup, which leaves each lane 256 registers; with 7 (kLnLongChunks) a
+// kernel of its own.
 // About one workgroup to each of the 256 CUs: the parameter gradients leave as
 // one partial row from each, and more of them would cost more than they hide.
 // So few rows that one workgroup takes them in two turns are left to one: it
 // writes the gradients itself, and the second launch (about as long as a turn)
 // is saved.
-// Longer rows still, and rows of fewer than 8 values (waves = 0): `groups` sets
-// of rows for the column kernel, 32 chunks of columns to a workgroup, about
-// 1024 workgroups.
+// waves = 0 (rows that neither kernel takes): `groups` sets of rows for the
+// column kernel, 32 chunks of columns to a workgroup, about 1024 workgroups.
 struct LnBwdPlan {
   int waves, chunks, teams, groups;
 };
 constexpr int64_t kLnBwdMaxChunks = 2048;
+// Rows of up to 28672, 8 waves of 7 chunks to a lane: dx, and with many rows of
+// a multiple of 8 values dweight and dbias as well.  That saves a second read of
+// x and dy but makes 256 partial rows: even at M (bytes of x + bytes of dy) =
+// 256 * 16, 512 rows in float32 and 1024 in bfloat16 (20480 columns, M = 512 and
+// 1024: float32 45 -> 42 and 85 -> 66 us, bfloat16 27 -> 31 and 44 -> 45).
+constexpr int kLnLongChunks = 7;
+constexpr int64_t kLnLongMaxChunks = kLnLongChunks * 512, kLnLongMinRows = 768;
 
 inline LnBwdPlan ln_bwd_plan(int64_t M, int64_t K, bool params) {
   const int64_t cpr = padded_k(K) / 8;
   LnBwdPlan p = {0, 1, 1, 1};
+  if (params && cpr > kLnBwdMaxChunks && cpr <= kLnLongMaxChunks && K % 8 == 0 && M >= kLnLongMinRows)
+    return {8, kLnLongChunks, 1, 256};
   if (cpr > kLnBwdMaxChunks || K < 8) {
     int64_t s = 1024 / ((cpr + 31) / 32);
     if (s > 256) s = 256;

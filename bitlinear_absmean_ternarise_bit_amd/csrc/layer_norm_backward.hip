@@ -5,10 +5,11 @@
 // in float32, from x as it was or from its 8-bit copy.  Bound by the bytes of
 // x, dy and dx: ln_backward_kernel reads each row once and keeps it in
 // registers between the row's sums and its dx, with the columns' dw and db in
-// registers across all of a workgroup's rows.  For rows over kLnBwdMaxChunks
-// chunks it gives dx alone, and a column kernel reads x and dy again for dw and
-// db; over kLnDxMaxChunks, and for rows of fewer than 8 values, dx comes from a
-// kernel that reads each row twice.
+// registers across all of a workgroup's rows.  Rows over kLnBwdMaxChunks chunks
+// take ln_backward_long_kernel, which keeps dw in LDS; where it does not apply
+// the first kernel gives dx alone, and a column kernel reads x and dy again for
+// dw and db; over kLnLongMaxChunks, and for rows of fewer than 8 values, dx
+// comes from a kernel that reads each row twice.
 #include "block_device.hpp"
 
 namespace bitlinear {
@@ -189,6 +190,116 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
   }
 }
 
+// Long rows of a multiple of 8 values, all three gradients from one pass over x
+// and dy: 8 waves, 7 chunks to a lane, a workgroup to each CU.  What does not
+// fit into registers beside dy and x: dw and two of a lane's 7 chunks of db lie
+// in LDS (144 KB; a lane adds to its own columns alone, 16 bytes at a time), the
+// weight is read again from the cache, a chunk ahead, and x stays as it is in
+// memory until its xhat is needed, twice.  The next row's chunk is loaded where
+// this row's has been stored.  2048x28672: float32 163 us, 8-bit x (dy float32,
+// dx bfloat16) 106; with all of db in registers, which spill, 193 and 120; the
+// two passes that it replaces 227 and 147.  8192x28672 from 8 bits 334 us, 5.0
+// TB/s (522 in two passes).
+// The same kernel for rows of up to 16384 is 5% to 30% slower than the one above.
+template <int XT, int DT, int OT>
+__global__ __launch_bounds__(512) void ln_backward_long_kernel(
+    const char* __restrict__ dY, const char* __restrict__ X, const float* __restrict__ x_scales,
+    const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t M, int K, int cpr,
+    const float* __restrict__ weight, char* __restrict__ dX, float* __restrict__ dw_out, float* __restrict__ db_out,
+    int64_t out_stride) {
+  constexpr int NC = kLnLongChunks, kStep = 512, kInLds = 2;
+  __shared__ float slots[2][16];
+  __shared__ __align__(16) float sums_lds[(NC + kInLds) * kStep * 8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  const int64_t G = cpr >> 3, Kp = int64_t(cpr) * 8;
+  const float inv_k = 1.0f / static_cast<float>(K);
+  auto place = [&](int j, int half) { return ((j * 2 + half) * kStep + tid) * 4; };
+  float held_db[NC - kInLds][8];
+  auto dw = [&](int j, int e) -> float& { return sums_lds[place(j, e >> 2) + (e & 3)]; };
+  auto db = [&](int j, int e) -> float& {
+    return j < kInLds ? dw(NC + j, e) : held_db[j < kInLds ? 0 : j - kInLds][e];
+  };
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) db(j, e) = dw(j, e) = 0.0f;
+  Raw<XT> rx[NC];
+  Raw<DT> rd[NC];
+  auto load = [&](int64_t m, int j) {
+    // behind the last row: a row without values
+    const int k = m < M ? K : 0, cp = m < M ? cpr : 0;
+    m = m < M ? m : 0;
+    rd[j] = fetch_whole<DT>(dY + m * K * kBytes<DT>, nullptr, k, cp, j * kStep, tid);
+    rx[j] = fetch_whole<XT>(X + (XT == kSaved8 ? m * Kp : m * K * kBytes<XT>), x_scales + m * G, k, cp, j * kStep,
+                            tid);
+  };
+  auto weight_chunk = [&](int j, float (&w)[8]) {
+    if (weight) {
+      chunk_f32<kF32>(fetch_whole<kF32>(reinterpret_cast<const char*>(weight), nullptr, K, cpr, j * kStep, tid), w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+    }
+  };
+  const int64_t stride = gridDim.x;
+  // consecutive rows to an XCD, as above
+  const uint32_t b = gridDim.x % 8 == 0 ? (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+  int64_t m = b;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) load(m, j);
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    arrive(rd[j]);
+    arrive(rx[j]);
+  }
+  for (int turn = 0; m < M; m += stride, turn ^= 1) {
+    const float mu = mean_in[m], rs = rstd_in[m];
+    float g[NC][8], s[2] = {0.0f, 0.0f}, w[2][8];
+    weight_chunk(0, w[0]);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      if (j + 1 < NC) weight_chunk(j + 1, w[(j + 1) & 1]);
+      float xh[8];
+      chunk_f32<DT>(rd[j], g[j]);
+      chunk_f32<XT>(rx[j], xh);
+      const float mean = j * kStep + tid < K >> 3 ? mu : 0.0f;  // behind the row x is 0
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[e] = (xh[e] - mean) * rs;
+        db(j, e) += g[j][e];
+        dw(j, e) = __fmaf_rn(g[j][e], xh[e], dw(j, e));
+        g[j][e] *= w[j & 1][e];
+        s[0] += g[j][e];
+        s[1] = __fmaf_rn(g[j][e], xh[e], s[1]);
+      }
+    }
+    team_sum<8>(s, slots[turn], wave, lane);
+    const float k1 = rs * (s[0] * inv_k), k2 = rs * (s[1] * inv_k);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      float xh[8];
+      chunk_f32<XT>(rx[j], xh);
+      const float mean = j * kStep + tid < K >> 3 ? mu : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        g[j][e] = __fmaf_rn(-k2, (xh[e] - mean) * rs, __fmaf_rn(rs, g[j][e], -k1));
+      const int at = j * kStep * 8 * kBytes<OT>, bytes = dX ? max(K * kBytes<OT> - at, 0) : 0;
+      put_chunk<OT, true>(row_resource(dX + (bytes ? m * K * kBytes<OT> + at : 0), bytes), tid, 8, g[j]);
+      load(m + stride, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    float v[8], u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = dw(j, e), u[e] = db(j, e);
+    const int c = j * kStep + tid, n = c < K >> 3 ? 8 : 0;
+    if (dw_out) store_chunk<kF32>(reinterpret_cast<char*>(dw_out + blockIdx.x * out_stride), c, n, v);
+    if (db_out) store_chunk<kF32>(reinterpret_cast<char*>(db_out + blockIdx.x * out_stride), c, n, u);
+  }
+}
+
 // dx of long rows, and of rows of fewer than 8 values (SHORT): one workgroup per
 // row, rows gridDim.x apart; the row is read for the two sums and again for the
 // output.
@@ -311,8 +422,6 @@ __global__ __launch_bounds__(1024) void ln_param_sum_kernel(const float* __restr
   }
 }
 
-constexpr int kLnDxMaxChunks = 7 * 512;  // K <= 28672: 8 waves hold a row for dx alone
-
 struct Args {
   const void* dY;
   BlockIn X;
@@ -347,12 +456,16 @@ template <int XT, int DT, int OT>
 hipError_t launch(const Args& a, hipStream_t stream) {
   const int cpr = static_cast<int>(padded_k(a.K) / 8), K = static_cast<int>(a.K);
   const LnBwdPlan p = ln_bwd_plan(a.M, a.K, a.dweight || a.dbias);
-  if (p.waves == 0) {
-    const char* dY = static_cast<const char*>(a.dY);
-    const char* X = static_cast<const char*>(a.X.p);
-    if (a.dX && K >= 8 && cpr <= kLnDxMaxChunks) {
-      const LnBwdPlan dx = {8, 7, 1, static_cast<int>(a.M < 256 ? a.M : 256)};
-      launch_one<XT, DT, OT, 8, 7, 512, false>(a, dx, stream);
+  const char* dY = static_cast<const char*>(a.dY);
+  const char* X = static_cast<const char*>(a.X.p);
+  if (p.chunks == kLnLongChunks) {
+    ln_backward_long_kernel<XT, DT, OT><<<p.groups, 512, 0, stream>>>(
+        dY, X, a.X.scales, a.mean, a.rstd, a.M, K, cpr, a.weight, static_cast<char*>(a.dX), dweight_to(a, p),
+        dbias_to(a, p), 2 * a.K);
+  } else if (p.waves == 0) {
+    if (a.dX && K >= 8 && cpr <= kLnLongMaxChunks) {
+      const LnBwdPlan dx = {8, kLnLongChunks, 1, static_cast<int>(a.M < 256 ? a.M : 256)};
+      launch_one<XT, DT, OT, 8, kLnLongChunks, 512, false>(a, dx, stream);
     } else if (a.dX) {
       const unsigned blocks = static_cast<unsigned>(a.M < (1 << 20) ? a.M : (1 << 20));
       auto kernel = K < 8 ? ln_dx_rows_kernel<XT, DT, OT, true> : ln_dx_rows_kernel<XT, DT, OT, false>;

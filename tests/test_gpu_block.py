@@ -298,6 +298,24 @@ def test_layer_norm_many_rows(M, K):
     assert all(torch.equal(a, b) for a, b in zip(again, (dX, dw, db)))
 
 
+@pytest.mark.parametrize("xdt,ddt,odt", [("f32", "f32", "f32"), ("bf16", "bf16", "bf16"), ("s8", "f32", "bf16"),
+                                         ("s8", "bf16", "f32"), ("bf16", "f32", "bf16"), ("f32", "bf16", "bf16")])
+@pytest.mark.parametrize("M,K", [(256, 16392), (767, 20000), (768, 16392), (770, 28672), (1030, 16448), (900, 20004)])
+def test_layer_norm_backward_many_long_rows(M, K, xdt, ddt, odt):
+    say(f"layer_norm_backward long rows M={M} K={K} {xdt} {ddt} {odt}")
+    g = torch.Generator(device=DEV).manual_seed(M + K)
+    X = torch.randn((M, K), generator=g, device=DEV).to(DT["f32" if xdt == "s8" else xdt])
+    dY = torch.randn((M, K), generator=g, device=DEV).to(DT[ddt])
+    w = 1 + 0.3 * torch.randn(K, generator=g, device=DEV)
+    _, mean, rstd, saved = bl.layer_norm(X, w, save=True)
+    x = saved if xdt == "s8" else X
+    xk = np_of(bl.restore_activations(saved, K) if xdt == "s8" else X)
+    dX, dw, db = bl.layer_norm_backward(dY, x, mean, rstd, w, out_dtype=DT[odt])
+    check_backward(np_of(dY), xk, np_of(mean), np_of(rstd), w.cpu().numpy(), np_of(dX), np_of(dw), np_of(db), odt)
+    again = bl.layer_norm_backward(dY, x, mean, rstd, w, out_dtype=DT[odt])
+    assert all(torch.equal(a, b) for a, b in zip(again, (dX, dw, db)))
+
+
 def test_layer_norm_large_offset_and_eps():
     """Rows far from zero (the two-pass variance) and eps as it is given."""
     rng = np.random.default_rng(0)
@@ -332,11 +350,12 @@ def test_statistics_stay_with_their_row(K):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("K", [6, 10, 100, 104, 4100, 5000, 20000, 20004, 33000])
-def test_layer_norm_backward_large_constant_rows(K, dt):
+@pytest.mark.parametrize("M,K", [(3, 6), (3, 10), (3, 100), (3, 104), (3, 4100), (3, 5000), (3, 20000), (3, 20004),
+                                 (3, 33000), (800, 16400), (800, 28664)])
+def test_layer_norm_backward_large_constant_rows(M, K, dt):
     """mean * rstd past the largest float32, xhat = 0: dX = rstd (dY - mean of dY), here rstd dY.
     Nothing rounds: the sums over dY = +1, -1, ... are sums of small integers."""
-    M, top, rs = 3, 2.0 ** 118, 2.0 ** 17
+    top, rs = 2.0 ** 118, 2.0 ** 17
     X = torch.full((M, K), top, device=DEV, dtype=DT[dt])
     dY = torch.ones((M, K), device=DEV)
     dY[:, 1::2] = -1
@@ -475,7 +494,7 @@ def test_more_rows_than_one_launch_takes():
     assert abs(float(db) - float(tail.double().sum())) <= 2000 * U * float(tail.double().abs().sum())
 
 
-@pytest.mark.parametrize("M,K", [(3, 100), (400, 520), (90, 9000), (40, 20000)])
+@pytest.mark.parametrize("M,K", [(3, 100), (400, 520), (90, 9000), (40, 20000), (270, 20000), (1000, 28672)])
 def test_gradients_one_at_a_time(M, K):
     """dX, dweight and dbias each alone, through the C ABI, equal the call for all three."""
     lib, g = abi.load(), torch.Generator(device=DEV).manual_seed(M)
