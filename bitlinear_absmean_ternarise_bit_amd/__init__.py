@@ -537,38 +537,41 @@ def _block():
     return _BLOCK
 
 
-def _plain_dtype(dtype, name):
-    d = _block().plain.get(dtype)
+def _plain_dtype(B, dtype, name):
+    d = B.plain.get(dtype)
     if d is None:
         raise ValueError(f"{name} must be float32 or bfloat16")
     return d
 
 
-def _matrix(t, name):
+def _matrix(B, t, name):
     """Checks a contiguous GPU [M, K] tensor; its abi dtype, M and K."""
-    _require_cuda(t, name)
-    if t.dim() != 2 or t.numel() == 0:
+    if not (t.is_cuda and t.is_contiguous()):
+        _require_cuda(t, name)
+    shape = t.shape
+    if len(shape) != 2 or t.numel() == 0:
         raise ValueError(f"{name} must be [M, K] with at least one value")
-    M, K = t.shape
-    return _plain_dtype(t.dtype, name), M, K
+    M, K = shape
+    return _plain_dtype(B, t.dtype, name), M, K
 
 
-def _vector(t, n, device, name):
+def _vector(B, t, n, device, name):
     """The address of a float32 tensor of n values on `device` (None: 0)."""
     if t is None:
         return 0
-    _require_cuda(t, name)
-    if t.dtype != _block().f32 or t.numel() != n:
+    if not (t.is_cuda and t.is_contiguous()):
+        _require_cuda(t, name)
+    if t.dtype != B.f32 or t.numel() != n:
         raise ValueError(f"{name} must hold {n} float32 values")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} is on another device")
     return t.data_ptr()
 
 
-def _whole_or_saved(x, K, name, M=None):
+def _whole_or_saved(B, x, K, name, M=None):
     """(data address, scales address, abi dtype, M, K, device) of a [M, K] tensor or a saved pair."""
     if not isinstance(x, (tuple, list)):
-        dt, m, k = _matrix(x, name)
+        dt, m, k = _matrix(B, x, name)
         if (K is not None and k != K) or (M is not None and m != M):
             raise ValueError(f"{name} does not have the other arrays' shape")
         return x.data_ptr(), 0, dt, m, k, x.device
@@ -577,7 +580,6 @@ def _whole_or_saved(x, K, name, M=None):
         raise ValueError(f"K is needed where {name} is saved in 8 bits")
     _require_cuda(codes, name + " codes")
     _require_cuda(scales, name + " scales")
-    B = _block()
     groups = (K + 63) // 64
     if codes.dtype != B.i8 or codes.dim() != 2 or codes.numel() == 0 or codes.shape[1] != 64 * groups:
         raise ValueError(f"{name} codes must be int8 [M, padded_k(K)]")
@@ -591,20 +593,19 @@ def _whole_or_saved(x, K, name, M=None):
     return codes.data_ptr(), scales.data_ptr(), abi.SAVED8, m, K, codes.device
 
 
-def _output(out, M, K, dtype, device, like=None):
+def _output(B, out, M, K, dtype, device, like=None):
     """`out`, checked, or a new [M, K] tensor (`like`: one of that shape on that device)."""
     if out is None:
         if like is not None and like.dtype == dtype:
-            return _block().empty_like(like)
-        return _block().empty(M, K, dtype=dtype, device=device)
+            return B.empty_like(like)
+        return B.empty(M, K, dtype=dtype, device=device)
     _require_cuda(out, "out")
     if out.shape != (M, K) or out.dtype != dtype or out.device != device:
         raise ValueError(f"out must be {dtype} [{M}, {K}] on {device}")
     return out
 
 
-def _empty_saved(M, K, device):
-    B = _block()
+def _empty_saved(B, M, K, device):
     groups = (K + 63) // 64
     return (B.empty(M, 64 * groups, dtype=B.i8, device=device),
             B.empty(M, groups, dtype=B.f32, device=device))
@@ -612,22 +613,22 @@ def _empty_saved(M, K, device):
 
 def save_activations(X):
     """X (float32 or bfloat16 [M, K]) in 8 bits: the pair (codes, scales)."""
-    B = _block()
-    dt, M, K = _matrix(X, "X")
+    B = _BLOCK or _block()
+    dt, M, K = _matrix(B, X, "X")
     device = X.device
-    codes, scales = saved = _empty_saved(M, K, device)
+    codes, scales = saved = _empty_saved(B, M, K, device)
     B.launch(B.save_activations, device, X.data_ptr(), dt, M, K, codes.data_ptr(), scales.data_ptr())
     return saved
 
 
 def restore_activations(saved, K: int, dtype=None, out=None):
     """The [M, K] values that ``saved`` stands for, as float32 (default) or bfloat16."""
-    B = _block()
-    codes, scales, _, M, K, device = _whole_or_saved(tuple(saved), K, "saved")
+    B = _BLOCK or _block()
+    codes, scales, _, M, K, device = _whole_or_saved(B, tuple(saved), K, "saved")
     if dtype is None:
         dtype = B.f32 if out is None else out.dtype
-    dt = _plain_dtype(dtype, "dtype")
-    X = _output(out, M, K, dtype, device)
+    dt = _plain_dtype(B, dtype, "dtype")
+    X = _output(B, out, M, K, dtype, device)
     B.launch(B.restore_activations, device, codes, scales, M, K, X.data_ptr(), dt)
     return X
 
@@ -640,16 +641,16 @@ def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, K: int | None = Non
     pair).  Returns Y; (Y, mean, rstd) with ``return_stats``, for :func:`layer_norm_backward`; and
     (Y, mean, rstd, saved) with ``save``, X in 8 bits from the same pass.
     """
-    B = _block()
-    x, xs, dt, M, K, device = _whole_or_saved(X, K, "X")
+    B = _BLOCK or _block()
+    x, xs, dt, M, K, device = _whole_or_saved(B, X, K, "X")
     like = None if xs else X
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else B.f32 if xs else X.dtype
-    ydt = _plain_dtype(out_dtype, "out_dtype")
-    w, b = _vector(weight, K, device, "weight"), _vector(bias, K, device, "bias")
+    ydt = _plain_dtype(B, out_dtype, "out_dtype")
+    w, b = _vector(B, weight, K, device, "weight"), _vector(B, bias, K, device, "bias")
     if save and xs:
         raise ValueError("X is saved already")
-    Y = _output(out, M, K, out_dtype, device, like)
+    Y = _output(B, out, M, K, out_dtype, device, like)
     if not (return_stats or save):
         B.launch(B.layer_norm, device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, 0, 0, 0, 0)
         return Y
@@ -659,7 +660,7 @@ def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, K: int | None = Non
         B.launch(B.layer_norm, device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mean.data_ptr(),
                  rstd.data_ptr(), 0, 0)
         return Y, mean, rstd
-    codes, scales = saved = _empty_saved(M, K, device)
+    codes, scales = saved = _empty_saved(B, M, K, device)
     B.launch(B.layer_norm, device, x, xs, dt, M, K, w, b, eps, Y.data_ptr(), ydt, mean.data_ptr(),
              rstd.data_ptr(), codes.data_ptr(), scales.data_ptr())
     return Y, mean, rstd, saved
@@ -672,25 +673,25 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, out_dtype=None, need_dx:
     ``X``: the forward's input, whole or as it was saved; ``mean``, ``rstd``: from the forward.  dX [M, K]
     is of ``out_dtype`` (default: dY's), dweight and dbias are float32 [K]; None where not needed.
     """
-    B = _block()
-    ddt, M, K = _matrix(dY, "dY")
+    B = _BLOCK or _block()
+    ddt, M, K = _matrix(B, dY, "dY")
     device = dY.device
-    x, xs, dt, _, _, xdev = _whole_or_saved(X, K, "X", M)
+    x, xs, dt, _, _, xdev = _whole_or_saved(B, X, K, "X", M)
     if xdev != device:
         raise ValueError("X is on another device")
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward are needed")
-    mp, rp = _vector(mean, M, device, "mean"), _vector(rstd, M, device, "rstd")
-    w = _vector(weight, K, device, "weight")
+    mp, rp = _vector(B, mean, M, device, "mean"), _vector(B, rstd, M, device, "rstd")
+    w = _vector(B, weight, K, device, "weight")
     if not (need_dx or need_dw):
         raise ValueError("nothing to compute")
     if out_dtype is None:
         out_dtype = dY.dtype
-    odt = _plain_dtype(out_dtype, "out_dtype")
+    odt = _plain_dtype(B, out_dtype, "out_dtype")
     dX = dw = db = None
     dxp = dwp = dbp = wsp = ws_bytes = 0
     if need_dx:
-        dX = _output(None, M, K, out_dtype, device, dY)
+        dX = _output(B, None, M, K, out_dtype, device, dY)
         dxp = dX.data_ptr()
     if need_dw:
         dw = B.empty(K, dtype=B.f32, device=device)
@@ -717,18 +718,18 @@ def relu2(H, K: int | None = None, out_dtype=None, save: bool = False, out=None)
     A is of ``out_dtype`` (default: H's; float32 for a saved pair).  With ``save`` returns (A, saved), H in
     8 bits from the same pass.
     """
-    B = _block()
-    h, hs, dt, M, K, device = _whole_or_saved(H, K, "H")
+    B = _BLOCK or _block()
+    h, hs, dt, M, K, device = _whole_or_saved(B, H, K, "H")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else B.f32 if hs else H.dtype
-    adt = _plain_dtype(out_dtype, "out_dtype")
+    adt = _plain_dtype(B, out_dtype, "out_dtype")
     if save and hs:
         raise ValueError("H is saved already")
-    A = _output(out, M, K, out_dtype, device, None if hs else H)
+    A = _output(B, out, M, K, out_dtype, device, None if hs else H)
     if not save:
         B.launch(B.relu2, device, h, hs, dt, M, K, A.data_ptr(), adt, 0, 0)
         return A
-    codes, scales = saved = _empty_saved(M, K, device)
+    codes, scales = saved = _empty_saved(B, M, K, device)
     B.launch(B.relu2, device, h, hs, dt, M, K, A.data_ptr(), adt, codes.data_ptr(), scales.data_ptr())
     return A, saved
 
@@ -738,15 +739,15 @@ def relu2_backward(dA, H, out_dtype=None, out=None):
 
     dH is of ``out_dtype`` (default: dA's; bfloat16 is what :func:`backward` takes).
     """
-    B = _block()
-    adt, M, K = _matrix(dA, "dA")
+    B = _BLOCK or _block()
+    adt, M, K = _matrix(B, dA, "dA")
     device = dA.device
-    h, hs, dt, _, _, hdev = _whole_or_saved(H, K, "H", M)
+    h, hs, dt, _, _, hdev = _whole_or_saved(B, H, K, "H", M)
     if hdev != device:
         raise ValueError("H is on another device")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else dA.dtype
-    odt = _plain_dtype(out_dtype, "out_dtype")
-    dH = _output(out, M, K, out_dtype, device, dA)
+    odt = _plain_dtype(B, out_dtype, "out_dtype")
+    dH = _output(B, out, M, K, out_dtype, device, dA)
     B.launch(B.relu2_backward, device, dA.data_ptr(), adt, h, hs, dt, M, K, dH.data_ptr(), odt)
     return dH
