@@ -99,7 +99,10 @@ int bitlinear_restore_activations(const int8_t* codes, const float* scales, int6
  *         BITLINEAR_SAVED8 input (BITLINEAR_ERR_ARG).
  *
  * Arithmetic in float32: the mean first, then the squares of the differences
- * to it; Y is rounded once at the end.
+ * to it; Y is rounded once at the end.  Rows whose mean is 32 or more standard
+ * deviations from 0 have it corrected by the sum of the differences, and
+ * variance and Y are those about the corrected mean (the one that is stored): a
+ * row of one value has that value as its mean and the bias as Y.
  * Errors: BITLINEAR_ERR_NULL (also one of a pair without the other), _SHAPE,
  * _DTYPE, _ALIGN, _ARG, _HIP.
  */

@@ -364,6 +364,54 @@ def test_layer_norm_backward_large_constant_rows(M, K, dt):
     assert torch.equal(dX, rs * dY) and not bool(dw.any()) and torch.equal(db, M * dY[0])
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [1, 5, 64, 300, 1003, 2048, 5633, 8200, 11008, 20004, 28672, 33000])
+def test_layer_norm_constant_rows(K, dt):
+    """A row of one value c has mean c, x - mean = 0 and rstd = 1 / sqrt(eps), whatever K c rounds to on the
+    way: Y is the bias and dweight 0, bit for bit.  rstd: the sum with eps, the root and the division round once
+    each (3 u, 4 allowed)."""
+    say(f"layer_norm constant rows K={K} {dt}")
+    c = np.array([3.0, 8000.0, 1.1, 8000.1, -1000.3, 1e-30, -123456.7, 0.0, 2.0 ** 60], np.float32)
+    X = on_gpu(np.repeat(c[:, None], K, axis=1), dt)
+    g = torch.Generator(device=DEV).manual_seed(K)
+    w, b = torch.randn(K, generator=g, device=DEV), torch.randn(K, generator=g, device=DEV)
+    dY = torch.randn((len(c), K), generator=g, device=DEV)
+    for eps in (1e-5, 1e-12):
+        rs = 1 / np.sqrt(float(np.float32(eps)))
+        Y, mean, rstd, saved = bl.layer_norm(X, w, b, eps, out_dtype=torch.float32, save=True)
+        assert torch.equal(mean, X[:, 0].float()) and torch.equal(Y, b.expand_as(Y))
+        inside(np_of(rstd), np.full(len(c), rs), 4 * U * rs, "rstd")
+        assert not bool(bl.layer_norm_backward(dY, X, mean, rstd, w)[1].any())
+        Ys, ms, _ = bl.layer_norm(saved, w, b, eps, K=K, return_stats=True)
+        assert torch.equal(ms, bl.restore_activations(saved, K)[:, 0]) and torch.equal(Ys, b.expand_as(Ys))
+
+
+@pytest.mark.parametrize("K", [300, 5633, 28672, 33000])
+def test_layer_norm_rows_far_from_zero(K):
+    """Rows of a large value plus 0 or a few of its float32 steps.  The stored mean is the nearest float32 but for the
+    sum of the differences (K / 64 + 32 roundings of their mean size) and one rounding of its own; Y and rstd are those
+    of the differences to the stored mean, each of which is exact."""
+    say(f"layer_norm far rows K={K}")
+    rng = np.random.default_rng(K)
+    top, eps = np.array([8192.0, -1e5, 2.0 ** 20, 3.0], np.float32), 1e-12
+    X = top[:, None] + np.spacing(np.abs(top))[:, None] * rng.integers(0, 5, (len(top), K)).astype(np.float32)
+    Y, mean, rstd = bl.layer_norm(on_gpu(X, "f32"), None, None, eps, return_stats=True)
+    X, m = X.astype(np.float64), np_of(mean).astype(np.float64)
+    off = np.abs(X - X.mean(axis=1, keepdims=True)).mean(axis=1)
+    # differences are at most 4 steps, to the first mean at most 4 + 2 (K / 64 + 32) / 2 of them: the sums are of
+    # numbers of that size
+    first = off + (depth(K) + 1) * U * np.abs(X).mean(axis=1)
+    inside(m, X.mean(axis=1), depth(K) * U * first + 1.001 * U * np.abs(m), "mean")
+    d = X - m[:, None]
+    var = (d * d).mean(axis=1)
+    wide = (d * d).mean(axis=1) + first * first  # what the sum of squares about the first mean can be
+    r = 1 / np.sqrt(var + float(np.float32(eps)))
+    lo = np.maximum(var - 4 * (depth(K) + 8) * U * wide, 0) + float(np.float32(eps))
+    inside(np_of(rstd), r, r * (np.sqrt((var + float(np.float32(eps))) / lo) - 1) + 4 * U * r, "rstd")
+    rs = np_of(rstd).astype(np.float64)[:, None]
+    inside(np_of(Y), d * rs, 2 * U * np.abs(d * rs), "Y")
+
+
 def test_layer_norm_gradient_by_differences():
     rng = np.random.default_rng(5)
     M, K, h = 3, 96, 2.0 ** -6
