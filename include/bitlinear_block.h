@@ -40,11 +40,12 @@
  *         s     = fp32(127 / amax)             (an IEEE division)
  *         code  = the integer nearest x * s    (the exact product, ties to even)
  *         x~    = fp32(scale * code)           (the value that is restored)
- * so |x~ - x| <= scale / 2 (1 + 2^-15) and |code| <= 127.  The scales follow
- * the group's own values: an outlier channel costs its 63 neighbours
- * resolution and nobody else.  A group whose amax is below 2^-100 is saved as
- * zeros; a group that holds an infinity or a NaN gets a NaN scale and is
- * restored as 64 NaNs, so a training loop's check for them still sees it.
+ * so |x~ - x| <= scale / 2 (1 + 2^-14) (the scale, s and x~ are rounded once
+ * each) and |code| <= 127.  The scales follow the group's own values: an
+ * outlier channel costs its 63 neighbours resolution and nobody else.  A group
+ * whose amax is below 2^-100 is saved as zeros (scale 0, off by amax at most);
+ * a group that holds an infinity or a NaN gets a NaN scale and is restored as 64
+ * NaNs, so a training loop's check for them still sees it.
  * As an input these arrays are dtype BITLINEAR_SAVED8: the codes are the data
  * pointer, the scales the *_scales pointer beside it (not read for the other
  * dtypes).

@@ -1,6 +1,8 @@
 """Pins of the oracle for the operators around BitLinear: layer norm against
 torch's float64 one and central differences, the saved format against its
 bounds, exact ties and a literal rendering with fractions."""
+import os
+import re
 from fractions import Fraction
 
 import numpy as np
@@ -8,6 +10,8 @@ import pytest
 import torch
 
 from oracle import block as B
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (4, 64), (2, 129)])
@@ -74,3 +78,28 @@ def test_saved_special_groups():
     T = np.zeros((1, 64), np.float32)
     T[0, :6] = [127, 0.5, 1.5, 2.5, -0.5, -2.5]
     assert B.save8(T)[0][0, :6].tolist() == [127, 0, 2, 2, 0, -2]
+
+
+def test_saved_bound_of_the_header():
+    """|x~ - x| <= scale / 2 (1 + 2^-14), where the roundings add up: values beside the borders between large codes.
+    With d0..d3 the relative errors of fp32(1/127) (2^-28), s, scale and x~ (2^-24 each) and r <= 1/2 the rounding of
+    x s:  x~ - x = x ((1 + d0)(1 + d1)(1 + d2)(1 + d3) - 1) + r scale (1 + d3)  and  |x| <= 127 scale (1 + 2^-23),
+    which is scale / 2 (1 + 2^-24 (1 + 254 * 3.07)) at most, below 1 + 2^-14 = 1 + 1024 * 2^-24."""
+    text = " ".join(open(os.path.join(ROOT, "include", "bitlinear_block.h")).read().replace("*", " ").split())
+    stated = re.search(r"\|x~ - x\| <= scale / 2 \(1 \+ 2\^-(\d+)\)", text)
+    assert stated
+    rng = np.random.default_rng(14)
+    n = 4000
+    amax = (rng.uniform(1, 2, n) * 2.0 ** rng.integers(-90, 120, n)).astype(np.float32)
+    amax[0] = float.fromhex("0x1.159004p+0")
+    X = np.zeros((n, 64), np.float32)
+    X[:, 0] = amax
+    s = (np.float32(127) / amax).astype(np.float64)
+    for j, code in enumerate(range(64, 127)):
+        border = ((code + 0.5) / s).astype(np.float32)
+        X[:, 1 + j] = np.nextafter(border, np.float32(np.inf if j % 2 else 0))
+    X[0, 1] = float.fromhex("0x1.1248c6p+0")
+    back = B.restore8(*B.save8(X), 64).astype(np.float64)
+    half = B.save8(X)[1].astype(np.float64) / 2
+    worst = (np.abs(back - X) / half - 1).max()
+    assert 2.0 ** -15 < worst <= 2.0 ** -int(stated.group(1)), worst * 2 ** 24
