@@ -6,7 +6,8 @@
  * products (and the status codes and dtypes used here).
  *
  * [PMV] is the produtoramaxvision.com.br blog article on BitNet b1.58: its
- * section on trade-offs keeps norms in floating point outside BitLinear.
+ * section on trade-offs keeps the norm, there RMSNorm, outside BitLinear.  The
+ * norm here is layer norm, with a mean and a bias; RMSNorm is not offered.
  * [MBC] is the shadowgraph.io page on a multimodal architecture around
  * bitnet.cpp: its bit_layers.py section gives ReLU^2 as BitNet's activation.
  *

@@ -6,10 +6,10 @@ formulas in float64 (float32 only where the saved format's definition says so);
 inputs are numpy arrays, outputs float64 and not rounded.
 
 [PMV] (the produtoramaxvision.com.br article on BitNet b1.58, its section on
-trade-offs) leaves the norm in floating point outside BitLinear; [MBC] (the
-shadowgraph.io page, bit_layers.py) gives ReLU^2 as the activation.  Neither
-says more about them: the norm is the ordinary layer norm, the saved format is
-this library's own.
+trade-offs) leaves the norm outside BitLinear and names RMSNorm; [MBC] (the
+shadowgraph.io page, bit_layers.py) gives ReLU^2 as the activation.  The norm
+here is another one, the ordinary layer norm (mean, biased variance, bias): the
+library's own choice, as the saved format is.
 """
 from __future__ import annotations
 
