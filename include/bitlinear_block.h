@@ -113,7 +113,8 @@ int bitlinear_layer_norm(const void* X, const float* x_scales, int x_dtype, int6
                          float* mean, float* rstd, int8_t* saved, float* saved_scales, void* stream);
 
 /* Workspace bytes of bitlinear_layer_norm_backward: partial sums of dweight
- * and dbias (at most 256 rows of 2 K float32; 0 for few rows). */
+ * and dbias (at most 256 rows of 2 K float32; 0 for few rows of at most 16384
+ * columns). */
 size_t bitlinear_layer_norm_backward_workspace_bytes(int64_t M, int64_t K);
 
 /*
@@ -147,7 +148,7 @@ int bitlinear_layer_norm_backward(const void* dY, int dy_dtype, const void* X, c
 /* ---- ReLU^2 ---------------------------------------------------------------- */
 /*
  * A = max(H, 0)^2: fp32(r * r), r = max(H, 0), as the FFN block forward's
- * hidden layer; a NaN stays a NaN.                                       [MBC]
+ * hidden layer, but for a NaN: it stays a NaN here (there it becomes 0). [MBC]
  *
  * H:      device [M, K], h_dtype BITLINEAR_F32, _BF16 or _SAVED8 (then
  *         h_scales: its scales).
