@@ -281,6 +281,28 @@ def test_layer_norm_backward(M, K, dt, ddt, odt):
         assert only_w[0] is None and torch.equal(only_w[1], dw) and torch.equal(only_w[2], db)
 
 
+@pytest.mark.parametrize("M,K", [(5, 7), (5, 67), (37, 1000), (9, 4096), (19, 11008), (3, 20000), (2, 33000)])
+def test_layer_norm_backward_every_mix(M, K):
+    """x whole in either type or saved, dY and dX in either type: twelve mixes."""
+    rng = np.random.default_rng(M * 19 + K)
+    w = (1 + 0.3 * rng.standard_normal(K)).astype(np.float32)
+    wd = torch.from_numpy(w).to(DEV)
+    for dt in ("f32", "bf16", "s8"):
+        X = stream_values(rng, M, K, "f32" if dt == "s8" else dt)
+        kept = on_gpu(X, "f32" if dt == "s8" else dt)
+        _, mean, rstd, saved = bl.layer_norm(kept, wd, None, 1e-5, save=True)
+        if dt == "s8":
+            kept, X = saved, B.restore8(saved[0].cpu().numpy(), saved[1].cpu().numpy(), K)
+        m, r = np_of(mean), np_of(rstd)
+        for ddt in ("f32", "bf16"):
+            dY = values(rng, (M, K), ddt, 1e-3)
+            for odt in ("f32", "bf16"):
+                say(f"layer_norm_backward M={M} K={K} {dt} {ddt} {odt}")
+                dX, dw, db = bl.layer_norm_backward(on_gpu(dY, ddt), kept, mean, rstd, wd, out_dtype=DT[odt])
+                assert dX.dtype == DT[odt]
+                check_backward(dY, X, m, r, w, np_of(dX), np_of(dw), np_of(db), odt)
+
+
 @pytest.mark.parametrize("M,K", [(4100, 264), (2500, 1024), (1500, 3000), (700, 8192)])
 def test_layer_norm_many_rows(M, K):
     """More rows than the card holds at once: dweight and dbias over every one of them."""
