@@ -40,10 +40,19 @@ struct LnBwdPlan {
 };
 constexpr int64_t kLnBwdMaxChunks = 2048;
 // Rows of up to 28672, 8 waves of 7 chunks to a lane: dx, and with many rows of
-// a multiple of 8 values dweight and dbias as well.  That saves a second read of
-// x and dy but makes 256 partial rows: even at M (bytes of x + bytes of dy) =
-// 256 * 16, 512 rows in float32 and 1024 in bfloat16 (20480 columns, M = 512 and
-// 1024: float32 45 -> 42 and 85 -> 66 us, bfloat16 27 -> 31 and 44 -> 45).
+// a multiple of 8 values dweight and dbias as well.  An eighth chunk does not
+// fit: dweight and two chunks of dbias in LDS are 144 KB of a CU's 160 with 7.
+// One pass saves a second read of x and dy but makes 256 partial rows, so it
+// gains with rows and with the bytes of a value.  Against two passes, us, at
+// 28672 and 16392 columns, M = 512, 768, 1024 and 2048 (types of x, dy, dx):
+//   f32 f32 f32      61/67  80/94  98/126  164/228   43/41  53/60  64/76  108/139
+//   8 bits f32 bf16  49/41  59/61  69/78   109/147   33/30  43/40  51/51   78/88
+//   bf16 bf16 bf16   45/35  54/51  62/68    98/127   30/27  38/33  46/42   69/75
+//   8 bits bf16 bf16 43/31  51/42  60/55    91/100   30/26  36/32  44/38   68/67
+// They are even at M (bytes of x + bytes of dy) of 4000 to 6500.  The rule is one
+// number of rows for all types: from 768 rows to that point it is up to 22%
+// slower than two passes where dy is bfloat16, up to 8% from 8 bits with dy
+// float32, and float32 rows below 768 miss up to 10%.
 constexpr int kLnLongChunks = 7;
 constexpr int64_t kLnLongMaxChunks = kLnLongChunks * 512, kLnLongMinRows = 768;
 

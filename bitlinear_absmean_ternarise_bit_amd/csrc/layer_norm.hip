@@ -53,9 +53,10 @@ constexpr int kLnWavesPerSimd = NC == 1 ? 8 : 4;
 // many teams as the card holds at once; each loads its next row before it works
 // on the current one, and keeps weight and bias in registers (NC <= 2), so that
 // nothing but that load is waited for; with NC = 4 the weight lies in LDS and the
-// bias is read again (2048x28672, against both read again: float32 106 -> 97 us,
-// bfloat16 52 -> 46; 5% slower where a team has one row).  8192x8192 bfloat16:
-// 43 us, 6.3 TB/s; with the 8-bit copy 61 us, 5.6 TB/s.
+// bias is read again (2048x28672, against both read again: float32 8% faster,
+// bfloat16 12%; 5% slower where a team has one row).  8192x8192 bfloat16: 49 us,
+// 5.4 TB/s, about 150 vector instructions for a wave's 512 columns, two thirds of
+// what the SIMDs issue in that time; with the 8-bit copy 63 us, 5.4 TB/s, 200.
 // WHOLE: K is a multiple of 8.
 template <int XT, int YT, bool SAVE, int W, int NC, bool WHOLE>
 __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void layer_norm_kernel(
@@ -186,7 +187,9 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256, kLnWavesPerSimd<NC>) void lay
 
 // Long rows, and rows of fewer than 8 values (SHORT): one workgroup per row,
 // rows gridDim.x apart; the row is read from memory (the caches after the first
-// time) for the mean, the variance and the output.
+// time) for the mean, the variance and the output.  That costs: 2048x53248
+// bfloat16 179 us, 2.4 TB/s of x and y once (2048x32768, held in registers, 56 us;
+// 2048x32776 105).
 template <int XT, int YT, bool SAVE, bool SHORT>
 __global__ __launch_bounds__(256) void layer_norm_rows_kernel(
     const char* __restrict__ X, const float* __restrict__ x_scales, int64_t M, int K, int cpr,

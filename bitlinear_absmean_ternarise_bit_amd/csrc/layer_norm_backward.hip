@@ -26,11 +26,14 @@ namespace {
 // partial row of each (the gradients themselves where it is the only one), so
 // no sum depends on the order in which anything runs.
 //
-// The vector ALU is the second bound: about 180 instructions for a wave's 512
-// columns are 7 TB/s at float32 dy and bfloat16 dx.  So dx is two FMAs,
-//   dx = rstd g - rstd c1 - xhat (rstd c2),   c1, c2 the sums over K,
-// and a value is converted once.  8192x8192, dy float32, dx bfloat16: from the
-// 8-bit copy 91 us (5.2 TB/s); all float32 147 us (5.5 TB/s).
+// dx is two FMAs,  dx = rstd g - rstd c1 - xhat (rstd c2),  c1, c2 the sums over
+// K, and a value is converted once: 125 (float32) to 150 (8-bit x) vector
+// instructions for a wave's 512 columns.  1024 SIMDs at 2.4 GHz and 4 clocks an
+// instruction issue 600 G of them a second, two to three times what the rates
+// here need.  8192x8192, dy float32, dx bfloat16: from the 8-bit copy 92 us (5.15
+// TB/s); all float32 147 us (5.5 TB/s).  Smaller arrays pay 4 to 6.5 us for the
+// teams' sums, the partial rows and their kernel: 2048x2048 from 8 bits 12.3
+// us, dx alone 7.3; 2048x4096 16.6 and 11.0.
 //
 // PARAMS false: dx alone, for rows whose dw and db do not fit beside them.
 // WHOLE: K is a multiple of 8.
@@ -197,9 +200,9 @@ __global__ __launch_bounds__(THREADS) void ln_backward_kernel(
 // weight is read again from the cache, a chunk ahead, and x stays as it is in
 // memory until its xhat is needed, twice.  The next row's chunk is loaded where
 // this row's has been stored.  2048x28672: float32 163 us, 8-bit x (dy float32,
-// dx bfloat16) 106; with all of db in registers, which spill, 193 and 120; the
-// two passes that it replaces 227 and 147.  8192x28672 from 8 bits 334 us, 5.0
-// TB/s (522 in two passes).
+// dx bfloat16) 108; with all of db in registers, which spill, 193 and 120; the
+// two passes that it replaces 228 and 147.  8192x28672 from 8 bits 337 us, 4.9
+// TB/s.
 // The same kernel for rows of up to 16384 is 5% to 30% slower than the one above.
 template <int XT, int DT, int OT>
 __global__ __launch_bounds__(512) void ln_backward_long_kernel(
@@ -302,7 +305,8 @@ __global__ __launch_bounds__(512) void ln_backward_long_kernel(
 
 // dx of long rows, and of rows of fewer than 8 values (SHORT): one workgroup per
 // row, rows gridDim.x apart; the row is read for the two sums and again for the
-// output.
+// output.  2048x32768 from 8 bits 159 us (2048x28672 in the kernels above 84),
+// 2048x53248 273, 2.8 TB/s of x, dy and dx once.
 template <int XT, int DT, int OT, bool SHORT>
 __global__ __launch_bounds__(256) void ln_dx_rows_kernel(
     const char* __restrict__ dY, const char* __restrict__ X, const float* __restrict__ x_scales,

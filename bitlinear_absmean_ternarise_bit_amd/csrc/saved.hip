@@ -22,8 +22,9 @@ __device__ __forceinline__ float relu(float h) { return h <= 0.0f ? 0.0f : h; }
 //   kRelu2:         in -> out (and codes, scales when SAVE)
 //   kRelu2Backward: dA, in -> out
 // SHORT: rows of fewer than 8 values.
-// Bound by HBM: 5.7 to 6.2 TB/s over arrays of 2048x11008 and larger (a copy of
-// 2 GiB reaches 4.9).  Workgroups are dealt round-robin to the 8 XCDs; each XCD
+// Bound by HBM: 5.8 to 6.2 TB/s over 8192x28672 float32, 5.2 to 5.9 over 8192x8192
+// bfloat16, 4.4 (restore) to 5.5 over 2048x11008 float32 (a copy reaches 4.9 to 5.1
+// with 2 and 1 GiB).  Workgroups are dealt round-robin to the 8 XCDs; each XCD
 // takes runs of kRun consecutive workgroups, 2 MiB of float32, so that it
 // streams through memory: 8192x28672, save 203 -> 192 us, ReLU^2 325 -> 315, its
 // backward 284 -> 274; nothing on arrays below 2048x11008; runs of 4, 1024 or
