@@ -126,7 +126,8 @@ size_t bitlinear_layer_norm_backward_workspace_bytes(int64_t M, int64_t K);
  * dY:     device [M, K], dy_dtype BITLINEAR_F32 (as bitlinear_backward writes
  *         its dX) or _BF16.
  * X, x_scales, x_dtype: the forward's input, whole or as it was saved in 8
- *         bits (BITLINEAR_SAVED8).
+ *         bits (BITLINEAR_SAVED8; xhat is then off by scale / 2 * rstd, so rows
+ *         that lie many standard deviations from 0 are better kept whole).
  * mean, rstd: device float32 [M], from the forward.
  * weight: device float32 [K], or NULL for none.
  * dX:     device [M, K], dx_dtype BITLINEAR_F32 or _BF16, or NULL.
