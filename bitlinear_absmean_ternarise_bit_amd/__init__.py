@@ -1,8 +1,8 @@
 """BitNet b1.58 BitLinear forward on MI355X (gfx950).
 
-A thin torch-facing binding over the C ABI in ``include/bitlinear.h`` and
-``include/bitlinear_block.h``: these functions only check and marshal arguments (device pointers, sizes, the
-current HIP stream); every step of the computation runs in the HIP kernels of
+A thin torch-facing binding over the C ABI in ``include/bitlinear.h``,
+``include/bitlinear_block.h`` and ``include/bitlinear_gated.h``: these functions
+only check and marshal arguments (device pointers, sizes, the current HIP stream); every step of the computation runs in the HIP kernels of
 ``libbitlinear.so``.  There is no CPU fallback: without the built library or a
 GPU the calls raise.
 
@@ -40,6 +40,10 @@ __all__ = [
     "layer_norm_backward",
     "relu2",
     "relu2_backward",
+    "gated_forward",
+    "gated_ffn_forward",
+    "gated_backward",
+    "gated_input_backward",
 ]
 
 
@@ -508,6 +512,8 @@ class _BlockCalls:
     def __init__(self):
         torch = _torch()
         lib = abi.load()
+        self.bf16, self.i32 = torch.bfloat16, torch.int32
+        self.forward_workspace_bytes = lib.bitlinear_forward_workspace_bytes
         self.f32, self.i8, self.empty, self.empty_like = torch.float32, torch.int8, torch.empty, torch.empty_like
         self.plain = {torch.float32: abi.F32, torch.bfloat16: abi.BF16}
         self.on_device = torch.cuda.device
@@ -515,7 +521,7 @@ class _BlockCalls:
         self.device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         self.stream_of = getattr(torch._C, "_cuda_getCurrentRawStream",
                                  lambda index: torch.cuda.current_stream(index).cuda_stream)
-        for name in abi.BLOCK_SIGNATURES:
+        for name in (*abi.BLOCK_SIGNATURES, *abi.GATED_SIGNATURES):
             setattr(self, name[len("bitlinear_"):], getattr(lib, name))
 
     def launch(self, fn, device, *args):
@@ -751,3 +757,183 @@ def relu2_backward(dA, H, out_dtype=None, out=None):
     dH = _output(B, out, M, K, out_dtype, device, dA)
     B.launch(B.relu2_backward, device, dA.data_ptr(), adt, h, hs, dt, M, K, dH.data_ptr(), odt)
     return dH
+
+
+# ---- the gated feed-forward block (include/bitlinear_gated.h) ----------------
+
+_ACTS = {"relu2": abi.ACT_RELU2, "silu": abi.ACT_SILU}
+
+
+def _act(act):
+    a = _ACTS.get(act)
+    if a is None:
+        raise ValueError("act must be 'relu2' or 'silu'")
+    return a
+
+
+def _path(path):
+    p = _PATHS.get(path)
+    if p is None:
+        raise ValueError("path must be 'auto', 'decode' or 'prefill'")
+    return p
+
+
+def _ternary(B, w, K, N, device, name):
+    """(packed address, gamma address, N) of (packed [N, packed_words(K)], gamma [1]) on `device`."""
+    packed, gamma = w
+    if not (packed.is_cuda and packed.is_contiguous()):
+        _require_cuda(packed, f"{name}'s packed weights")
+    if packed.dim() != 2 or packed.element_size() != 4 or packed.shape[1] != (K + 63) // 64 * 4 or not packed.numel() \
+            or (N is not None and packed.shape[0] != N):
+        raise ValueError(f"{name}'s packed weights must hold padded_k({K}) // 16 32-bit words for each of "
+                         f"{'their' if N is None else N} rows")
+    if packed.get_device() != device.index:
+        raise ValueError(f"{name}'s packed weights are on another device")
+    return packed.data_ptr(), _vector(B, gamma, 1, device, f"{name}'s gamma"), packed.shape[0]
+
+
+def _workspace(B, workspace, need, device):
+    """(address, bytes, tensor to keep) of `workspace`, or of a new one of `need` bytes."""
+    if workspace is None:
+        if not need:
+            return 0, 0, None
+        workspace = B.empty(need, dtype=B.i8, device=device)
+        return workspace.data_ptr(), need, workspace
+    _require_cuda(workspace, "workspace")
+    if workspace.device != device:
+        raise ValueError("workspace is on another device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _fits_decode(M, K, N):
+    """decode_fits without the library's calls: at most 16 tokens, their codes within 65536 bytes."""
+    return M <= 16 and M * ((K + 63) // 64 * 64 + 16) <= 65536 and M * N < (1 << 29)
+
+
+def gated_forward(X, gate, up, K: int | None = None, act: str = "relu2", out_dtype=None, save=None,
+                  path: str = "auto", out=None, workspace=None):
+    """H = act(BitLinear_gate(X)) * BitLinear_up(X), act 'relu2' or 'silu'.
+
+    X: float32 or bfloat16 [M, D], or its codes as :func:`quantize_activations` returns them (then K = D is
+    needed; ``path`` and ``workspace`` do not apply).  ``gate``, ``up``: (packed [F, words(D)], gamma [1]).
+    H [M, F] is of ``out_dtype`` (default float32).  With ``save`` a dtype returns (H, G, U), both projections
+    in that type, for :func:`gated_backward`.
+    """
+    B = _BLOCK or _block()
+    a, p = _act(act), _path(path)
+    codes = isinstance(X, (tuple, list))
+    if codes:
+        Xq, ga, rs = X
+        if K is None:
+            raise ValueError("K is needed where X is given as codes")
+        for t, nm in ((Xq, "Xq"), (rs, "rowsum")):
+            _require_cuda(t, nm)
+        M, device = Xq.shape[0], Xq.device
+        if Xq.dtype != B.i8 or Xq.dim() != 2 or not Xq.numel() or Xq.shape[1] != (K + 63) // 64 * 64:
+            raise ValueError("Xq must be int8 [M, padded_k(K)]")
+        if rs.dtype != B.i32 or rs.numel() != M or rs.device != device:
+            raise ValueError("rowsum must hold M int32 values on X's device")
+        gap = _vector(B, ga, M, device, "gamma_a")
+    else:
+        dt, M, D = _matrix(B, X, "X")
+        if K is not None and K != D:
+            raise ValueError("K does not match X")
+        K, device = D, X.device
+    gp, gg, F = _ternary(B, gate, K, None, device, "gate")
+    up_, ug, _ = _ternary(B, up, K, F, device, "up")
+    if out_dtype is None:
+        out_dtype = B.f32 if out is None else out.dtype
+    hdt = _plain_dtype(B, out_dtype, "out_dtype")
+    H = _output(B, out, M, F, out_dtype, device)
+    G = U = None
+    G_, U_, sdt = 0, 0, 0
+    if save is not None:
+        sdt = _plain_dtype(B, save, "save")
+        G = B.empty(M, F, dtype=save, device=device)
+        U = B.empty_like(G)
+        G_, U_ = G.data_ptr(), U.data_ptr()
+    if codes:
+        B.launch(B.gated_forward_quantized, device, Xq.data_ptr(), gap, rs.data_ptr(), M, K, F, gp, gg, up_, ug, a,
+                 H.data_ptr(), hdt, G_, U_, sdt)
+    else:
+        need = 0
+        if workspace is None and not (p != abi.PATH_PREFILL and _fits_decode(M, K, F)) and p != abi.PATH_DECODE:
+            need = B.forward_workspace_bytes(M, K)
+        wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
+        B.launch(B.gated_forward, device, X.data_ptr(), dt, M, K, F, gp, gg, up_, ug, a, H.data_ptr(), hdt, G_, U_,
+                 sdt, p, wsp, ws_bytes)
+    return H if save is None else (H, G, U)
+
+
+def gated_ffn_forward(X, gate, up, down, act: str = "relu2", path: str = "auto", return_hidden: bool = False,
+                      out=None, workspace=None):
+    """Y = BitLinear_down(act(BitLinear_gate(X)) * BitLinear_up(X)) for X float32 or bfloat16 [M, D].
+
+    ``gate``, ``up`` = (packed [F, words(D)], gamma [1]), ``down`` = (packed [D_out, words(F)], gamma [1]).
+    Returns Y float32 [M, D_out] (and the hidden layer float32 [M, F] if asked).
+    """
+    B = _BLOCK or _block()
+    a, p = _act(act), _path(path)
+    dt, M, D = _matrix(B, X, "X")
+    device = X.device
+    gp, gg, F = _ternary(B, gate, D, None, device, "gate")
+    up_, ug, _ = _ternary(B, up, D, F, device, "up")
+    dp, dg, Do = _ternary(B, down, F, None, device, "down")
+    Y = _output(B, out, M, Do, B.f32, device)
+    H = B.empty(M, F, dtype=B.f32, device=device) if return_hidden else None
+    need = 0 if workspace is not None else B.gated_ffn_workspace_bytes(M, D, F)
+    wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
+    B.launch(B.gated_ffn_forward, device, X.data_ptr(), dt, M, D, F, Do, gp, gg, up_, ug, a, dp, dg, Y.data_ptr(),
+             H.data_ptr() if return_hidden else 0, p, wsp, ws_bytes)
+    return (Y, H) if return_hidden else Y
+
+
+def gated_backward(dH, G, U, act: str = "relu2", out_dtype=None):
+    """(dG, dU) of H = act(G) * U from dH (float32 or bfloat16 [M, F]) and the kept G and U.
+
+    Both are of ``out_dtype`` (default bfloat16, what :func:`gated_input_backward` and :func:`backward` take).
+    """
+    B = _BLOCK or _block()
+    a = _act(act)
+    hdt, M, F = _matrix(B, dH, "dH")
+    gdt, m, f = _matrix(B, G, "G")
+    udt, m2, f2 = _matrix(B, U, "U")
+    if (m, f) != (M, F) or (m2, f2) != (M, F) or udt != gdt:
+        raise ValueError("dH, G and U must have one shape, G and U one dtype")
+    device = dH.device
+    if G.device != device or U.device != device:
+        raise ValueError("dH, G and U are on different devices")
+    if out_dtype is None:
+        out_dtype = B.bf16
+    odt = _plain_dtype(B, out_dtype, "out_dtype")
+    dG = B.empty(M, F, dtype=out_dtype, device=device)
+    dU = B.empty_like(dG)
+    B.launch(B.gated_backward, device, dH.data_ptr(), hdt, G.data_ptr(), U.data_ptr(), gdt, M, F, a, dG.data_ptr(),
+             dU.data_ptr(), odt)
+    return dG, dU
+
+
+def gated_input_backward(dG, dU, gateT, upT, K: int, out=None, workspace=None):
+    """dX = gamma_gate (dG W_gate) + gamma_up (dU W_up), float32 [M, K], from bfloat16 dG, dU [M, F].
+
+    ``gateT``, ``upT`` = (packedT [K, words(F)] as :func:`pack_transposed` returns it, gamma [1]); K: the
+    projections' input width.  Their dW: :func:`backward` with dG and dU, ``need_dx=False``.
+    """
+    B = _BLOCK or _block()
+    _, M, F = _matrix(B, dG, "dG")
+    _, m, f = _matrix(B, dU, "dU")
+    if dG.dtype != B.bf16 or dU.dtype != B.bf16 or (m, f) != (M, F):
+        raise ValueError("dG and dU must be bfloat16 of one shape")
+    device = dG.device
+    if dU.device != device:
+        raise ValueError("dG and dU are on different devices")
+    gp, gg, _ = _ternary(B, gateT, F, K, device, "gateT")
+    up_, ug, _ = _ternary(B, upT, F, K, device, "upT")
+    dX = _output(B, out, M, K, B.f32, device)
+    need = 0
+    if workspace is None and (F % 8 or dG.data_ptr() % 16 or dU.data_ptr() % 16):
+        need = B.gated_input_backward_workspace_bytes(M, F)
+    wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
+    B.launch(B.gated_input_backward, device, dG.data_ptr(), dU.data_ptr(), M, F, K, gp, gg, up_, ug, dX.data_ptr(),
+             wsp, ws_bytes)
+    return dX

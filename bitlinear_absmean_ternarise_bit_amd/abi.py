@@ -1,5 +1,5 @@
-"""ctypes view of libbitlinear.so (the C ABI declared in include/bitlinear.h and
-include/bitlinear_block.h) and of the benchmark's probe library libbitlinear_probe.so
+"""ctypes view of libbitlinear.so (the C ABI declared in include/bitlinear.h,
+bitlinear_block.h and bitlinear_gated.h) and of the benchmark's probe library libbitlinear_probe.so
 (include/bitlinear_probe.h).
 
 Loading is lazy and fails loudly: there is no fallback implementation.
@@ -23,6 +23,9 @@ ERR_ARG = -7
 F32 = 0
 BF16 = 1
 SAVED8 = 2  # an input saved in 8 bits (bitlinear_block.h)
+
+ACT_RELU2 = 0  # bitlinear_gated.h
+ACT_SILU = 1
 
 PATH_AUTO = 0
 PATH_DECODE = 1
@@ -78,6 +81,20 @@ BLOCK_SIGNATURES = {
     "bitlinear_relu2_backward": (_int, [_p, _int, _p, _p, _int, _i64, _i64, _p, _int, _p]),
 }
 
+# the gated feed-forward block (include/bitlinear_gated.h, same library)
+GATED_SIGNATURES = {
+    "bitlinear_gated_forward": (_int, [_p, _int, _i64, _i64, _i64, _p, _p, _p, _p, _int, _p, _int, _p, _p, _int, _int,
+                                       _p, _sz, _p]),
+    "bitlinear_gated_forward_quantized": (_int, [_p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _int, _p, _int, _p, _p,
+                                                 _int, _p]),
+    "bitlinear_gated_ffn_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "bitlinear_gated_ffn_forward": (_int, [_p, _int, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _int, _p, _p, _p, _p,
+                                           _int, _p, _sz, _p]),
+    "bitlinear_gated_backward": (_int, [_p, _int, _p, _p, _int, _i64, _i64, _int, _p, _p, _int, _p]),
+    "bitlinear_gated_input_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "bitlinear_gated_input_backward": (_int, [_p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _sz, _p]),
+}
+
 NOALLOC_SCRATCH_BYTES = 80 * 1024 * 1024  # BITLINEAR_NOALLOC_SCRATCH_BYTES
 
 # the attainable-peak probes of libbitlinear_probe.so (not the BitLinear ABI)
@@ -121,7 +138,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the BitLinear HIP library (once).  Raises if it has not been built."""
     global _LIB
     if _LIB is None:
-        _LIB = _open(path, {**SIGNATURES, **BLOCK_SIGNATURES})
+        _LIB = _open(path, {**SIGNATURES, **BLOCK_SIGNATURES, **GATED_SIGNATURES})
     return _LIB
 
 

@@ -3,64 +3,15 @@
 #include <stdint.h>
 
 #include "../../include/bitlinear.h"
-#include "kernels.hpp"
+#include "abi_common.hpp"
 
 using namespace bitlinear;
 
 namespace {
 
-constexpr int64_t kMaxK = int64_t(1) << 20;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int check_mnk(int64_t M, int64_t N, int64_t K) {
-  if (M < 1 || N < 1 || K < 1) return BITLINEAR_ERR_SHAPE;
-  if (K > kMaxK) return BITLINEAR_ERR_SHAPE;
-  if (N > (int64_t(1) << 31) || M > (int64_t(1) << 31)) return BITLINEAR_ERR_SHAPE;
-  if (static_cast<uint64_t>(N) * static_cast<uint64_t>(K) >= (uint64_t(1) << 32)) return BITLINEAR_ERR_SHAPE;
-  // the kernels address a packed matrix (N * Kp / 4 bytes; the radix-3 form,
-  // N * Kp3 / 5, is never larger) with 32-bit signed byte counts
-  if (static_cast<uint64_t>(N) * static_cast<uint64_t>(padded_k(K)) / 4 >= (uint64_t(1) << 31))
-    return BITLINEAR_ERR_SHAPE;
-  if (static_cast<uint64_t>(M) * static_cast<uint64_t>(N) >= (uint64_t(1) << 40)) return BITLINEAR_ERR_SHAPE;
-  if (static_cast<uint64_t>(M) * static_cast<uint64_t>(K) >= (uint64_t(1) << 40)) return BITLINEAR_ERR_SHAPE;
-  return BITLINEAR_OK;
-}
-
-int check_x(const void* X, int x_dtype) {
-  if (x_dtype != BITLINEAR_F32 && x_dtype != BITLINEAR_BF16) return BITLINEAR_ERR_DTYPE;
-  if (!aligned(X, x_dtype == BITLINEAR_F32 ? 4 : 2)) return BITLINEAR_ERR_ALIGN;
-  return BITLINEAR_OK;
-}
-
-// The decode kernel keeps all token codes in LDS and addresses a layer's
-// outputs with 32-bit offsets.
-bool decode_fits(int64_t M, int64_t K, int64_t N) {
-  return M <= kDecodeMaxM && M * (padded_k(K) + 16) <= kDecodeMaxCodes && M * N < (int64_t(1) << 29);
-}
-
 bool decode_fits_r3(int64_t M, int64_t K, int64_t N) {
   return M <= kDecodeMaxM && M * (r3_padded_k(K) + 16) <= kDecodeMaxCodes && M * N < (int64_t(1) << 29);
 }
-
-struct PrefillWs {
-  int8_t* xq;
-  float* ga;
-  int32_t* rs;
-};
-
-PrefillWs prefill_ws(void* ws, int64_t M, int64_t K) {
-  char* p = static_cast<char*>(ws);
-  PrefillWs w;
-  w.xq = reinterpret_cast<int8_t*>(p);
-  p += align256(static_cast<size_t>(M) * static_cast<size_t>(padded_k(K)));
-  w.ga = reinterpret_cast<float*>(p);
-  p += align256(static_cast<size_t>(M) * 4);
-  w.rs = reinterpret_cast<int32_t*>(p);
-  return w;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? BITLINEAR_OK : BITLINEAR_ERR_HIP; }
 
 }  // namespace
 

@@ -4,58 +4,12 @@
 #include <stdint.h>
 
 #include "../../include/bitlinear_block.h"
+#include "abi_common.hpp"
 #include "block_ops.hpp"
 
 using namespace bitlinear;
 
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int check_mk(int64_t M, int64_t K) {
-  if (M < 1 || K < 1 || K > (int64_t(1) << 20) || M > (int64_t(1) << 31)) return BITLINEAR_ERR_SHAPE;
-  return static_cast<uint64_t>(M) * static_cast<uint64_t>(K) >= (uint64_t(1) << 40) ? BITLINEAR_ERR_SHAPE
-                                                                                    : BITLINEAR_OK;
-}
-
-bool plain_dtype(int dt) { return dt == BITLINEAR_F32 || dt == BITLINEAR_BF16; }
-
-// A memory range of an argument; NULL ranges overlap nothing.
-struct Range {
-  const void* p;
-  uint64_t bytes;
-};
-
-bool overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y ? y - x < a.bytes : x - y < b.bytes;
-}
-
-// Whether an output overlaps an input or another output.
-template <int NO, int NI>
-bool any_overlap(const Range (&out)[NO], const Range (&in)[NI]) {
-  for (int i = 0; i < NO; ++i) {
-    for (int j = 0; j < NI; ++j)
-      if (overlap(out[i], in[j])) return true;
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i], out[j])) return true;
-  }
-  return false;
-}
-
-// Sizes of arrays within the limits of check_mk (no overflow in 64 bits).
-Range array(const void* p, int dt, int64_t M, int64_t K) {
-  const uint64_t m = static_cast<uint64_t>(M);
-  if (dt == BITLINEAR_SAVED8) return {p, m * static_cast<uint64_t>(padded_k(K))};
-  return {p, m * static_cast<uint64_t>(K) * (dt == BITLINEAR_F32 ? 4 : 2)};
-}
-Range floats(const float* p, int64_t n) { return {p, static_cast<uint64_t>(n) * 4}; }
-Range scale_range(const float* p, int64_t M, int64_t K) { return floats(p, M * saved_groups(K)); }
-
-bool aligned_to(const void* p, int dt) {
-  return aligned(p, dt == BITLINEAR_F32 ? 4 : dt == BITLINEAR_BF16 ? 2 : 16);
-}
 
 // An input that may be whole or saved: dtype, scales, alignment.
 int check_in(const void* p, const float* scales, int dt) {
@@ -72,8 +26,6 @@ int check_saved_out(const int8_t* codes, const float* scales, int in_dtype) {
   if (in_dtype == BITLINEAR_SAVED8) return BITLINEAR_ERR_ARG;
   return aligned(codes, 16) && aligned(scales, 4) ? BITLINEAR_OK : BITLINEAR_ERR_ALIGN;
 }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? BITLINEAR_OK : BITLINEAR_ERR_HIP; }
 
 BlockIn block_in(const void* p, const float* scales, int dt) {
   return {p, dt == BITLINEAR_SAVED8 ? scales : nullptr, dt};

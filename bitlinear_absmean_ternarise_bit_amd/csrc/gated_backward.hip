@@ -1,0 +1,109 @@
+// Backward of the gated feed-forward block (include/bitlinear_gated.h):
+// through act(G) * U, element by element, and the input's gradient, the sum of
+// two products on the bf16 matrix cores.
+#include "bf16_gemm.hpp"
+#include "flat_device.hpp"
+#include "gated_device.hpp"
+#include "gated_ops.hpp"
+
+namespace bitlinear {
+
+namespace {
+
+// dG and dU from dH, G and U, each read once, each written once.
+template <int HT, int GT, int OT>
+__global__ __launch_bounds__(256) void gated_backward_kernel(const char* dH, const char* G, const char* U, int64_t n,
+                                                             int act, char* dG, char* dU) {
+  const int64_t first = 8 * (static_cast<int64_t>(streaming_block()) * 256 + threadIdx.x);
+  if (first >= n) return;
+  const int m = static_cast<int>(min(n - first, int64_t(8)));
+  float d[8], g[8], u[8];
+  load_flat<HT>(dH + first * kBytes<HT>, m, d);
+  load_flat<GT>(G + first * kBytes<GT>, m, g);
+  load_flat<GT>(U + first * kBytes<GT>, m, u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (act == kActRelu2) {
+      const float r = g[i] <= 0.0f ? 0.0f : g[i];
+      g[i] = __fmul_rn(d[i], __fmul_rn(u[i], 2.0f * r));
+      u[i] = __fmul_rn(d[i], __fmul_rn(r, r));
+    } else {
+      const float s = sigmoid(g[i]);
+      const float slope = __fmul_rn(s, __fmaf_rn(g[i], __fsub_rn(1.0f, s), 1.0f));
+      const float a = __fmul_rn(g[i], s);
+      g[i] = __fmul_rn(__fmul_rn(d[i], u[i]), slope);
+      u[i] = __fmul_rn(d[i], a);
+    }
+  }
+  store_chunk<OT>(dG + first * kBytes<OT>, 0, m, g);
+  store_chunk<OT>(dU + first * kBytes<OT>, 0, m, u);
+}
+
+template <int HT, int GT, int OT>
+hipError_t launch_as(const void* dH, const void* G, const void* U, int64_t n, int act, void* dG, void* dU,
+                     hipStream_t stream) {
+  for (int64_t i = 0; i < n; i += 8 * kFlatChunks) {
+    const int64_t part = n - i < 8 * kFlatChunks ? n - i : 8 * kFlatChunks;
+    gated_backward_kernel<HT, GT, OT><<<static_cast<unsigned>((part + 2047) / 2048), 256, 0, stream>>>(
+        static_cast<const char*>(dH) + i * kBytes<HT>, static_cast<const char*>(G) + i * kBytes<GT>,
+        static_cast<const char*>(U) + i * kBytes<GT>, part, act, static_cast<char*>(dG) + i * kBytes<OT>,
+        static_cast<char*>(dU) + i * kBytes<OT>);
+  }
+  return hipGetLastError();
+}
+
+template <int HT, int GT>
+hipError_t launch_to(const void* dH, const void* G, const void* U, int64_t n, int act, void* dG, void* dU, int d_dtype,
+                     hipStream_t s) {
+  return d_dtype == kF32 ? launch_as<HT, GT, kF32>(dH, G, U, n, act, dG, dU, s)
+                         : launch_as<HT, GT, kBf16>(dH, G, U, n, act, dG, dU, s);
+}
+
+// C[p, q] = gamma A B^T + gamma2 A2 B2^T (bf16_gemm.hpp, EPI 2)
+template <int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 1) void bf16_two_products_kernel(
+    const uint16_t* __restrict__ A, int64_t P, int64_t lda, const void* __restrict__ B, int64_t Q, int64_t Rp,
+    float* __restrict__ C, const float* __restrict__ gamma, int bytes_a, int bytes_b, int tiles_p, int tiles_q,
+    SecondProduct second) {
+  bf16_gemm_nt_body<BM, BN, WM, WN, 1, 2>(A, P, lda, B, Q, Rp, C, Q, gamma, nullptr, 0, bytes_a, bytes_b, tiles_p,
+                                          tiles_q, second);
+}
+
+}  // namespace
+
+hipError_t launch_gated_backward(const void* dH, int dh_dtype, const void* G, const void* U, int gu_dtype, int64_t M,
+                                 int64_t F, int act, void* dG, void* dU, int d_dtype, hipStream_t s) {
+  const int64_t n = M * F;
+  if (dh_dtype == kF32)
+    return gu_dtype == kF32 ? launch_to<kF32, kF32>(dH, G, U, n, act, dG, dU, d_dtype, s)
+                            : launch_to<kF32, kBf16>(dH, G, U, n, act, dG, dU, d_dtype, s);
+  return gu_dtype == kF32 ? launch_to<kBf16, kF32>(dH, G, U, n, act, dG, dU, d_dtype, s)
+                          : launch_to<kBf16, kBf16>(dH, G, U, n, act, dG, dU, d_dtype, s);
+}
+
+hipError_t launch_gated_input_backward(const uint16_t* dG, const uint16_t* dU, int64_t M, int64_t F, int64_t D,
+                                       const uint32_t* packedT_gate, const float* gamma_gate,
+                                       const uint32_t* packedT_up, const float* gamma_up, float* dX, void* copies,
+                                       hipStream_t stream) {
+  const int64_t Fp = padded_k(F);
+  int64_t lda = F;
+  if (copies) {
+    uint16_t* a = static_cast<uint16_t*>(copies);
+    uint16_t* b = a + backward_ws_part(M, Fp) / 2;
+    int64_t blocks = (M * Fp + 255) / 256;
+    if (blocks > 65536) blocks = 65536;
+    pad_rows_bf16_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(dG, M, F, a, Fp);
+    pad_rows_bf16_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(dU, M, F, b, Fp);
+    dG = a;
+    dU = b;
+    lda = Fp;
+  }
+  const int bytes_a = static_cast<int>(M * lda * 2), bytes_b = static_cast<int>(D * (Fp / 4));
+  const SecondProduct second = {dU, packedT_up, gamma_up};
+  const int tiles_p = static_cast<int>((M + 255) / 256), tiles_q = static_cast<int>((D + 127) / 128);
+  bf16_two_products_kernel<256, 128, 4, 2><<<static_cast<unsigned>(tiles_p * tiles_q), 512, 0, stream>>>(
+      dG, M, lda, packedT_gate, D, Fp, dX, gamma_gate, bytes_a, bytes_b, tiles_p, tiles_q, second);
+  return hipGetLastError();
+}
+
+}  // namespace bitlinear

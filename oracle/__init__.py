@@ -17,3 +17,4 @@ from .bitlinear_oracle import (R3_UNIT, pack_codes_r3, r3_byte, r3_packed_bytes,
 from .bitlinear_oracle import (LUT_ENTRIES, LUT_GROUP, lut_digits, lut_forward, lut_gemv, lut_index,
                                lut_table)
 from . import block_oracle as block  # the operators around BitLinear
+from . import gated_oracle as gated  # the gated feed-forward block
