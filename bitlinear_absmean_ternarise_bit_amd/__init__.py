@@ -1,7 +1,7 @@
 """BitNet b1.58 BitLinear forward on MI355X (gfx950).
 
 A thin torch-facing binding over the C ABI in ``include/bitlinear.h``,
-``include/bitlinear_block.h`` and ``include/bitlinear_gated.h``: these functions
+``bitlinear_block.h``, ``bitlinear_gated.h`` and ``bitlinear_adapters.h``: these functions
 only check and marshal arguments (device pointers, sizes, the current HIP stream); every step of the computation runs in the HIP kernels of
 ``libbitlinear.so``.  There is no CPU fallback: without the built library or a
 GPU the calls raise.
@@ -44,6 +44,10 @@ __all__ = [
     "gated_ffn_forward",
     "gated_backward",
     "gated_input_backward",
+    "adapters_forward",
+    "adapted_forward",
+    "adapters_backward",
+    "dropout",
 ]
 
 
@@ -521,7 +525,7 @@ class _BlockCalls:
         self.device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         self.stream_of = getattr(torch._C, "_cuda_getCurrentRawStream",
                                  lambda index: torch.cuda.current_stream(index).cuda_stream)
-        for name in (*abi.BLOCK_SIGNATURES, *abi.GATED_SIGNATURES):
+        for name in (*abi.BLOCK_SIGNATURES, *abi.GATED_SIGNATURES, *abi.ADAPTER_SIGNATURES):
             setattr(self, name[len("bitlinear_"):], getattr(lib, name))
 
     def launch(self, fn, device, *args):
@@ -937,3 +941,160 @@ def gated_input_backward(dG, dU, gateT, upT, K: int, out=None, workspace=None):
     B.launch(B.gated_input_backward, device, dG.data_ptr(), dU.data_ptr(), M, F, K, gp, gg, up_, ug, dX.data_ptr(),
              wsp, ws_bytes)
     return dX
+
+
+# ---- low-rank adapters and dropout (include/bitlinear_adapters.h) --------------
+#
+# Adapters are a triple (down [A, R, K], up [A, R, N], scales float32 [A]), down
+# and up float32 or bfloat16; rows int32 [M] names the adapter of each token
+# (outside 0 .. A - 1: none).
+
+def _adapters(B, adapters, rows, M, K, N, device):
+    """(A, R, N, addresses of down and up, their abi dtype, addresses of scales and rows), checked."""
+    down, up, scales = adapters
+    for t, nm in ((down, "down"), (up, "up"), (rows, "rows")):
+        if not (t.is_cuda and t.is_contiguous()):
+            _require_cuda(t, nm)
+        if t.get_device() != device.index:
+            raise ValueError(f"{nm} is on another device")
+    wdt = _plain_dtype(B, down.dtype, "down")
+    if up.dtype != down.dtype:
+        raise ValueError("down and up must have one dtype")
+    if down.dim() != 3 or up.dim() != 3 or not down.numel() or not up.numel() or up.shape[:2] != down.shape[:2]:
+        raise ValueError("down must be [A, R, K] and up [A, R, N]")
+    A, R, k = down.shape
+    n = up.shape[2]
+    if k != K or (N is not None and n != N):
+        raise ValueError("down and up do not match the projection")
+    if rows.dtype != B.i32 or rows.dim() != 1 or rows.shape[0] != M:
+        raise ValueError("rows must hold M int32 values")
+    return A, R, n, down.data_ptr(), up.data_ptr(), wdt, _vector(B, scales, A, device, "scales"), rows.data_ptr()
+
+
+def adapters_forward(X, adapters, rows, Y, return_low: bool = False, workspace=None):
+    """Y[m] += scale[a] (X[m] down[a]^T) up[a], a = rows[m], into Y (float32 [M, N], as :func:`forward`
+    returns it), which is returned.
+
+    X: float32 or bfloat16 [M, K].  With ``return_low`` returns (Y, T), T = X down^T float32 [M, R] for
+    :func:`adapters_backward`.
+    """
+    B = _BLOCK or _block()
+    dt, M, K = _matrix(B, X, "X")
+    device = X.device
+    A, R, N, dn, up, wdt, sc, ids = _adapters(B, adapters, rows, M, K, None, device)
+    _output(B, Y, M, N, B.f32, device)
+    T = B.empty(M, R, dtype=B.f32, device=device) if return_low else None
+    need = 0 if workspace is not None else B.adapters_workspace_bytes(M, K, N, R)
+    wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
+    B.launch(B.adapters_forward, device, X.data_ptr(), dt, M, K, N, ids, A, R, dn, up, wdt, sc, Y.data_ptr(),
+             T.data_ptr() if return_low else 0, wsp, ws_bytes)
+    return (Y, T) if return_low else Y
+
+
+def adapted_forward(X, packed, gamma, adapters, rows, K: int | None = None, path: str = "auto",
+                    return_low: bool = False, out=None, workspace=None):
+    """Y[m] = BitLinear(X)[m] + scale[a] (X[m] down[a]^T) up[a], a = rows[m]: a shared ternary projection
+    and every token's own adapter.
+
+    X: float32 or bfloat16 [M, K]; ``packed``, ``gamma``, ``path``: as for :func:`forward`.  Returns Y
+    float32 [M, N], or (Y, T) with ``return_low`` (see :func:`adapters_forward`).
+    """
+    B = _BLOCK or _block()
+    p = _path(path)
+    dt, M, Kx = _matrix(B, X, "X")
+    if K is not None and K != Kx:
+        raise ValueError("K does not match X")
+    K, device = Kx, X.device
+    pk, gm, N = _ternary(B, (packed, gamma), K, None, device, "the projection")
+    A, R, _, dn, up, wdt, sc, ids = _adapters(B, adapters, rows, M, K, N, device)
+    Y = _output(B, out, M, N, B.f32, device)
+    T = B.empty(M, R, dtype=B.f32, device=device) if return_low else None
+    need = 0
+    if workspace is None:
+        need = B.adapters_workspace_bytes(M, K, N, R)
+        if not (p != abi.PATH_PREFILL and _fits_decode(M, K, N)):
+            need += B.forward_workspace_bytes(M, K)
+    wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
+    B.launch(B.adapted_forward, device, X.data_ptr(), dt, M, K, pk, N, gm, ids, A, R, dn, up, wdt, sc, Y.data_ptr(),
+             T.data_ptr() if return_low else 0, p, wsp, ws_bytes)
+    return (Y, T) if return_low else Y
+
+
+def adapters_backward(dY, X, T, adapters, rows, dX=None, need_dx: bool = True, need_dw: bool = True,
+                      workspace=None):
+    """Gradients (dX, ddown, dup) of :func:`adapters_forward` from dY (float32 or bfloat16 [M, N]).
+
+    ``X``, ``T``: the forward's input and its X down^T.  ``dX``: a float32 [M, K] tensor to add to (the
+    frozen projection's, from :func:`backward`); else a new one, zeros for tokens without an adapter.
+    ddown, dup: float32 [A, R, K] and [A, R, N].  None where not needed.
+    """
+    B = _BLOCK or _block()
+    ddt, M, N = _matrix(B, dY, "dY")
+    xdt, m, K = _matrix(B, X, "X")
+    device = dY.device
+    if m != M:
+        raise ValueError("X and dY do not have the same rows")
+    if X.device != device:
+        raise ValueError("X is on another device")
+    A, R, _, dn, up, wdt, sc, ids = _adapters(B, adapters, rows, M, K, N, device)
+    if not (need_dx or need_dw):
+        raise ValueError("nothing to compute")
+    if dX is not None and not need_dx:
+        raise ValueError("dX is given and not needed")
+    accumulate = dX is not None
+    tp = _vector(B, T, M * R, device, "T") if need_dw else 0
+    if need_dw and T is None:
+        raise ValueError("T of the forward is needed")
+    dd = du = None
+    dxp = ddp = dup_ = 0
+    if need_dx:
+        dX = _output(B, dX, M, K, B.f32, device)
+        dxp = dX.data_ptr()
+    if need_dw:
+        dd = B.empty(A, R, K, dtype=B.f32, device=device)
+        du = B.empty(A, R, N, dtype=B.f32, device=device)
+        ddp, dup_ = dd.data_ptr(), du.data_ptr()
+    need = 0 if workspace is not None else B.adapters_backward_workspace_bytes(M, K, N, A, R)
+    wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
+    B.launch(B.adapters_backward, device, dY.data_ptr(), ddt, X.data_ptr(), xdt, tp, M, K, N, ids, A, R, dn, up, wdt,
+             sc, dxp, int(accumulate), ddp, dup_, wsp, ws_bytes)
+    return dX, dd, du
+
+
+def dropout(X, p: float, seed: int, offset: int = 0, residual=None, out_dtype=None, out=None):
+    """X with each value dropped with probability p and the others times 1 / (1 - p), plus ``residual``.
+
+    X, ``residual``: float32 or bfloat16 of one shape.  The mask is a function of (seed, offset, index), 64
+    bits each, and never stored: the backward pass is the same call on the gradient.  The result is of
+    ``out_dtype`` (default: X's); ``out`` may be X or the residual itself.
+    """
+    B = _BLOCK or _block()
+    if not (X.is_cuda and X.is_contiguous()):
+        _require_cuda(X, "X")
+    xdt = _plain_dtype(B, X.dtype, "X")
+    n, device = X.numel(), X.device
+    if n == 0:
+        raise ValueError("X must hold at least one value")
+    rp = rdt = 0
+    if residual is not None:
+        if not (residual.is_cuda and residual.is_contiguous()):
+            _require_cuda(residual, "residual")
+        rdt = _plain_dtype(B, residual.dtype, "residual")
+        if residual.shape != X.shape or residual.get_device() != device.index:
+            raise ValueError("residual must have X's shape and device")
+        rp = residual.data_ptr()
+    if out_dtype is None:
+        out_dtype = X.dtype if out is None else out.dtype
+    ydt = _plain_dtype(B, out_dtype, "out_dtype")
+    if not (0.0 <= p < 1.0):
+        raise ValueError("p must be at least 0 and below 1")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must be unsigned 64-bit numbers")
+    if out is None:
+        out = B.empty_like(X, dtype=out_dtype)
+    else:
+        _require_cuda(out, "out")
+        if out.shape != X.shape or out.dtype != out_dtype or out.device != device:
+            raise ValueError(f"out must be {out_dtype} of X's shape on {device}")
+    B.launch(B.dropout, device, X.data_ptr(), xdt, rp, rdt, n, p, seed, offset, out.data_ptr(), ydt)
+    return out

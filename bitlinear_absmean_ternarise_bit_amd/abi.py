@@ -1,5 +1,5 @@
 """ctypes view of libbitlinear.so (the C ABI declared in include/bitlinear.h,
-bitlinear_block.h and bitlinear_gated.h) and of the benchmark's probe library libbitlinear_probe.so
+bitlinear_block.h, bitlinear_gated.h and bitlinear_adapters.h) and of the benchmark's probe library libbitlinear_probe.so
 (include/bitlinear_probe.h).
 
 Loading is lazy and fails loudly: there is no fallback implementation.
@@ -34,6 +34,8 @@ PATH_PREFILL = 2
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
+_u64 = ctypes.c_uint64
 _sz = ctypes.c_size_t
 _p = ctypes.c_void_p
 
@@ -95,6 +97,20 @@ GATED_SIGNATURES = {
     "bitlinear_gated_input_backward": (_int, [_p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
 
+# low-rank adapters and dropout (include/bitlinear_adapters.h, same library)
+ADAPTER_SIGNATURES = {
+    "bitlinear_adapters_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "bitlinear_adapters_forward": (_int, [_p, _int, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _int, _p, _p, _p, _p, _sz,
+                                          _p]),
+    "bitlinear_adapted_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "bitlinear_adapted_forward": (_int, [_p, _int, _i64, _i64, _p, _i64, _p, _p, _i64, _i64, _p, _p, _int, _p, _p, _p,
+                                         _int, _p, _sz, _p]),
+    "bitlinear_adapters_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "bitlinear_adapters_backward": (_int, [_p, _int, _p, _int, _p, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _int, _p,
+                                           _p, _int, _p, _p, _p, _sz, _p]),
+    "bitlinear_dropout": (_int, [_p, _int, _p, _int, _i64, _f64, _u64, _u64, _p, _int, _p]),
+}
+
 NOALLOC_SCRATCH_BYTES = 80 * 1024 * 1024  # BITLINEAR_NOALLOC_SCRATCH_BYTES
 
 # the attainable-peak probes of libbitlinear_probe.so (not the BitLinear ABI)
@@ -138,7 +154,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the BitLinear HIP library (once).  Raises if it has not been built."""
     global _LIB
     if _LIB is None:
-        _LIB = _open(path, {**SIGNATURES, **BLOCK_SIGNATURES, **GATED_SIGNATURES})
+        _LIB = _open(path, {**SIGNATURES, **BLOCK_SIGNATURES, **GATED_SIGNATURES, **ADAPTER_SIGNATURES})
     return _LIB
 
 

@@ -1,0 +1,100 @@
+// Internal launch interface and sizes of the low-rank adapters and of dropout
+// (include/bitlinear_adapters.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "block_ops.hpp"
+#include "sizes.hpp"
+
+namespace bitlinear {
+
+constexpr int64_t kAdapterMaxR = 256, kAdapterMaxA = 65535;
+
+// Adapters of M tokens: ids, and one of the two weight arrays [A, R, C].
+struct Adapters {
+  const int32_t* rows;
+  const float* scales;
+  int A, R, w_dtype;
+};
+
+inline int64_t padded_r(int64_t R) { return (R + 15) / 16 * 16; }
+
+// The first product, T = X W^T over C columns, goes over blocks of 16 tokens
+// and is cut along the columns where tokens are few, into parts that are added
+// by whoever reads T.  `spread`: that many workgroups share the adapters of a
+// block (each takes every spread-th one).
+struct ShrinkPlan {
+  int spread, parts;
+};
+inline ShrinkPlan shrink_plan(int64_t M, int64_t C) {
+  const int64_t blocks = (M + 15) / 16;
+  ShrinkPlan p = {1, 1};
+  if (blocks < 16) p.spread = static_cast<int>(M < 16 ? M : 16);
+  int64_t parts = 512 / (blocks * p.spread);
+  const int64_t most = (C + 255) / 256;  // at least 256 columns, 64 to a wave
+  if (parts > most) parts = most;
+  if (parts > 16) parts = 16;
+  p.parts = static_cast<int>(parts < 1 ? 1 : parts);
+  return p;
+}
+
+// The gradients dW[a] = V^T X over C columns: workgroups of 128 columns, one
+// adapter and up to 64 of its R rows, cut along the tokens into parts that a
+// second launch adds.
+struct GradPlan {
+  int tiles, groups, parts;
+};
+inline GradPlan grad_plan(int64_t M, int64_t C, int64_t A, int64_t R) {
+  GradPlan p;
+  p.tiles = static_cast<int>((C + 127) / 128);
+  p.groups = static_cast<int>((R + 63) / 64);
+  int64_t parts = 512 / (int64_t(p.tiles) * p.groups * A);
+  const int64_t most = (M + 255) / 256;  // at least 64 tokens to a wave
+  if (parts > most) parts = most;
+  if (parts > 16) parts = 16;
+  p.parts = static_cast<int>(parts < 1 ? 1 : parts);
+  return p;
+}
+
+// Workspaces: T's parts [parts, M, padded_r(R)] float32; for the backward V's
+// parts, V, and the parts of whichever gradient needs more.
+inline size_t shrink_ws_bytes(int64_t M, int64_t C, int64_t R) {
+  const ShrinkPlan p = shrink_plan(M, C);
+  return align256(size_mul(size_mul(size_t(p.parts) * 4, size_t(M)), size_t(padded_r(R))));
+}
+inline size_t grad_ws_bytes(int64_t M, int64_t C, int64_t A, int64_t R) {
+  const GradPlan p = grad_plan(M, C, A, R);
+  return p.parts == 1 ? 256 : align256(size_mul(size_mul(size_t(p.parts) * 4, size_t(A)), size_mul(size_t(R), size_t(C))));
+}
+inline size_t adapters_ws_bytes(int64_t M, int64_t K, int64_t R) {
+  if (!size_args_ok(M) || !size_args_ok(K) || !size_args_ok(R) || R > kAdapterMaxR) return 0;
+  return shrink_ws_bytes(M, K, R);
+}
+inline size_t adapters_backward_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t A, int64_t R) {
+  if (!size_args_ok(M) || !size_args_ok(K) || !size_args_ok(N) || !size_args_ok(R) || R > kAdapterMaxR || A < 1 ||
+      A > kAdapterMaxA)
+    return 0;
+  const size_t v = align256(size_mul(size_mul(size_t(M), size_t(R)), 4));
+  const size_t d = grad_ws_bytes(M, K, A, R), u = grad_ws_bytes(M, N, A, R);
+  if (d == 0 || u == 0) return 0;
+  return size_add(size_add(shrink_ws_bytes(M, N, R), v), d > u ? d : u);
+}
+
+// parts of T = X W^T (rows without an adapter are not written)
+hipError_t launch_shrink(const void* X, int x_dtype, int64_t M, int64_t C, const Adapters& ad, const void* W,
+                         float* parts, hipStream_t stream);
+// Y[m] (+)= scale T[m] W from T's parts (of a shrink over C0 columns); T: NULL,
+// or where the whole T goes ([M, R], zeros for rows without an adapter)
+hipError_t launch_expand(const float* parts, int64_t M, int64_t C0, int64_t C, const Adapters& ad, const void* W,
+                         float* Y, bool accumulate, float* T, hipStream_t stream);
+// T alone
+hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, hipStream_t stream);
+// dW[a] = scale[a] V^T X, V [M, R]; ws: grad_ws_bytes
+hipError_t launch_adapter_grad(const float* V, const void* X, int x_dtype, int64_t M, int64_t C, const Adapters& ad,
+                               float* dW, float* ws, hipStream_t stream);
+hipError_t launch_dropout(const void* X, int x_dtype, const void* residual, int r_dtype, int64_t n, double p,
+                          uint64_t seed, uint64_t offset, void* Y, int y_dtype, hipStream_t stream);
+
+}  // namespace bitlinear

@@ -18,3 +18,4 @@ from .bitlinear_oracle import (LUT_ENTRIES, LUT_GROUP, lut_digits, lut_forward, 
                                lut_table)
 from . import block_oracle as block  # the operators around BitLinear
 from . import gated_oracle as gated  # the gated feed-forward block
+from . import adapter_oracle as adapters  # low-rank adapters and dropout
