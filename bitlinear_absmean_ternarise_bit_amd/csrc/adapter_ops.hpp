@@ -21,18 +21,19 @@ struct Adapters {
 
 inline int64_t padded_r(int64_t R) { return (R + 15) / 16 * 16; }
 
-// The first product, T = X W^T over C columns, goes over blocks of 16 tokens
-// and is cut along the columns where tokens are few, into parts that are added
-// by whoever reads T.  `spread`: that many workgroups share the adapters of a
-// block (each takes every spread-th one).
+// The first product, T = X W^T over C columns: `blocks` blocks of 16 tokens to a
+// workgroup (4 with 256 tokens or more, so that W is read once for 64), cut along
+// the columns where those are few, into parts that are added by whoever reads T.
+// `spread`: that many workgroups share the adapters of a block (each takes every
+// spread-th one).
 struct ShrinkPlan {
-  int spread, parts;
+  int blocks, spread, parts;
 };
 inline ShrinkPlan shrink_plan(int64_t M, int64_t C) {
-  const int64_t blocks = (M + 15) / 16;
-  ShrinkPlan p = {1, 1};
-  if (blocks < 16) p.spread = static_cast<int>(M < 16 ? M : 16);
-  int64_t parts = 512 / (blocks * p.spread);
+  ShrinkPlan p = {M >= 256 ? 4 : 1, 1, 1};
+  const int64_t groups = (M + 16 * p.blocks - 1) / (16 * p.blocks);
+  if (p.blocks == 1) p.spread = static_cast<int>(M < 16 ? M : 16);
+  int64_t parts = 512 / (groups * p.spread);
   const int64_t most = (C + 255) / 256;  // at least 256 columns, 64 to a wave
   if (parts > most) parts = most;
   if (parts > 16) parts = 16;
@@ -40,7 +41,13 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t C) {
   return p;
 }
 
-// The gradients dW[a] = V^T X over C columns: workgroups of 128 columns, one
+// The second product, Y += T W over C columns: 2 blocks of 16 tokens to a
+// workgroup of 512 columns where that makes two workgroups for every CU, else 1.
+inline int expand_blocks(int64_t M, int64_t C) {
+  return (M + 31) / 32 * ((C + 511) / 512) >= 512 ? 2 : 1;
+}
+
+// The gradients dW[a] = V^T X over C columns: workgroups of 64 columns, one
 // adapter and up to 64 of its R rows, cut along the tokens into parts that a
 // second launch adds.
 struct GradPlan {
@@ -48,7 +55,7 @@ struct GradPlan {
 };
 inline GradPlan grad_plan(int64_t M, int64_t C, int64_t A, int64_t R) {
   GradPlan p;
-  p.tiles = static_cast<int>((C + 127) / 128);
+  p.tiles = static_cast<int>((C + 63) / 64);
   p.groups = static_cast<int>((R + 63) / 64);
   int64_t parts = 512 / (int64_t(p.tiles) * p.groups * A);
   const int64_t most = (M + 255) / 256;  // at least 64 tokens to a wave

@@ -34,7 +34,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kBlock = 16;      // tokens of a block
-constexpr int kTileCols = 128;  // columns of a wave in expand and grad
+constexpr int kTileCols = 128;  // columns of a wave in expand
+constexpr int kGradCols = 4;    // columns of a lane in grad
 constexpr int64_t kMaxGrid = int64_t(1) << 20;  // workgroups; each walks every gridDim.x-th item
 
 template <int DT>
@@ -56,39 +57,64 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&p)[3]) {
   }
 }
 
-// Chunk c (eight columns) of a row of C, zeros behind it.
-template <int DT>
-__device__ __forceinline__ Raw<DT> any_chunk(const char* row, int64_t C, int64_t c) {
-  const int n = static_cast<int>(max(int64_t(0), min(int64_t(8), C - 8 * c)));
-  // the row's last 16 columns are enough to place what is left of it
-  const int64_t skip = C > 16 ? (C - 9) / 8 * 8 : 0;  // a multiple of 8; 9 to 16 columns follow, or all of a short row
-  if (n == 8 || C <= 16) {
-    const int K = n == 8 ? 8 : static_cast<int>(C);
-    const char* at = n == 8 ? row + 8 * c * kBytes<DT> : row;
-    const int cc = n == 8 ? 0 : static_cast<int>(c);
-    return K >= 8 ? load_chunk<DT, false>(at, nullptr, K, cc, n) : load_chunk<DT, true>(at, nullptr, K, cc, n);
+// CW consecutive values at p, aligned to their type only.
+template <int DT, int CW>
+struct Some;  // as they lie in memory: CW / 2 words of bfloat16, CW of float32
+template <int CW>
+struct Some<kF32, CW> {
+  uint32_t w[CW];
+};
+template <int CW>
+struct Some<kBf16, CW> {
+  uint32_t w[CW / 2];
+};
+typedef v2u v2u_by2 __attribute__((aligned(2)));
+template <int DT, int CW>
+__device__ __forceinline__ Some<DT, CW> load_some(const char* p) {
+  Some<DT, CW> r;
+  if constexpr (DT == kBf16 && CW == 4) {
+    const v2u a = *reinterpret_cast<const v2u_by2*>(p);
+    r.w[0] = a.x, r.w[1] = a.y;
+  } else if constexpr (DT == kBf16) {
+    const v4u a = *reinterpret_cast<const v4u_by2*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = a[i];
+  } else {
+#pragma unroll
+    for (int h = 0; h < CW / 4; ++h) {
+      const v4u a = *reinterpret_cast<const v4u_by4*>(p + 16 * h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[4 * h + i] = a[i];
+    }
   }
-  return load_chunk<DT, false>(row + skip * kBytes<DT>, nullptr, static_cast<int>(C - skip),
-                               static_cast<int>(c - skip / 8), n);
+  return r;
 }
-template <int DT>
-__device__ __forceinline__ Raw<DT> whole_chunk(const char* row, int64_t c) {
-  return fetch_chunk<DT, false>(row + 8 * c * kBytes<DT>, nullptr, 8, 1, 0);
+
+// A lane's CW columns of a row of C >= CW: chunk c, or the row's last CW columns
+// where the chunk is cut by the row's end or behind it.  Every load is then whole,
+// without a branch, and column j of the lane is its own where j >= `skip` (CW:
+// none): each column of the row has one owner.
+struct Columns {
+  int64_t first;
+  int skip;
+};
+template <int CW>
+__device__ __forceinline__ Columns lane_columns(int64_t C, int64_t c) {
+  const int64_t over = CW * (c + 1) - C;
+  return {over > 0 ? C - CW : CW * c, static_cast<int>(max(int64_t(0), min(over, int64_t(CW))))};
 }
 
 // Eight consecutive values of a row as operand planes (shrink).
 template <int DT>
-__device__ __forceinline__ void row_planes(const Raw<DT>& r, bf16x8 (&p)[kPlanes<DT>]) {
+__device__ __forceinline__ void row_planes(const Some<DT, 8>& r, bf16x8 (&p)[kPlanes<DT>]) {
   if constexpr (DT == kBf16) {
-    p[0] = __builtin_bit_cast(bf16x8, r.a);
+    p[0] = __builtin_bit_cast(bf16x8, v4u{r.w[0], r.w[1], r.w[2], r.w[3]});
   } else {
-    float v[8];
-    chunk_f32<DT>(r, v);
     v4u w[3];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t s[3];
-      split(v[2 * i], v[2 * i + 1], s);
+      split(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]), s);
 #pragma unroll
       for (int q = 0; q < 3; ++q) w[q][i] = s[q];
     }
@@ -97,26 +123,23 @@ __device__ __forceinline__ void row_planes(const Raw<DT>& r, bf16x8 (&p)[kPlanes
   }
 }
 
-// Four rows of eight columns as the operand planes of each column: element i of
+// Four rows of CW columns as the operand planes of each column: element i of
 // plane q of column j is row i's (expand, grad: rows are the contraction).
-template <int DT>
-__device__ __forceinline__ void column_planes(const Raw<DT> (&r)[4], s16x4 (&p)[kPlanes<DT>][8]) {
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <int DT, int CW>
+__device__ __forceinline__ void column_planes(const Some<DT, CW> (&r)[4], s16x4 (&p)[kPlanes<DT>][CW]) {
   if constexpr (DT == kBf16) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      p[0][2 * h] = __builtin_bit_cast(s16x4, u32x2{lower(r[0].a[h], r[1].a[h]), lower(r[2].a[h], r[3].a[h])});
-      p[0][2 * h + 1] = __builtin_bit_cast(s16x4, u32x2{upper(r[0].a[h], r[1].a[h]), upper(r[2].a[h], r[3].a[h])});
+    for (int h = 0; h < CW / 2; ++h) {
+      p[0][2 * h] = __builtin_bit_cast(s16x4, u32x2{lower(r[0].w[h], r[1].w[h]), lower(r[2].w[h], r[3].w[h])});
+      p[0][2 * h + 1] = __builtin_bit_cast(s16x4, u32x2{upper(r[0].w[h], r[1].w[h]), upper(r[2].w[h], r[3].w[h])});
     }
   } else {
-    float v[4][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) chunk_f32<DT>(r[i], v[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < CW; ++j) {
       uint32_t lo[3], hi[3];
-      split(v[0][j], v[1][j], lo);
-      split(v[2][j], v[3][j], hi);
+      split(__uint_as_float(r[0].w[j]), __uint_as_float(r[1].w[j]), lo);
+      split(__uint_as_float(r[2].w[j]), __uint_as_float(r[3].w[j]), hi);
 #pragma unroll
       for (int q = 0; q < 3; ++q) p[q][j] = __builtin_bit_cast(s16x4, u32x2{lo[q], hi[q]});
     }
@@ -125,7 +148,6 @@ __device__ __forceinline__ void column_planes(const Raw<DT> (&r)[4], s16x4 (&p)[
 
 // Four float32 as operand planes.
 __device__ __forceinline__ void value_planes(const f32x4& v, s16x4 (&p)[3]) {
-  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   uint32_t lo[3], hi[3];
   split(v[0], v[1], lo);
   split(v[2], v[3], hi);
@@ -133,99 +155,127 @@ __device__ __forceinline__ void value_planes(const f32x4& v, s16x4 (&p)[3]) {
   for (int q = 0; q < 3; ++q) p[q] = __builtin_bit_cast(s16x4, u32x2{lo[q], hi[q]});
 }
 
-// The adapter of token m0 + lane (lanes 0 to 15), -1 for none.
-__device__ __forceinline__ int token_adapter(const Adapters& ad, int64_t m0, int64_t M, int lane) {
+// The adapter of token m0 + lane, -1 for none; `tokens`: those of the group.
+__device__ __forceinline__ int token_adapter(const Adapters& ad, int64_t m0, int64_t M, int tokens, int lane) {
   const int64_t m = m0 + lane;
-  const int id = lane < kBlock && m < M ? ad.rows[m] : -1;
+  const int id = lane < tokens && m < M ? ad.rows[m] : -1;
   return id >= 0 && id < ad.A ? id : -1;
 }
 
-// Calls f(a, mine) for the adapters of a block, every `spread`-th one from
-// `from`: mine has bit t set where token t is a's.  The same for all lanes.
+// Calls f(a, mine) for the adapters of a group of up to 64 tokens, every
+// `spread`-th one from `from`: mine has bit t set where token t is a's.  The
+// same for all lanes.
 template <typename F>
 __device__ __forceinline__ void each_adapter(int id, int spread, int from, F&& f) {
-  uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0)) & 0xffffu;
+  uint64_t todo = __ballot(id >= 0);
   for (int n = 0; todo; ++n) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-    const uint32_t mine = static_cast<uint32_t>(__ballot(id == a)) & 0xffffu;
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    const uint64_t mine = __ballot(id == a);
     todo &= ~mine;
     if (n % spread == from) f(a, mine);
   }
 }
 
 // ---- shrink ---------------------------------------------------------------------
-// A workgroup takes a block of 16 tokens, one part of the columns and every
-// spread-th adapter of the block; its four waves share the part's columns in
+// A workgroup takes RB blocks of 16 tokens, one part of the columns and every
+// spread-th adapter of those tokens; its four waves share the part's columns in
 // steps of 32 (v_mfma_f32_16x16x32_bf16: lane l holds token or rank row l % 16,
 // columns 8 (l / 16) .. + 7) and add their sums in LDS.  RT tiles of 16 ranks at
-// a time.
-template <int XT, int WT, int RT>
-__global__ __launch_bounds__(kThreads) void shrink_kernel(const char* __restrict__ X, int64_t M, int64_t C, Adapters ad,
+// a time.  With RB = 4 a step's rows of W are read, and split into planes, once
+// for 64 tokens; with few tokens RB = 1 makes more workgroups.
+template <int XT, int WT, int RB, int RT>
+__global__ __launch_bounds__(kThreads, 2) void shrink_kernel(const char* __restrict__ X, int64_t M, int64_t C, Adapters ad,
                                                           const char* __restrict__ W, float* __restrict__ parts,
-                                                          int64_t blocks) {
-  __shared__ f32x4 sums[kWaves][RT][kWave];
+                                                          int64_t groups) {
+  __shared__ f32x4 sums[kWaves][RB * RT][kWave];
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int Rp = (ad.R + 15) & ~15;
   const int64_t steps = (C + 31) / 32, whole = C / 32;
   const int64_t q = static_cast<int64_t>(blockIdx.y) * kWaves + wave, Q = static_cast<int64_t>(gridDim.y) * kWaves;
   const int64_t lo = q * steps / Q, hi = (q + 1) * steps / Q;
-  for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
-    const int64_t m0 = block * kBlock;
-    const char* xrow = X + min(m0 + l, M - 1) * C * kBytes<XT>;
+  for (int64_t group = blockIdx.x; group < groups; group += gridDim.x) {
+    const int64_t m0 = group * (RB * kBlock);
+    const char* xrow[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) xrow[b] = X + min(m0 + kBlock * b + l, M - 1) * C * kBytes<XT>;
     float* out = parts + (static_cast<int64_t>(blockIdx.y) * M + m0) * Rp;
-    each_adapter(token_adapter(ad, m0, M, lane), gridDim.z, blockIdx.z, [&](int a, uint32_t mine) {
+    each_adapter(token_adapter(ad, m0, M, RB * kBlock, lane), gridDim.z, blockIdx.z, [&](int a, uint64_t mine) {
       for (int r0 = 0; r0 < ad.R; r0 += 16 * RT) {
-        f32x4 acc[RT];
+        f32x4 acc[RB][RT];
         const char* wrow[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int b = 0; b < RB; ++b) acc[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
           wrow[t] = W + (static_cast<int64_t>(a) * ad.R + min(r0 + 16 * t + l, ad.R - 1)) * C * kBytes<WT>;
         }
-        auto add = [&](const Raw<XT>& xr, const Raw<WT> (&wr)[RT]) {
-          bf16x8 x[kPlanes<XT>];
-          row_planes<XT>(xr, x);
+        auto add = [&](const Some<XT, 8> (&xr)[RB], const Some<WT, 8> (&wr)[RT]) {
+          bf16x8 w[RT][kPlanes<WT>];
 #pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            bf16x8 w[kPlanes<WT>];
-            row_planes<WT>(wr[t], w);
+          for (int t = 0; t < RT; ++t) row_planes<WT>(wr[t], w[t]);
 #pragma unroll
-            for (int p = 0; p < kPlanes<XT>; ++p)
+          for (int b = 0; b < RB; ++b) {
+            bf16x8 x[kPlanes<XT>];
+            row_planes<XT>(xr[b], x);
 #pragma unroll
-              for (int s = 0; s < kPlanes<WT>; ++s)
-                if (p + s <= 2) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[p], w[s], acc[t], 0, 0, 0);
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+              for (int p = 0; p < kPlanes<XT>; ++p)
+#pragma unroll
+                for (int s = 0; s < kPlanes<WT>; ++s)
+                  if (p + s <= 2) acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[p], w[t][s], acc[b][t], 0, 0, 0);
           }
         };
+        auto load = [&](int64_t col, Some<XT, 8> (&xr)[RB], Some<WT, 8> (&wr)[RT]) {
+#pragma unroll
+          for (int b = 0; b < RB; ++b) xr[b] = load_some<XT, 8>(xrow[b] + col * kBytes<XT>);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) wr[t] = load_some<WT, 8>(wrow[t] + col * kBytes<WT>);
+        };
         const int64_t end = min(hi, whole);
-#pragma unroll 4
+#pragma unroll 2
         for (int64_t st = lo; st < end; ++st) {
-          const int64_t c = 4 * st + g;
-          Raw<WT> wr[RT];
-          const Raw<XT> xr = whole_chunk<XT>(xrow, c);
-#pragma unroll
-          for (int t = 0; t < RT; ++t) wr[t] = whole_chunk<WT>(wrow[t], c);
+          Some<XT, 8> xr[RB];
+          Some<WT, 8> wr[RT];
+          load(32 * st + 8 * g, xr, wr);
           add(xr, wr);
         }
-        if (whole >= lo && whole < hi) {  // the step that the row's end cuts
-          const int64_t c = 4 * whole + g;
-          Raw<WT> wr[RT];
-          const Raw<XT> xr = any_chunk<XT>(xrow, C, c);
+        if (whole >= lo && whole < hi) {
+          // the step that the row's end cuts: columns that are not the lane's own
+          // meet zeros (their weights are this row's too: they can make nothing
+          // non-finite that is not so anyway)
+          const Columns at = lane_columns<8>(C, 4 * whole + g);
+          Some<XT, 8> xr[RB];
+          Some<WT, 8> wr[RT];
+          load(at.first, xr, wr);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) wr[t] = any_chunk<WT>(wrow[t], C, c);
+          for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (XT == kF32) {
+                if (j < at.skip) xr[b].w[j] = 0u;
+              } else {
+                if (j < at.skip) xr[b].w[j / 2] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+              }
+            }
           add(xr, wr);
         }
 #pragma unroll
-        for (int t = 0; t < RT; ++t) sums[wave][t][lane] = acc[t];
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) sums[wave][b * RT + t][lane] = acc[b][t];
         __syncthreads();
-        if (wave < RT) {
-          f32x4 v = sums[0][wave][lane];
+        for (int i = wave; i < RB * RT; i += kWaves) {
+          f32x4 v = sums[0][i][lane];
 #pragma unroll
-          for (int w = 1; w < kWaves; ++w) v += sums[w][wave][lane];
-          const int r = r0 + 16 * wave + l;
+          for (int w = 1; w < kWaves; ++w) v += sums[w][i][lane];
+          const int b = i / RT, r = r0 + 16 * (i - b * RT) + l;
           if (r < Rp) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (mine >> (4 * g + i) & 1u) out[static_cast<int64_t>(4 * g + i) * Rp + r] = r < ad.R ? v[i] : 0.0f;
+            for (int k = 0; k < 4; ++k) {
+              const int token = kBlock * b + 4 * g + k;
+              if (mine >> token & 1u) out[static_cast<int64_t>(token) * Rp + r] = r < ad.R ? v[k] : 0.0f;
+            }
           }
         }
         __syncthreads();
@@ -235,92 +285,152 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(const char* __restrict
 }
 
 // ---- expand ---------------------------------------------------------------------
-// A wave takes a block of 16 tokens and 128 columns; four waves to a workgroup.
+// A workgroup takes RB blocks of 16 tokens and 512 columns, 128 to a wave.  T's
+// parts are added once, scaled and split into planes in LDS; T itself leaves from
+// the workgroups of the first columns, if the caller wants it.
 // v_mfma_f32_16x16x16_bf16 with T as the rows (lane l: token l % 16, ranks
 // 4 (l / 16) .. + 3) and W as the columns: lane l loads eight consecutive columns
-// 8 (l % 16) .. + 7 of its four rank rows, 16 or 32 bytes a load, and column j of
-// each lane's eight is an operand of its own, so no transposition through LDS is
-// needed and a lane ends with eight consecutive columns of four tokens.
-template <int WT>
-__global__ __launch_bounds__(kThreads) void expand_kernel(const float* __restrict__ parts, int nparts, int64_t M,
+// of its four rank rows, 16 or 32 bytes a load, and column j of each lane's eight
+// is an operand of its own, so no transposition through LDS is needed and a lane
+// ends with eight consecutive columns of four tokens of each block, which it adds
+// to Y.
+template <int WT, int RB>
+__global__ __launch_bounds__(kThreads, 2) void expand_kernel(const float* __restrict__ parts, int nparts, int64_t M,
                                                           int64_t C, Adapters ad, const char* __restrict__ W, float* Y,
                                                           int accumulate, float* __restrict__ T, int64_t items,
                                                           int64_t tiles) {
+  // Y is asked for ahead of the products where the registers hold it beside
+  // them (float32 weights with two blocks: they do not)
+  constexpr bool kAhead = WT == kBf16 || RB == 1;
+  extern __shared__ __align__(16) short low[];  // [3 planes][RB * 16 tokens][Rp + 4]
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-  const int Rp = (ad.R + 15) & ~15;
+  const int Rp = (ad.R + 15) & ~15, stride = Rp + 4, plane = RB * kBlock * stride;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t block = item / tiles, m0 = block * kBlock;
-    const int64_t n0 = ((item - block * tiles) * kWaves + wave) * kTileCols;
-    const bool low_out = T != nullptr && n0 == 0;  // this wave also writes T
-    if (n0 >= C) continue;
-    const int64_t c = n0 / 8 + l;  // the lane's chunk of eight columns
-    const int n = static_cast<int>(max(int64_t(0), min(int64_t(8), C - 8 * c)));
-    const int id = token_adapter(ad, m0, M, lane);
-    const float* trow = parts + min(m0 + l, M - 1) * Rp + 4 * g;
-    auto add_row = [&](int64_t m, const float (&d)[8]) {
-      char* y = reinterpret_cast<char*>(Y + m * C + n0) + 32 * l;
-      float v[8];
-      if (accumulate && n > 0) {
-        chunk_f32<kF32>(n == 8 ? load_chunk<kF32, false>(y, nullptr, 8, 0, 8) : load_chunk<kF32, true>(y, nullptr, n, 0, n), v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], d[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = d[j];
+    const int64_t group = item / tiles, tile = item - group * tiles, m0 = group * (RB * kBlock);
+    for (int i = threadIdx.x; i < RB * kBlock * (Rp / 4); i += kThreads) {
+      const int token = i / (Rp / 4), r = 4 * (i - token * (Rp / 4));
+      const int64_t m = m0 + token;
+      const int id = m < M ? ad.rows[m] : -1;
+      const bool has = id >= 0 && id < ad.A;
+      f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (has) {
+        const float* from = parts + m * Rp + r;
+        t = *reinterpret_cast<const f32x4*>(from);
+#pragma unroll 4
+        for (int s = 1; s < nparts; ++s) t += *reinterpret_cast<const f32x4*>(from + static_cast<int64_t>(s) * M * Rp);
       }
-      store_chunk<kF32>(y, 0, n, v);
-    };
-    each_adapter(id, gridDim.y, blockIdx.y, [&](int a, uint32_t mine) {
-      const float scale = ad.scales[a];
-      f32x4 d[8];
+      if (T != nullptr && tile == 0 && blockIdx.y == 0 && m < M) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int r0 = 0; r0 < ad.R; r0 += 16) {
-        Raw<WT> w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + 4 * g + i;
-          const char* row = W + (static_cast<int64_t>(a) * ad.R + min(r, ad.R - 1)) * C * kBytes<WT>;
-          w[i] = any_chunk<WT>(row, C, c);
-          if (r >= ad.R) w[i] = Raw<WT>{};
-        }
-        f32x4 t = *reinterpret_cast<const f32x4*>(trow + r0);
-        for (int s = 1; s < nparts; ++s) t += *reinterpret_cast<const f32x4*>(trow + static_cast<int64_t>(s) * M * Rp + r0);
-        if (low_out && (mine >> l & 1u)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (r0 + 4 * g + i < ad.R) T[(m0 + l) * ad.R + r0 + 4 * g + i] = t[i];
-        }
-        s16x4 tp[3], wp[kPlanes<WT>][8];
-        value_planes(t * scale, tp);
-        column_planes<WT>(w, wp);
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-#pragma unroll
-          for (int s = 0; s < kPlanes<WT>; ++s)
-            if (p + s <= 2) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                d[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(tp[p], wp[s][j], d[j], 0, 0, 0);
-            }
+        for (int k = 0; k < 4; ++k)
+          if (r + k < ad.R) T[m * ad.R + r + k] = t[k];
       }
+      s16x4 p[3];
+      value_planes(t * (has ? ad.scales[id] : 0.0f), p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v[8] = {d[0][i], d[1][i], d[2][i], d[3][i], d[4][i], d[5][i], d[6][i], d[7][i]};
-        if (mine >> (4 * g + i) & 1u) add_row(m0 + 4 * g + i, v);
-      }
-    });
-    if (blockIdx.y == 0 && (low_out || !accumulate)) {  // tokens without an adapter
-      const uint32_t none = ~static_cast<uint32_t>(__ballot(id >= 0));
-      const float zero[8] = {};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 4 * g + i;
-        if (!accumulate && m < M && (none >> (4 * g + i) & 1u)) add_row(m, zero);
-      }
-      if (low_out && m0 + l < M && (none >> l & 1u))
-        for (int r = g; r < ad.R; r += 4) T[(m0 + l) * ad.R + r] = 0.0f;
+      for (int s = 0; s < 3; ++s) *reinterpret_cast<s16x4*>(low + s * plane + token * stride + r) = p[s];
     }
+    __syncthreads();
+    const int64_t n0 = (tile * kWaves + wave) * kTileCols;
+    if (n0 < C) {
+      const Columns at = lane_columns<8>(C, n0 / 8 + l);
+      const bool inside = n0 + kTileCols <= C;
+      const int id = token_adapter(ad, m0, M, RB * kBlock, lane);
+      // The group's rows of Y as a buffer resource: rows and columns that are not
+      // to be touched lie at an offset past it, where loads give zeros and stores
+      // are dropped, so no row takes a branch.
+      const __amdgpu_buffer_rsrc_t yres = __builtin_amdgcn_make_buffer_rsrc(
+          Y + m0 * C, 0, static_cast<int>(min(M - m0, int64_t(RB * kBlock)) * C * 4), 0x00020000);
+      const uint32_t row_bytes = static_cast<uint32_t>(C) * 4u, y_col = static_cast<uint32_t>(at.first) * 4u;
+      auto y_at = [&](int token, uint64_t rows) {
+        return rows >> token & 1u ? static_cast<uint32_t>(token) * row_bytes + y_col : kNowhere;
+      };
+      auto store_row = [&](uint32_t off, const float (&v)[8]) {
+        if (inside) {
+          __builtin_amdgcn_raw_buffer_store_b128(v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                     __float_as_uint(v[3])}, yres, off, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                                                     __float_as_uint(v[7])}, yres, off + 16u, 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), yres, j >= at.skip ? off + 4u * j : kNowhere, 0,
+                                                  0);
+        }
+      };
+      auto load_w = [&](int a, int r0, Some<WT, 8> (&w)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = load_some<WT, 8>(W + ((static_cast<int64_t>(a) * ad.R + min(r0 + 4 * g + i, ad.R - 1)) * C + at.first) *
+                                          kBytes<WT>);
+      };
+      each_adapter(id, gridDim.y, blockIdx.y, [&](int a, uint64_t mine) {
+        Some<WT, 8> w[4];
+        load_w(a, 0, w);
+        v4u y[kAhead ? RB : 1][4][2];
+        auto load_y = [&](int b, v4u (&v)[4][2]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t off = y_at(kBlock * b + 4 * g + i, mine);
+            v[i][0] = __builtin_amdgcn_raw_buffer_load_b128(yres, off, 0, 0);
+            v[i][1] = __builtin_amdgcn_raw_buffer_load_b128(yres, off + 16u, 0, 0);
+          }
+        };
+        if (kAhead && accumulate) {
+#pragma unroll
+          for (int b = 0; b < RB; ++b) load_y(b, y[b]);
+        }
+        f32x4 d[RB][8];
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r0 = 0; r0 < ad.R; r0 += 16) {
+          if (r0 + 16 > ad.R) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (r0 + 4 * g + i >= ad.R) w[i] = Some<WT, 8>{};
+          }
+          s16x4 wp[kPlanes<WT>][8];
+          column_planes<WT, 8>(w, wp);
+          if (r0 + 16 < ad.R) load_w(a, r0 + 16, w);
+#pragma unroll
+          for (int b = 0; b < RB; ++b) {
+            s16x4 tp[3];
+#pragma unroll
+            for (int s = 0; s < 3; ++s)
+              tp[s] = *reinterpret_cast<const s16x4*>(low + s * plane + (kBlock * b + l) * stride + r0 + 4 * g);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+              for (int s = 0; s < kPlanes<WT>; ++s)
+                if (p + s <= 2) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    d[b][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(tp[p], wp[s][j], d[b][j], 0, 0, 0);
+                }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          if (!kAhead && accumulate) load_y(b, y[0]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              v[j] = accumulate ? __fadd_rn(__uint_as_float(y[kAhead ? b : 0][i][j >> 2][j & 3]), d[b][j][i]) : d[b][j][i];
+            store_row(y_at(kBlock * b + 4 * g + i, mine), v);
+          }
+        }
+      });
+      if (!accumulate && blockIdx.y == 0) {  // tokens without an adapter (the resource ends with the last token)
+        const uint64_t none = ~__ballot(id >= 0);
+        const float zero[8] = {};
+        for (int b = 0; b < RB; ++b)
+          for (int i = 0; i < 4; ++i) store_row(y_at(kBlock * b + 4 * g + i, none), zero);
+      }
+    }
+    __syncthreads();  // the next item's planes overwrite these
   }
 }
 
@@ -341,18 +451,19 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict_
 }
 
 // ---- grad -----------------------------------------------------------------------
-// A workgroup takes 128 columns, one adapter, RT tiles of 16 ranks and one part
+// A workgroup takes 64 columns, one adapter, RT tiles of 16 ranks and one part
 // of the tokens; each of its four waves a quarter of those, 16 tokens at a time
-// (blocks without one of the adapter's are passed over).  V is the row operand
-// (lane l: rank l % 16, tokens 4 (l / 16) .. + 3), X the columns as in expand.
-// The waves' sums meet in LDS, and each wave then writes one of every four ranks,
-// eight consecutive columns to a lane.
+// (blocks without one of the adapter's are passed over), with the next block's
+// loads on their way.  V is the row operand (lane l: rank l % 16, tokens
+// 4 (l / 16) .. + 3), X the columns as in expand.  The waves' sums meet in LDS,
+// and each wave then writes one of every four ranks.
 template <int XT, int RT>
-__global__ __launch_bounds__(kThreads) void grad_kernel(const float* __restrict__ V, const char* __restrict__ X,
+__global__ __launch_bounds__(kThreads, 2) void grad_kernel(const float* __restrict__ V, const char* __restrict__ X,
                                                         int64_t M, int64_t C, Adapters ad, float* __restrict__ out,
                                                         int scaled, int nparts, int64_t items, int64_t tiles,
                                                         int groups) {
-  __shared__ f32x4 sums[kWaves][8][kWave];
+  constexpr int CW = kGradCols;
+  __shared__ f32x4 sums[kWaves][CW][kWave];
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int64_t blocks = (M + kBlock - 1) / kBlock;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -363,78 +474,114 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const float* __restrict_
     rest /= groups;
     const int a = static_cast<int>(rest % ad.A), part = static_cast<int>(rest / ad.A);
     const int r0 = group * 16 * RT;
-    const int64_t c = tile * (kTileCols / 8) + l;
+    const Columns at = lane_columns<CW>(C, tile * 16 + l);
     const int64_t q = static_cast<int64_t>(part) * kWaves + wave, Q = static_cast<int64_t>(nparts) * kWaves;
     const int64_t lo = q * blocks / Q, hi = (q + 1) * blocks / Q;
-    f32x4 acc[RT][8];
+    f32x4 acc[RT][CW];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t b = lo; b < hi; b += 4) {
-      const int64_t mine_at = b * kBlock + lane;
-      const uint64_t here = __ballot(mine_at < min(hi * kBlock, M) && ad.rows[mine_at < M ? mine_at : M - 1] == a);
-      for (int sub = 0; sub < 4; ++sub) {
-        const uint32_t mine = static_cast<uint32_t>(here >> (16 * sub)) & 0xffffu;
-        if (!mine) continue;
-        const int64_t m0 = (b + sub) * kBlock;
-        Raw<XT> x[4];
-        f32x4 v[RT];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t m = min(m0 + 4 * g + i, M - 1);
-          const bool use = mine >> (4 * g + i) & 1u;
-          x[i] = any_chunk<XT>(X + m * C * kBytes<XT>, C, c);
-          if (!use) x[i] = Raw<XT>{};
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const int r = r0 + 16 * t + l;
-            const float e = V[m * ad.R + min(r, ad.R - 1)];
-            v[t][i] = use && r < ad.R ? e : 0.0f;
-          }
+      for (int j = 0; j < CW; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // The adapter's tokens, 64 at a time, the ids of the next 64 already loaded.
+    auto ids_at = [&](int64_t b) {
+      const int64_t m = b * kBlock + lane;
+      return m < min(hi * kBlock, M) ? ad.rows[m] : -1;
+    };
+    int64_t base = lo;
+    int sub = 0;
+    uint64_t here = __ballot(ids_at(lo) == a);
+    int ids_next = ids_at(lo + 4);
+    auto next = [&](uint32_t& mine) -> int64_t {  // the next block that holds one of them, -1 at the end
+      for (;;) {
+        if (sub == 4) {
+          base += 4;
+          sub = 0;
+          here = __ballot(ids_next == a);
+          ids_next = ids_at(base + 4);
         }
-        s16x4 xp[kPlanes<XT>][8];
-        column_planes<XT>(x, xp);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          s16x4 vp[3];
-          value_planes(v[t], vp);
-#pragma unroll
-          for (int p = 0; p < 3; ++p)
-#pragma unroll
-            for (int s = 0; s < kPlanes<XT>; ++s)
-              if (p + s <= 2) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vp[p], xp[s][j], acc[t][j], 0, 0, 0);
-              }
-        }
+        if (base + sub >= hi) return -1;
+        mine = static_cast<uint32_t>(here >> (16 * sub)) & 0xffffu;
+        const int64_t b = base + sub++;
+        if (mine) return b;
       }
+    };
+    auto load = [&](int64_t b, Some<XT, CW> (&xr)[4], float (&vr)[RT][4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t m = min(b * kBlock + 4 * g + i, M - 1);
+        xr[i] = load_some<XT, CW>(X + (m * C + at.first) * kBytes<XT>);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) vr[t][i] = V[m * ad.R + min(r0 + 16 * t + l, ad.R - 1)];
+      }
+    };
+    auto add = [&](uint32_t own, Some<XT, CW> (&xr)[4], float (&vr)[RT][4]) {
+      if (own != 0xffffu) {  // rows of others: zeros on both sides
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!(own >> (4 * g + i) & 1u)) {
+            xr[i] = Some<XT, CW>{};
+#pragma unroll
+            for (int t = 0; t < RT; ++t) vr[t][i] = 0.0f;
+          }
+      }
+      s16x4 xp[kPlanes<XT>][CW];
+      column_planes<XT, CW>(xr, xp);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        s16x4 vp[3];
+        value_planes(f32x4{vr[t][0], vr[t][1], vr[t][2], vr[t][3]}, vp);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int s = 0; s < kPlanes<XT>; ++s)
+            if (p + s <= 2) {
+#pragma unroll
+              for (int j = 0; j < CW; ++j)
+                acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(vp[p], xp[s][j], acc[t][j], 0, 0, 0);
+            }
+      }
+    };
+    Some<XT, CW> x0[4], x1[4];
+    float v0[RT][4], v1[RT][4];
+    uint32_t mine0 = 0u, mine1 = 0u;
+    int64_t b = next(mine0);
+    if (b >= 0) load(b, x0, v0);
+    while (b >= 0) {
+      b = next(mine1);
+      if (b >= 0) load(b, x1, v1);
+      add(mine0, x0, v0);
+      if (b < 0) break;
+      b = next(mine0);
+      if (b >= 0) load(b, x0, v0);
+      add(mine1, x1, v1);
     }
     const float scale = scaled ? ad.scales[a] : 1.0f;
-    const int n = static_cast<int>(max(int64_t(0), min(int64_t(8), C - 8 * c)));
+#pragma unroll
     for (int t = 0; t < RT; ++t) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f32x4 mine = acc[0][j];
-#pragma unroll
-        for (int s = 1; s < RT; ++s) mine = t == s ? acc[s][j] : mine;
-        sums[wave][j][lane] = mine;
-      }
+      for (int j = 0; j < CW; ++j) sums[wave][j][lane] = acc[t][j];
       __syncthreads();
       const int r = r0 + 16 * t + 4 * g + wave;
-      float v[8];
+      if (r >= ad.R) continue;
+      float* to = out + ((static_cast<int64_t>(part) * ad.A + a) * ad.R + r) * C + at.first;
+      float v[CW];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < CW; ++j) {
         float s = reinterpret_cast<const float*>(&sums[0][j][lane])[wave];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) s += reinterpret_cast<const float*>(&sums[w][j][lane])[wave];
         v[j] = __fmul_rn(s, scale);
       }
-      if (r < ad.R && n > 0) {
-        float* to = out + ((static_cast<int64_t>(part) * ad.A + a) * ad.R + r) * C + 8 * c;
-        store_chunk<kF32>(reinterpret_cast<char*>(to), 0, n, v);
+      if (at.skip == 0) {
+#pragma unroll
+        for (int h = 0; h < CW / 4; ++h)
+          *reinterpret_cast<v4u_by4*>(to + 4 * h) = v4u{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                                                        __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])};
+      } else {
+#pragma unroll
+        for (int j = 0; j < CW; ++j)
+          if (j >= at.skip) to[j] = v[j];
       }
     }
     __syncthreads();
@@ -453,24 +600,141 @@ __global__ __launch_bounds__(kThreads) void grad_join_kernel(const float* __rest
   }
 }
 
+// ---- fewer than 8 columns, or more than 2^24 ---------------------------------------
+// A lane's eight columns do not fit, or a group's rows of Y do not fit a buffer
+// resource: one thread to a value, float32 sums.
+template <int DT>
+__device__ __forceinline__ float value_at(const char* p, int64_t i) {
+  if constexpr (DT == kF32) return reinterpret_cast<const float*>(p)[i];
+  else return bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+
+template <int XT, int WT>
+__global__ __launch_bounds__(kThreads) void shrink_short_kernel(const char* __restrict__ X, int64_t M, int64_t C, Adapters ad,
+                                                                const char* __restrict__ W, float* __restrict__ T) {
+  const int Rp = (ad.R + 15) & ~15;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < M * Rp;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t m = i / Rp;
+    const int r = static_cast<int>(i - m * Rp), id = ad.rows[m];
+    float v = 0.0f;
+    if (id >= 0 && id < ad.A && r < ad.R)
+      for (int64_t c = 0; c < C; ++c)
+        v = __fmaf_rn(value_at<XT>(X, m * C + c), value_at<WT>(W, (static_cast<int64_t>(id) * ad.R + r) * C + c), v);
+    T[i] = v;
+  }
+}
+
+template <int WT>
+__global__ __launch_bounds__(kThreads) void expand_short_kernel(const float* __restrict__ parts, int nparts, int64_t M,
+                                                                int64_t C, Adapters ad, const char* __restrict__ W, float* Y,
+                                                                int accumulate) {
+  const int Rp = (ad.R + 15) & ~15;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < M * C;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int64_t m = i / C;
+    const int64_t c = i - m * C;
+    const int id = ad.rows[m];
+    const bool has = id >= 0 && id < ad.A;
+    if (!has) {
+      if (!accumulate) Y[i] = 0.0f;
+      continue;
+    }
+    const float scale = ad.scales[id];
+    float v = 0.0f;
+    for (int r = 0; r < ad.R; ++r) {
+      float t = parts[m * Rp + r];
+      for (int s = 1; s < nparts; ++s) t += parts[(s * M + m) * Rp + r];
+      v = __fmaf_rn(__fmul_rn(t, scale), value_at<WT>(W, (static_cast<int64_t>(id) * ad.R + r) * C + c), v);
+    }
+    Y[i] = accumulate ? __fadd_rn(Y[i], v) : v;
+  }
+}
+
+// one workgroup to a value of dW: its tokens in turn, the threads' sums in LDS
+template <int XT>
+__global__ __launch_bounds__(kThreads) void grad_short_kernel(const float* __restrict__ V, const char* __restrict__ X,
+                                                              int64_t M, int64_t C, Adapters ad, float* __restrict__ dW,
+                                                              int64_t n) {
+  __shared__ float slot[kWaves];
+  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
+    const int64_t row = i / C;
+    const int64_t c = i - row * C;
+    const int a = static_cast<int>(row / ad.R), r = static_cast<int>(row - int64_t(a) * ad.R);
+    float v[1] = {0.0f};
+    for (int64_t m = threadIdx.x; m < M; m += kThreads)
+      if (ad.rows[m] == a) v[0] = __fmaf_rn(V[m * ad.R + r], value_at<XT>(X, m * C + c), v[0]);
+    team_sum<kWaves, 1>(v, slot, wave_id(), threadIdx.x & 63);
+    if (threadIdx.x == 0) dW[i] = __fmul_rn(v[0], ad.scales[a]);
+    __syncthreads();
+  }
+}
+
 unsigned flat_grid(int64_t n) {
   return static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, int64_t(1) << 16));
 }
 
-template <int XT, int WT>
+bool few_or_many(int64_t C) { return C < 8 || C > (int64_t(1) << 24); }
+
+template <int XT, int WT, int RB>
 hipError_t shrink_as(const void* X, int64_t M, int64_t C, const Adapters& ad, const void* W, float* parts,
-                     hipStream_t s) {
-  const ShrinkPlan p = shrink_plan(M, C);
-  const int64_t blocks = (M + kBlock - 1) / kBlock;
-  const dim3 grid(static_cast<unsigned>(std::min(blocks, kMaxGrid)), p.parts, p.spread);
-  auto kernel = ad.R <= 16 ? shrink_kernel<XT, WT, 1> : ad.R <= 32 ? shrink_kernel<XT, WT, 2> : shrink_kernel<XT, WT, 4>;
-  kernel<<<grid, kThreads, 0, s>>>(static_cast<const char*>(X), M, C, ad, static_cast<const char*>(W), parts, blocks);
+                     const ShrinkPlan& p, hipStream_t s) {
+  const int64_t groups = (M + RB * kBlock - 1) / (RB * kBlock);
+  const dim3 grid(static_cast<unsigned>(std::min(groups, kMaxGrid)), p.parts, p.spread);
+  auto kernel = ad.R <= 16   ? shrink_kernel<XT, WT, RB, 1>
+                : ad.R <= 32 ? shrink_kernel<XT, WT, RB, 2>
+                             : shrink_kernel<XT, WT, RB, 4>;
+  kernel<<<grid, kThreads, 0, s>>>(static_cast<const char*>(X), M, C, ad, static_cast<const char*>(W), parts, groups);
   return hipGetLastError();
+}
+
+template <int XT, int WT>
+hipError_t shrink_any(const void* X, int64_t M, int64_t C, const Adapters& ad, const void* W, float* parts,
+                      hipStream_t s) {
+  const ShrinkPlan p = shrink_plan(M, C);
+  if (few_or_many(C)) {
+    shrink_short_kernel<XT, WT><<<flat_grid(M * padded_r(ad.R)), kThreads, 0, s>>>(
+        static_cast<const char*>(X), M, C, ad, static_cast<const char*>(W), parts);
+    return hipGetLastError();
+  }
+  return p.blocks == 4 ? shrink_as<XT, WT, 4>(X, M, C, ad, W, parts, p, s)
+                       : shrink_as<XT, WT, 1>(X, M, C, ad, W, parts, p, s);
+}
+
+template <int WT, int RB>
+hipError_t expand_as(const float* parts, int nparts, int spread, int64_t M, int64_t C, const Adapters& ad,
+                     const void* W, float* Y, bool accumulate, float* T, hipStream_t s) {
+  const int64_t groups = (M + RB * kBlock - 1) / (RB * kBlock);
+  const int64_t tiles = (C + kWaves * kTileCols - 1) / (kWaves * kTileCols), items = groups * tiles;
+  const dim3 grid(static_cast<unsigned>(std::min(items, kMaxGrid)), spread);
+  const size_t lds = size_t(3) * RB * kBlock * (padded_r(ad.R) + 4) * 2;
+  expand_kernel<WT, RB><<<grid, kThreads, lds, s>>>(parts, nparts, M, C, ad, static_cast<const char*>(W), Y, accumulate,
+                                                    T, items, tiles);
+  return hipGetLastError();
+}
+
+template <int WT>
+hipError_t expand_any(const float* parts, int64_t M, int64_t C0, int64_t C, const Adapters& ad, const void* W, float* Y,
+                      bool accumulate, float* T, hipStream_t s) {
+  const ShrinkPlan p = shrink_plan(M, C0);
+  if (few_or_many(C)) {
+    expand_short_kernel<WT><<<flat_grid(M * C), kThreads, 0, s>>>(parts, p.parts, M, C, ad,
+                                                                 static_cast<const char*>(W), Y, accumulate);
+    return T ? launch_join(parts, M, C0, ad, T, s) : hipGetLastError();
+  }
+  return expand_blocks(M, C) == 2 ? expand_as<WT, 2>(parts, p.parts, 1, M, C, ad, W, Y, accumulate, T, s)
+                                  : expand_as<WT, 1>(parts, p.parts, p.spread, M, C, ad, W, Y, accumulate, T, s);
 }
 
 template <int XT>
 hipError_t grad_as(const float* V, const void* X, int64_t M, int64_t C, const Adapters& ad, float* dW, float* ws,
                    hipStream_t s) {
+  if (few_or_many(C)) {
+    const int64_t n = int64_t(ad.A) * ad.R * C;
+    grad_short_kernel<XT><<<static_cast<unsigned>(std::min(n, kMaxGrid)), kThreads, 0, s>>>(
+        V, static_cast<const char*>(X), M, C, ad, dW, n);
+    return hipGetLastError();
+  }
   const GradPlan p = grad_plan(M, C, ad.A, ad.R);
   const int64_t items = int64_t(p.tiles) * p.groups * ad.A * p.parts;
   const unsigned grid = static_cast<unsigned>(std::min(items, kMaxGrid));
@@ -490,22 +754,16 @@ hipError_t grad_as(const float* V, const void* X, int64_t M, int64_t C, const Ad
 hipError_t launch_shrink(const void* X, int x_dtype, int64_t M, int64_t C, const Adapters& ad, const void* W,
                          float* parts, hipStream_t s) {
   if (x_dtype == kF32)
-    return ad.w_dtype == kF32 ? shrink_as<kF32, kF32>(X, M, C, ad, W, parts, s)
-                              : shrink_as<kF32, kBf16>(X, M, C, ad, W, parts, s);
-  return ad.w_dtype == kF32 ? shrink_as<kBf16, kF32>(X, M, C, ad, W, parts, s)
-                            : shrink_as<kBf16, kBf16>(X, M, C, ad, W, parts, s);
+    return ad.w_dtype == kF32 ? shrink_any<kF32, kF32>(X, M, C, ad, W, parts, s)
+                              : shrink_any<kF32, kBf16>(X, M, C, ad, W, parts, s);
+  return ad.w_dtype == kF32 ? shrink_any<kBf16, kF32>(X, M, C, ad, W, parts, s)
+                            : shrink_any<kBf16, kBf16>(X, M, C, ad, W, parts, s);
 }
 
 hipError_t launch_expand(const float* parts, int64_t M, int64_t C0, int64_t C, const Adapters& ad, const void* W,
                          float* Y, bool accumulate, float* T, hipStream_t s) {
-  const ShrinkPlan p = shrink_plan(M, C0);
-  const int64_t blocks = (M + kBlock - 1) / kBlock, tiles = (C + kWaves * kTileCols - 1) / (kWaves * kTileCols);
-  const int64_t items = blocks * tiles;
-  const dim3 grid(static_cast<unsigned>(std::min(items, kMaxGrid)), p.spread);
-  auto kernel = ad.w_dtype == kF32 ? expand_kernel<kF32> : expand_kernel<kBf16>;
-  kernel<<<grid, kThreads, 0, s>>>(parts, p.parts, M, C, ad, static_cast<const char*>(W), Y, accumulate, T, items,
-                                   tiles);
-  return hipGetLastError();
+  return ad.w_dtype == kF32 ? expand_any<kF32>(parts, M, C0, C, ad, W, Y, accumulate, T, s)
+                            : expand_any<kBf16>(parts, M, C0, C, ad, W, Y, accumulate, T, s);
 }
 
 hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, hipStream_t s) {
