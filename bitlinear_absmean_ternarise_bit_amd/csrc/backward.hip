@@ -30,9 +30,6 @@ namespace bitlinear {
 
 namespace {
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kTile = 64;  // transpose / pack tiles
 
 __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
@@ -414,7 +411,7 @@ hipError_t launch_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, 
     // dY's rows serve as they are when they start on 16-byte boundaries
     const bool direct = N % 8 == 0 && reinterpret_cast<uintptr_t>(dY) % 16 == 0;
     if (!direct) {
-      int64_t blocks = (M * Np + 255) / 256;
+      int64_t blocks = (M * (Np / 8) + 255) / 256;
       if (blocks > 65536) blocks = 65536;
       pad_rows_bf16_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(dY, M, N, dYp, Np);
     }

@@ -4,6 +4,7 @@
 
 #include <type_traits>
 
+#include "block_device.hpp"
 #include "kernels.hpp"
 
 namespace bitlinear {
@@ -13,14 +14,20 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 namespace {
 
-// dYp[m, n] = dY[m, n] for n < N, 0 for N <= n < Np (bf16 bit patterns).
+// dYp[m, n] = dY[m, n] for n < N, 0 for N <= n < Np (bf16 bit patterns; Np a
+// multiple of 64): a thread to 8 columns, read at any address (2048x4097: value
+// by value 20 us, this 9).
 __global__ __launch_bounds__(256) void pad_rows_bf16_kernel(const uint16_t* __restrict__ src, int64_t M, int64_t N,
                                                             uint16_t* __restrict__ dst, int64_t Np) {
-  const int64_t total = M * Np;
+  const int64_t per_row = Np >> 3, total = M * per_row;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t m = i / Np, n = i - m * Np;
-    dst[i] = n < N ? src[m * N + n] : static_cast<uint16_t>(0);
+    const int64_t m = i / per_row;
+    const int c = static_cast<int>(i - m * per_row), n = chunk_values(static_cast<int>(N), c);
+    const char* row = reinterpret_cast<const char*>(src + m * N);
+    const Raw<kBf16> r = N >= 8 ? load_chunk<kBf16, false>(row, nullptr, static_cast<int>(N), c, n)
+                                : load_chunk<kBf16, true>(row, nullptr, static_cast<int>(N), c, n);
+    *reinterpret_cast<v4u*>(dst + 8 * i) = r.a;
   }
 }
 

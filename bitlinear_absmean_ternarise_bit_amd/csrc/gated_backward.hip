@@ -90,7 +90,7 @@ hipError_t launch_gated_input_backward(const uint16_t* dG, const uint16_t* dU, i
   if (copies) {
     uint16_t* a = static_cast<uint16_t*>(copies);
     uint16_t* b = a + backward_ws_part(M, Fp) / 2;
-    int64_t blocks = (M * Fp + 255) / 256;
+    int64_t blocks = (M * (Fp / 8) + 255) / 256;
     if (blocks > 65536) blocks = 65536;
     pad_rows_bf16_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(dG, M, F, a, Fp);
     pad_rows_bf16_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(dU, M, F, b, Fp);
@@ -100,9 +100,16 @@ hipError_t launch_gated_input_backward(const uint16_t* dG, const uint16_t* dU, i
   }
   const int bytes_a = static_cast<int>(M * lda * 2), bytes_b = static_cast<int>(D * (Fp / 4));
   const SecondProduct second = {dU, packedT_up, gamma_up};
-  const int tiles_p = static_cast<int>((M + 255) / 256), tiles_q = static_cast<int>((D + 127) / 128);
-  bf16_two_products_kernel<256, 128, 4, 2><<<static_cast<unsigned>(tiles_p * tiles_q), 512, 0, stream>>>(
-      dG, M, lda, packedT_gate, D, Fp, dX, gamma_gate, bytes_a, bytes_b, tiles_p, tiles_q, second);
+  // the largest tile that still makes a workgroup for most CUs
+  auto tiles = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((D + bn - 1) / bn); };
+  auto go = [&](auto kernel, int bm, int bn, int threads) {
+    const int tiles_p = static_cast<int>((M + bm - 1) / bm), tiles_q = static_cast<int>((D + bn - 1) / bn);
+    kernel<<<static_cast<unsigned>(tiles_p * tiles_q), threads, 0, stream>>>(
+        dG, M, lda, packedT_gate, D, Fp, dX, gamma_gate, bytes_a, bytes_b, tiles_p, tiles_q, second);
+  };
+  if (tiles(256, 128) >= 192) go(bf16_two_products_kernel<256, 128, 4, 2>, 256, 128, 512);
+  else if (tiles(128, 128) >= 128) go(bf16_two_products_kernel<128, 128, 2, 2>, 128, 128, 256);
+  else go(bf16_two_products_kernel<64, 64, 1, 2>, 64, 64, 128);
   return hipGetLastError();
 }
 
