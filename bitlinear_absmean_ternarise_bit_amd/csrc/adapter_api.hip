@@ -94,7 +94,14 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
                       floats(scales, A)};
   if (any_overlap(out, in)) return BITLINEAR_ERR_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  const Adapters ad = {rows, scales, static_cast<int>(A), static_cast<int>(R), w_dtype};
+  const int64_t piece = path == BITLINEAR_PATH_PREFILL ? 0 : adapted_decode_piece(M, K, N);
   hipError_t e;
+  if (piece) {
+    float* parts = static_cast<float*>(workspace);
+    e = launch_adapted_decode(X, x_dtype, M, K, packed, N, gamma, Y, ad, down, parts, piece, s);
+    return hip_status(e == hipSuccess ? launch_expand(parts, M, K, N, ad, up, Y, true, T, s) : e);
+  }
   if (decode) {
     e = launch_decode(X, x_dtype, M, K, packed, N, gamma, Y, nullptr, 1, s);
   } else {
@@ -103,7 +110,6 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
     if (e == hipSuccess) e = launch_prefill_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, nullptr, s);
   }
   if (e != hipSuccess) return BITLINEAR_ERR_HIP;
-  const Adapters ad = {rows, scales, static_cast<int>(A), static_cast<int>(R), w_dtype};
   return add_adapters(X, x_dtype, M, K, N, ad, down, up, Y, T, workspace, s);
 }
 

@@ -21,267 +21,18 @@
 // adapters are zeros on both sides by selection, not by multiplication.
 #include <algorithm>
 
-#include "adapter_ops.hpp"
-#include "block_device.hpp"
+#include "adapter_device.hpp"
 
 namespace bitlinear {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kThreads = 256, kWaves = 4;
-constexpr int kBlock = 16;      // tokens of a block
-constexpr int kTileCols = 128;  // columns of a wave in expand
-constexpr int kGradCols = 4;    // columns of a lane in grad
-constexpr int64_t kMaxGrid = int64_t(1) << 20;  // workgroups; each walks every gridDim.x-th item
-
-template <int DT>
-constexpr int kPlanes = DT == kF32 ? 3 : 1;
-
-// upper or lower halves of two words, the first one's in the lower half
-__device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
-__device__ __forceinline__ uint32_t lower(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
-
-// Planes of two float32: what truncation leaves is exact each time, and the third
-// plane holds the last 8 bits.
-__device__ __forceinline__ void split(float a, float b, uint32_t (&p)[3]) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    p[i] = upper(ua, ub);
-    a = __fsub_rn(a, __uint_as_float(ua & 0xffff0000u));
-    b = __fsub_rn(b, __uint_as_float(ub & 0xffff0000u));
-  }
-}
-
-// CW consecutive values at p, aligned to their type only.
-template <int DT, int CW>
-struct Some;  // as they lie in memory: CW / 2 words of bfloat16, CW of float32
-template <int CW>
-struct Some<kF32, CW> {
-  uint32_t w[CW];
-};
-template <int CW>
-struct Some<kBf16, CW> {
-  uint32_t w[CW / 2];
-};
-typedef v2u v2u_by2 __attribute__((aligned(2)));
-template <int DT, int CW>
-__device__ __forceinline__ Some<DT, CW> load_some(const char* p) {
-  Some<DT, CW> r;
-  if constexpr (DT == kBf16 && CW == 4) {
-    const v2u a = *reinterpret_cast<const v2u_by2*>(p);
-    r.w[0] = a.x, r.w[1] = a.y;
-  } else if constexpr (DT == kBf16) {
-    const v4u a = *reinterpret_cast<const v4u_by2*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.w[i] = a[i];
-  } else {
-#pragma unroll
-    for (int h = 0; h < CW / 4; ++h) {
-      const v4u a = *reinterpret_cast<const v4u_by4*>(p + 16 * h);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.w[4 * h + i] = a[i];
-    }
-  }
-  return r;
-}
-
-// A lane's CW columns of a row of C >= CW: chunk c, or the row's last CW columns
-// where the chunk is cut by the row's end or behind it.  Every load is then whole,
-// without a branch, and column j of the lane is its own where j >= `skip` (CW:
-// none): each column of the row has one owner.
-struct Columns {
-  int64_t first;
-  int skip;
-};
-template <int CW>
-__device__ __forceinline__ Columns lane_columns(int64_t C, int64_t c) {
-  const int64_t over = CW * (c + 1) - C;
-  return {over > 0 ? C - CW : CW * c, static_cast<int>(max(int64_t(0), min(over, int64_t(CW))))};
-}
-
-// Eight consecutive values of a row as operand planes (shrink).
-template <int DT>
-__device__ __forceinline__ void row_planes(const Some<DT, 8>& r, bf16x8 (&p)[kPlanes<DT>]) {
-  if constexpr (DT == kBf16) {
-    p[0] = __builtin_bit_cast(bf16x8, v4u{r.w[0], r.w[1], r.w[2], r.w[3]});
-  } else {
-    v4u w[3];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t s[3];
-      split(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]), s);
-#pragma unroll
-      for (int q = 0; q < 3; ++q) w[q][i] = s[q];
-    }
-#pragma unroll
-    for (int q = 0; q < 3; ++q) p[q] = __builtin_bit_cast(bf16x8, w[q]);
-  }
-}
-
-// Four rows of CW columns as the operand planes of each column: element i of
-// plane q of column j is row i's (expand, grad: rows are the contraction).
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-template <int DT, int CW>
-__device__ __forceinline__ void column_planes(const Some<DT, CW> (&r)[4], s16x4 (&p)[kPlanes<DT>][CW]) {
-  if constexpr (DT == kBf16) {
-#pragma unroll
-    for (int h = 0; h < CW / 2; ++h) {
-      p[0][2 * h] = __builtin_bit_cast(s16x4, u32x2{lower(r[0].w[h], r[1].w[h]), lower(r[2].w[h], r[3].w[h])});
-      p[0][2 * h + 1] = __builtin_bit_cast(s16x4, u32x2{upper(r[0].w[h], r[1].w[h]), upper(r[2].w[h], r[3].w[h])});
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < CW; ++j) {
-      uint32_t lo[3], hi[3];
-      split(__uint_as_float(r[0].w[j]), __uint_as_float(r[1].w[j]), lo);
-      split(__uint_as_float(r[2].w[j]), __uint_as_float(r[3].w[j]), hi);
-#pragma unroll
-      for (int q = 0; q < 3; ++q) p[q][j] = __builtin_bit_cast(s16x4, u32x2{lo[q], hi[q]});
-    }
-  }
-}
-
-// Four float32 as operand planes.
-__device__ __forceinline__ void value_planes(const f32x4& v, s16x4 (&p)[3]) {
-  uint32_t lo[3], hi[3];
-  split(v[0], v[1], lo);
-  split(v[2], v[3], hi);
-#pragma unroll
-  for (int q = 0; q < 3; ++q) p[q] = __builtin_bit_cast(s16x4, u32x2{lo[q], hi[q]});
-}
-
-// The adapter of token m0 + lane, -1 for none; `tokens`: those of the group.
-__device__ __forceinline__ int token_adapter(const Adapters& ad, int64_t m0, int64_t M, int tokens, int lane) {
-  const int64_t m = m0 + lane;
-  const int id = lane < tokens && m < M ? ad.rows[m] : -1;
-  return id >= 0 && id < ad.A ? id : -1;
-}
-
-// Calls f(a, mine) for the adapters of a group of up to 64 tokens, every
-// `spread`-th one from `from`: mine has bit t set where token t is a's.  The
-// same for all lanes.
-template <typename F>
-__device__ __forceinline__ void each_adapter(int id, int spread, int from, F&& f) {
-  uint64_t todo = __ballot(id >= 0);
-  for (int n = 0; todo; ++n) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-    const uint64_t mine = __ballot(id == a);
-    todo &= ~mine;
-    if (n % spread == from) f(a, mine);
-  }
-}
-
-// ---- shrink ---------------------------------------------------------------------
-// A workgroup takes RB blocks of 16 tokens, one part of the columns and every
-// spread-th adapter of those tokens; its four waves share the part's columns in
-// steps of 32 (v_mfma_f32_16x16x32_bf16: lane l holds token or rank row l % 16,
-// columns 8 (l / 16) .. + 7) and add their sums in LDS.  RT tiles of 16 ranks at
-// a time.  With RB = 4 a step's rows of W are read, and split into planes, once
-// for 64 tokens; with few tokens RB = 1 makes more workgroups.
 template <int XT, int WT, int RB, int RT>
-__global__ __launch_bounds__(kThreads, 2) void shrink_kernel(const char* __restrict__ X, int64_t M, int64_t C, Adapters ad,
-                                                          const char* __restrict__ W, float* __restrict__ parts,
-                                                          int64_t groups) {
-  __shared__ f32x4 sums[kWaves][RB * RT][kWave];
-  const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-  const int Rp = (ad.R + 15) & ~15;
-  const int64_t steps = (C + 31) / 32, whole = C / 32;
-  const int64_t q = static_cast<int64_t>(blockIdx.y) * kWaves + wave, Q = static_cast<int64_t>(gridDim.y) * kWaves;
-  const int64_t lo = q * steps / Q, hi = (q + 1) * steps / Q;
-  for (int64_t group = blockIdx.x; group < groups; group += gridDim.x) {
-    const int64_t m0 = group * (RB * kBlock);
-    const char* xrow[RB];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) xrow[b] = X + min(m0 + kBlock * b + l, M - 1) * C * kBytes<XT>;
-    float* out = parts + (static_cast<int64_t>(blockIdx.y) * M + m0) * Rp;
-    each_adapter(token_adapter(ad, m0, M, RB * kBlock, lane), gridDim.z, blockIdx.z, [&](int a, uint64_t mine) {
-      for (int r0 = 0; r0 < ad.R; r0 += 16 * RT) {
-        f32x4 acc[RB][RT];
-        const char* wrow[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-#pragma unroll
-          for (int b = 0; b < RB; ++b) acc[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          wrow[t] = W + (static_cast<int64_t>(a) * ad.R + min(r0 + 16 * t + l, ad.R - 1)) * C * kBytes<WT>;
-        }
-        auto add = [&](const Some<XT, 8> (&xr)[RB], const Some<WT, 8> (&wr)[RT]) {
-          bf16x8 w[RT][kPlanes<WT>];
-#pragma unroll
-          for (int t = 0; t < RT; ++t) row_planes<WT>(wr[t], w[t]);
-#pragma unroll
-          for (int b = 0; b < RB; ++b) {
-            bf16x8 x[kPlanes<XT>];
-            row_planes<XT>(xr[b], x);
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-              for (int p = 0; p < kPlanes<XT>; ++p)
-#pragma unroll
-                for (int s = 0; s < kPlanes<WT>; ++s)
-                  if (p + s <= 2) acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[p], w[t][s], acc[b][t], 0, 0, 0);
-          }
-        };
-        auto load = [&](int64_t col, Some<XT, 8> (&xr)[RB], Some<WT, 8> (&wr)[RT]) {
-#pragma unroll
-          for (int b = 0; b < RB; ++b) xr[b] = load_some<XT, 8>(xrow[b] + col * kBytes<XT>);
-#pragma unroll
-          for (int t = 0; t < RT; ++t) wr[t] = load_some<WT, 8>(wrow[t] + col * kBytes<WT>);
-        };
-        const int64_t end = min(hi, whole);
-#pragma unroll 2
-        for (int64_t st = lo; st < end; ++st) {
-          Some<XT, 8> xr[RB];
-          Some<WT, 8> wr[RT];
-          load(32 * st + 8 * g, xr, wr);
-          add(xr, wr);
-        }
-        if (whole >= lo && whole < hi) {
-          // the step that the row's end cuts: columns that are not the lane's own
-          // meet zeros (their weights are this row's too: they can make nothing
-          // non-finite that is not so anyway)
-          const Columns at = lane_columns<8>(C, 4 * whole + g);
-          Some<XT, 8> xr[RB];
-          Some<WT, 8> wr[RT];
-          load(at.first, xr, wr);
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if constexpr (XT == kF32) {
-                if (j < at.skip) xr[b].w[j] = 0u;
-              } else {
-                if (j < at.skip) xr[b].w[j / 2] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
-              }
-            }
-          add(xr, wr);
-        }
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int t = 0; t < RT; ++t) sums[wave][b * RT + t][lane] = acc[b][t];
-        __syncthreads();
-        for (int i = wave; i < RB * RT; i += kWaves) {
-          f32x4 v = sums[0][i][lane];
-#pragma unroll
-          for (int w = 1; w < kWaves; ++w) v += sums[w][i][lane];
-          const int b = i / RT, r = r0 + 16 * (i - b * RT) + l;
-          if (r < Rp) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int token = kBlock * b + 4 * g + k;
-              if (mine >> token & 1u) out[static_cast<int64_t>(token) * Rp + r] = r < ad.R ? v[k] : 0.0f;
-            }
-          }
-        }
-        __syncthreads();
-      }
-    });
-  }
+__global__ __launch_bounds__(kAdapterThreads, 2) void shrink_kernel(const char* __restrict__ X, int64_t M, int64_t C,
+                                                                    Adapters ad, const char* __restrict__ W,
+                                                                    float* __restrict__ parts, int64_t groups) {
+  shrink_body<XT, WT, RB, RT>(X, M, C, ad, W, parts, groups, blockIdx.x, gridDim.x, blockIdx.y, gridDim.y, blockIdx.z,
+                              gridDim.z);
 }
 
 // ---- expand ---------------------------------------------------------------------
@@ -295,7 +46,7 @@ __global__ __launch_bounds__(kThreads, 2) void shrink_kernel(const char* __restr
 // ends with eight consecutive columns of four tokens of each block, which it adds
 // to Y.
 template <int WT, int RB>
-__global__ __launch_bounds__(kThreads, 2) void expand_kernel(const float* __restrict__ parts, int nparts, int64_t M,
+__global__ __launch_bounds__(kAdapterThreads, 2) void expand_kernel(const float* __restrict__ parts, int nparts, int64_t M,
                                                           int64_t C, Adapters ad, const char* __restrict__ W, float* Y,
                                                           int accumulate, float* __restrict__ T, int64_t items,
                                                           int64_t tiles) {
@@ -307,7 +58,7 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(const float* __rest
   const int Rp = (ad.R + 15) & ~15, stride = Rp + 4, plane = RB * kBlock * stride;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t group = item / tiles, tile = item - group * tiles, m0 = group * (RB * kBlock);
-    for (int i = threadIdx.x; i < RB * kBlock * (Rp / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < RB * kBlock * (Rp / 4); i += kAdapterThreads) {
       const int token = i / (Rp / 4), r = 4 * (i - token * (Rp / 4));
       const int64_t m = m0 + token;
       const int id = m < M ? ad.rows[m] : -1;
@@ -330,7 +81,7 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(const float* __rest
       for (int s = 0; s < 3; ++s) *reinterpret_cast<s16x4*>(low + s * plane + token * stride + r) = p[s];
     }
     __syncthreads();
-    const int64_t n0 = (tile * kWaves + wave) * kTileCols;
+    const int64_t n0 = (tile * kAdapterWaves + wave) * kTileCols;
     if (n0 < C) {
       const Columns at = lane_columns<8>(C, n0 / 8 + l);
       const bool inside = n0 + kTileCols <= C;
@@ -435,12 +186,12 @@ __global__ __launch_bounds__(kThreads, 2) void expand_kernel(const float* __rest
 }
 
 // T[m, r] from its parts, zeros for rows without an adapter.
-__global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict__ parts, int nparts, int64_t M,
+__global__ __launch_bounds__(kAdapterThreads) void join_kernel(const float* __restrict__ parts, int nparts, int64_t M,
                                                         Adapters ad, float* __restrict__ T) {
   const int Rp = (ad.R + 15) & ~15;
   const int64_t n = M * ad.R;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAdapterThreads + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kAdapterThreads) {
     const int64_t m = i / ad.R;
     const int id = ad.rows[m];
     float v = 0.0f;
@@ -458,12 +209,12 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict_
 // 4 (l / 16) .. + 3), X the columns as in expand.  The waves' sums meet in LDS,
 // and each wave then writes one of every four ranks.
 template <int XT, int RT>
-__global__ __launch_bounds__(kThreads, 2) void grad_kernel(const float* __restrict__ V, const char* __restrict__ X,
+__global__ __launch_bounds__(kAdapterThreads, 2) void grad_kernel(const float* __restrict__ V, const char* __restrict__ X,
                                                         int64_t M, int64_t C, Adapters ad, float* __restrict__ out,
                                                         int scaled, int nparts, int64_t items, int64_t tiles,
                                                         int groups) {
   constexpr int CW = kGradCols;
-  __shared__ f32x4 sums[kWaves][CW][kWave];
+  __shared__ f32x4 sums[kAdapterWaves][CW][kWave];
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int64_t blocks = (M + kBlock - 1) / kBlock;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -475,7 +226,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(const float* __restri
     const int a = static_cast<int>(rest % ad.A), part = static_cast<int>(rest / ad.A);
     const int r0 = group * 16 * RT;
     const Columns at = lane_columns<CW>(C, tile * 16 + l);
-    const int64_t q = static_cast<int64_t>(part) * kWaves + wave, Q = static_cast<int64_t>(nparts) * kWaves;
+    const int64_t q = static_cast<int64_t>(part) * kAdapterWaves + wave, Q = static_cast<int64_t>(nparts) * kAdapterWaves;
     const int64_t lo = q * blocks / Q, hi = (q + 1) * blocks / Q;
     f32x4 acc[RT][CW];
 #pragma unroll
@@ -570,7 +321,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(const float* __restri
       for (int j = 0; j < CW; ++j) {
         float s = reinterpret_cast<const float*>(&sums[0][j][lane])[wave];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) s += reinterpret_cast<const float*>(&sums[w][j][lane])[wave];
+        for (int w = 1; w < kAdapterWaves; ++w) s += reinterpret_cast<const float*>(&sums[w][j][lane])[wave];
         v[j] = __fmul_rn(s, scale);
       }
       if (at.skip == 0) {
@@ -589,11 +340,11 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(const float* __restri
 }
 
 // dW = scale * the sum of its parts
-__global__ __launch_bounds__(kThreads) void grad_join_kernel(const float* __restrict__ parts, int nparts, int64_t n,
+__global__ __launch_bounds__(kAdapterThreads) void grad_join_kernel(const float* __restrict__ parts, int nparts, int64_t n,
                                                              int64_t per_adapter, const float* __restrict__ scales,
                                                              float* __restrict__ dW) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAdapterThreads + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * kAdapterThreads) {
     float v = parts[i];
     for (int s = 1; s < nparts; ++s) v += parts[s * n + i];
     dW[i] = __fmul_rn(v, scales[i / per_adapter]);
@@ -610,11 +361,11 @@ __device__ __forceinline__ float value_at(const char* p, int64_t i) {
 }
 
 template <int XT, int WT>
-__global__ __launch_bounds__(kThreads) void shrink_short_kernel(const char* __restrict__ X, int64_t M, int64_t C, Adapters ad,
+__global__ __launch_bounds__(kAdapterThreads) void shrink_short_kernel(const char* __restrict__ X, int64_t M, int64_t C, Adapters ad,
                                                                 const char* __restrict__ W, float* __restrict__ T) {
   const int Rp = (ad.R + 15) & ~15;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < M * Rp;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAdapterThreads + threadIdx.x; i < M * Rp;
+       i += static_cast<int64_t>(gridDim.x) * kAdapterThreads) {
     const int64_t m = i / Rp;
     const int r = static_cast<int>(i - m * Rp), id = ad.rows[m];
     float v = 0.0f;
@@ -626,12 +377,12 @@ __global__ __launch_bounds__(kThreads) void shrink_short_kernel(const char* __re
 }
 
 template <int WT>
-__global__ __launch_bounds__(kThreads) void expand_short_kernel(const float* __restrict__ parts, int nparts, int64_t M,
+__global__ __launch_bounds__(kAdapterThreads) void expand_short_kernel(const float* __restrict__ parts, int nparts, int64_t M,
                                                                 int64_t C, Adapters ad, const char* __restrict__ W, float* Y,
                                                                 int accumulate) {
   const int Rp = (ad.R + 15) & ~15;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < M * C;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAdapterThreads + threadIdx.x; i < M * C;
+       i += static_cast<int64_t>(gridDim.x) * kAdapterThreads) {
     const int64_t m = i / C;
     const int64_t c = i - m * C;
     const int id = ad.rows[m];
@@ -653,25 +404,25 @@ __global__ __launch_bounds__(kThreads) void expand_short_kernel(const float* __r
 
 // one workgroup to a value of dW: its tokens in turn, the threads' sums in LDS
 template <int XT>
-__global__ __launch_bounds__(kThreads) void grad_short_kernel(const float* __restrict__ V, const char* __restrict__ X,
+__global__ __launch_bounds__(kAdapterThreads) void grad_short_kernel(const float* __restrict__ V, const char* __restrict__ X,
                                                               int64_t M, int64_t C, Adapters ad, float* __restrict__ dW,
                                                               int64_t n) {
-  __shared__ float slot[kWaves];
+  __shared__ float slot[kAdapterWaves];
   for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
     const int64_t row = i / C;
     const int64_t c = i - row * C;
     const int a = static_cast<int>(row / ad.R), r = static_cast<int>(row - int64_t(a) * ad.R);
     float v[1] = {0.0f};
-    for (int64_t m = threadIdx.x; m < M; m += kThreads)
+    for (int64_t m = threadIdx.x; m < M; m += kAdapterThreads)
       if (ad.rows[m] == a) v[0] = __fmaf_rn(V[m * ad.R + r], value_at<XT>(X, m * C + c), v[0]);
-    team_sum<kWaves, 1>(v, slot, wave_id(), threadIdx.x & 63);
+    team_sum<kAdapterWaves, 1>(v, slot, wave_id(), threadIdx.x & 63);
     if (threadIdx.x == 0) dW[i] = __fmul_rn(v[0], ad.scales[a]);
     __syncthreads();
   }
 }
 
 unsigned flat_grid(int64_t n) {
-  return static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, int64_t(1) << 16));
+  return static_cast<unsigned>(std::min<int64_t>((n + kAdapterThreads - 1) / kAdapterThreads, int64_t(1) << 16));
 }
 
 bool few_or_many(int64_t C) { return C < 8 || C > (int64_t(1) << 24); }
@@ -684,7 +435,7 @@ hipError_t shrink_as(const void* X, int64_t M, int64_t C, const Adapters& ad, co
   auto kernel = ad.R <= 16   ? shrink_kernel<XT, WT, RB, 1>
                 : ad.R <= 32 ? shrink_kernel<XT, WT, RB, 2>
                              : shrink_kernel<XT, WT, RB, 4>;
-  kernel<<<grid, kThreads, 0, s>>>(static_cast<const char*>(X), M, C, ad, static_cast<const char*>(W), parts, groups);
+  kernel<<<grid, kAdapterThreads, 0, s>>>(static_cast<const char*>(X), M, C, ad, static_cast<const char*>(W), parts, groups);
   return hipGetLastError();
 }
 
@@ -693,7 +444,7 @@ hipError_t shrink_any(const void* X, int64_t M, int64_t C, const Adapters& ad, c
                       hipStream_t s) {
   const ShrinkPlan p = shrink_plan(M, C);
   if (few_or_many(C)) {
-    shrink_short_kernel<XT, WT><<<flat_grid(M * padded_r(ad.R)), kThreads, 0, s>>>(
+    shrink_short_kernel<XT, WT><<<flat_grid(M * padded_r(ad.R)), kAdapterThreads, 0, s>>>(
         static_cast<const char*>(X), M, C, ad, static_cast<const char*>(W), parts);
     return hipGetLastError();
   }
@@ -705,10 +456,10 @@ template <int WT, int RB>
 hipError_t expand_as(const float* parts, int nparts, int spread, int64_t M, int64_t C, const Adapters& ad,
                      const void* W, float* Y, bool accumulate, float* T, hipStream_t s) {
   const int64_t groups = (M + RB * kBlock - 1) / (RB * kBlock);
-  const int64_t tiles = (C + kWaves * kTileCols - 1) / (kWaves * kTileCols), items = groups * tiles;
+  const int64_t tiles = (C + kAdapterWaves * kTileCols - 1) / (kAdapterWaves * kTileCols), items = groups * tiles;
   const dim3 grid(static_cast<unsigned>(std::min(items, kMaxGrid)), spread);
   const size_t lds = size_t(3) * RB * kBlock * (padded_r(ad.R) + 4) * 2;
-  expand_kernel<WT, RB><<<grid, kThreads, lds, s>>>(parts, nparts, M, C, ad, static_cast<const char*>(W), Y, accumulate,
+  expand_kernel<WT, RB><<<grid, kAdapterThreads, lds, s>>>(parts, nparts, M, C, ad, static_cast<const char*>(W), Y, accumulate,
                                                     T, items, tiles);
   return hipGetLastError();
 }
@@ -718,7 +469,7 @@ hipError_t expand_any(const float* parts, int64_t M, int64_t C0, int64_t C, cons
                       bool accumulate, float* T, hipStream_t s) {
   const ShrinkPlan p = shrink_plan(M, C0);
   if (few_or_many(C)) {
-    expand_short_kernel<WT><<<flat_grid(M * C), kThreads, 0, s>>>(parts, p.parts, M, C, ad,
+    expand_short_kernel<WT><<<flat_grid(M * C), kAdapterThreads, 0, s>>>(parts, p.parts, M, C, ad,
                                                                  static_cast<const char*>(W), Y, accumulate);
     return T ? launch_join(parts, M, C0, ad, T, s) : hipGetLastError();
   }
@@ -731,7 +482,7 @@ hipError_t grad_as(const float* V, const void* X, int64_t M, int64_t C, const Ad
                    hipStream_t s) {
   if (few_or_many(C)) {
     const int64_t n = int64_t(ad.A) * ad.R * C;
-    grad_short_kernel<XT><<<static_cast<unsigned>(std::min(n, kMaxGrid)), kThreads, 0, s>>>(
+    grad_short_kernel<XT><<<static_cast<unsigned>(std::min(n, kMaxGrid)), kAdapterThreads, 0, s>>>(
         V, static_cast<const char*>(X), M, C, ad, dW, n);
     return hipGetLastError();
   }
@@ -740,11 +491,11 @@ hipError_t grad_as(const float* V, const void* X, int64_t M, int64_t C, const Ad
   const unsigned grid = static_cast<unsigned>(std::min(items, kMaxGrid));
   const bool one = p.parts == 1;
   auto kernel = ad.R <= 16 ? grad_kernel<XT, 1> : ad.R <= 32 ? grad_kernel<XT, 2> : grad_kernel<XT, 4>;
-  kernel<<<grid, kThreads, 0, s>>>(V, static_cast<const char*>(X), M, C, ad, one ? dW : ws, one, p.parts, items, p.tiles,
+  kernel<<<grid, kAdapterThreads, 0, s>>>(V, static_cast<const char*>(X), M, C, ad, one ? dW : ws, one, p.parts, items, p.tiles,
                                    p.groups);
   if (!one) {
     const int64_t per = int64_t(ad.R) * C, n = per * ad.A;
-    grad_join_kernel<<<flat_grid(n), kThreads, 0, s>>>(ws, p.parts, n, per, ad.scales, dW);
+    grad_join_kernel<<<flat_grid(n), kAdapterThreads, 0, s>>>(ws, p.parts, n, per, ad.scales, dW);
   }
   return hipGetLastError();
 }
@@ -767,7 +518,7 @@ hipError_t launch_expand(const float* parts, int64_t M, int64_t C0, int64_t C, c
 }
 
 hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, hipStream_t s) {
-  join_kernel<<<flat_grid(M * ad.R), kThreads, 0, s>>>(parts, shrink_plan(M, C0).parts, M, ad, T);
+  join_kernel<<<flat_grid(M * ad.R), kAdapterThreads, 0, s>>>(parts, shrink_plan(M, C0).parts, M, ad, T);
   return hipGetLastError();
 }
 

@@ -261,6 +261,20 @@ def test_streams_and_graph():
         assert torch.equal(h1, bl.gated_forward(new[:1].contiguous(), P.gate.gpu, P.up.gpu))
 
 
+@pytest.mark.parametrize("K", [1, 7, 8, 9, 63, 2041, 2049, 8191, 8193, 28671, 28673])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_codes_of_rows_of_any_length(K, dt):
+    M = 6
+    X = to_type(np.random.default_rng(K).standard_normal((M, K)) * 3, dt)
+    X[2] = 0.0
+    buf = torch.empty(M * K + 1, dtype=DT[dt], device=DEV)
+    for x in (on_gpu(X, dt), buf[1:].view(M, K).copy_(on_gpu(X, dt))):  # and rows one value off
+        Xq, ga, rs = bl.quantize_activations(x)
+        gA, q, r = O.absmax_quantize(X)
+        assert np.array_equal(Xq.cpu().numpy()[:, :K], q) and not Xq[:, K:].any()
+        assert same(np_of(ga), gA) and np.array_equal(rs.cpu().numpy(), r)
+
+
 def test_refused_on_the_gpu():
     P = Problem(4, 64, 32)
     w = P.gate.gpu
