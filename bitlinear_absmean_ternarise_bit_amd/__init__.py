@@ -782,18 +782,27 @@ def _path(path):
     return p
 
 
-def _ternary(B, w, K, N, device, name):
-    """(packed address, gamma address, N) of (packed [N, packed_words(K)], gamma [1]) on `device`."""
+def _placed(t, index, name):
+    """Raises unless t is a contiguous tensor on GPU `index`."""
+    if t.get_device() != index or not t.is_contiguous():
+        _require_cuda(t, name)
+        raise ValueError(f"{name} is on another device")
+
+
+def _ternary(B, w, K, N, index, name):
+    """(packed address, gamma address, N) of (packed [N, packed_words(K)], gamma [1]) on GPU `index`."""
     packed, gamma = w
-    if not (packed.is_cuda and packed.is_contiguous()):
-        _require_cuda(packed, f"{name}'s packed weights")
-    if packed.dim() != 2 or packed.element_size() != 4 or packed.shape[1] != (K + 63) // 64 * 4 or not packed.numel() \
-            or (N is not None and packed.shape[0] != N):
+    if packed.get_device() != index or not packed.is_contiguous():
+        _placed(packed, index, f"{name}'s packed weights")
+    shape = packed.shape
+    if len(shape) != 2 or shape[1] != (K + 63) // 64 * 4 or shape[0] < 1 or packed.element_size() != 4 \
+            or (N is not None and shape[0] != N):
         raise ValueError(f"{name}'s packed weights must hold padded_k({K}) // 16 32-bit words for each of "
                          f"{'their' if N is None else N} rows")
-    if packed.get_device() != device.index:
-        raise ValueError(f"{name}'s packed weights are on another device")
-    return packed.data_ptr(), _vector(B, gamma, 1, device, f"{name}'s gamma"), packed.shape[0]
+    if gamma.get_device() != index or gamma.dtype != B.f32 or gamma.numel() != 1:
+        _placed(gamma, index, f"{name}'s gamma")
+        raise ValueError(f"{name}'s gamma must hold 1 float32 value")
+    return packed.data_ptr(), gamma.data_ptr(), shape[0]
 
 
 def _workspace(B, workspace, need, device):
@@ -843,8 +852,8 @@ def gated_forward(X, gate, up, K: int | None = None, act: str = "relu2", out_dty
         if K is not None and K != D:
             raise ValueError("K does not match X")
         K, device = D, X.device
-    gp, gg, F = _ternary(B, gate, K, None, device, "gate")
-    up_, ug, _ = _ternary(B, up, K, F, device, "up")
+    gp, gg, F = _ternary(B, gate, K, None, device.index, "gate")
+    up_, ug, _ = _ternary(B, up, K, F, device.index, "up")
     if out_dtype is None:
         out_dtype = B.f32 if out is None else out.dtype
     hdt = _plain_dtype(B, out_dtype, "out_dtype")
@@ -880,9 +889,9 @@ def gated_ffn_forward(X, gate, up, down, act: str = "relu2", path: str = "auto",
     a, p = _act(act), _path(path)
     dt, M, D = _matrix(B, X, "X")
     device = X.device
-    gp, gg, F = _ternary(B, gate, D, None, device, "gate")
-    up_, ug, _ = _ternary(B, up, D, F, device, "up")
-    dp, dg, Do = _ternary(B, down, F, None, device, "down")
+    gp, gg, F = _ternary(B, gate, D, None, device.index, "gate")
+    up_, ug, _ = _ternary(B, up, D, F, device.index, "up")
+    dp, dg, Do = _ternary(B, down, F, None, device.index, "down")
     Y = _output(B, out, M, Do, B.f32, device)
     H = B.empty(M, F, dtype=B.f32, device=device) if return_hidden else None
     need = 0 if workspace is not None else B.gated_ffn_workspace_bytes(M, D, F)
@@ -931,8 +940,8 @@ def gated_input_backward(dG, dU, gateT, upT, K: int, out=None, workspace=None):
     device = dG.device
     if dU.device != device:
         raise ValueError("dG and dU are on different devices")
-    gp, gg, _ = _ternary(B, gateT, F, K, device, "gateT")
-    up_, ug, _ = _ternary(B, upT, F, K, device, "upT")
+    gp, gg, _ = _ternary(B, gateT, F, K, device.index, "gateT")
+    up_, ug, _ = _ternary(B, upT, F, K, device.index, "upT")
     dX = _output(B, out, M, K, B.f32, device)
     need = 0
     if workspace is None and (F % 8 or dG.data_ptr() % 16 or dU.data_ptr() % 16):
@@ -952,23 +961,25 @@ def gated_input_backward(dG, dU, gateT, upT, K: int, out=None, workspace=None):
 def _adapters(B, adapters, rows, M, K, N, device):
     """(A, R, N, addresses of down and up, their abi dtype, addresses of scales and rows), checked."""
     down, up, scales = adapters
-    for t, nm in ((down, "down"), (up, "up"), (rows, "rows")):
-        if not (t.is_cuda and t.is_contiguous()):
-            _require_cuda(t, nm)
-        if t.get_device() != device.index:
-            raise ValueError(f"{nm} is on another device")
+    index = device.index
+    for t, nm in ((down, "down"), (up, "up"), (rows, "rows"), (scales, "scales")):
+        if t.get_device() != index or not t.is_contiguous():
+            _placed(t, index, nm)
     wdt = _plain_dtype(B, down.dtype, "down")
     if up.dtype != down.dtype:
         raise ValueError("down and up must have one dtype")
-    if down.dim() != 3 or up.dim() != 3 or not down.numel() or not up.numel() or up.shape[:2] != down.shape[:2]:
+    ds, us = down.shape, up.shape
+    if len(ds) != 3 or len(us) != 3 or us[:2] != ds[:2] or 0 in ds or us[2] < 1:
         raise ValueError("down must be [A, R, K] and up [A, R, N]")
-    A, R, k = down.shape
-    n = up.shape[2]
+    A, R, k = ds
+    n = us[2]
     if k != K or (N is not None and n != N):
         raise ValueError("down and up do not match the projection")
-    if rows.dtype != B.i32 or rows.dim() != 1 or rows.shape[0] != M:
+    if rows.dtype != B.i32 or rows.shape != (M,):
         raise ValueError("rows must hold M int32 values")
-    return A, R, n, down.data_ptr(), up.data_ptr(), wdt, _vector(B, scales, A, device, "scales"), rows.data_ptr()
+    if scales.dtype != B.f32 or scales.numel() != A:
+        raise ValueError(f"scales must hold {A} float32 values")
+    return A, R, n, down.data_ptr(), up.data_ptr(), wdt, scales.data_ptr(), rows.data_ptr()
 
 
 def adapters_forward(X, adapters, rows, Y, return_low: bool = False, workspace=None):
@@ -1005,15 +1016,11 @@ def adapted_forward(X, packed, gamma, adapters, rows, K: int | None = None, path
     if K is not None and K != Kx:
         raise ValueError("K does not match X")
     K, device = Kx, X.device
-    pk, gm, N = _ternary(B, (packed, gamma), K, None, device, "the projection")
+    pk, gm, N = _ternary(B, (packed, gamma), K, None, device.index, "the projection")
     A, R, _, dn, up, wdt, sc, ids = _adapters(B, adapters, rows, M, K, N, device)
     Y = _output(B, out, M, N, B.f32, device)
     T = B.empty(M, R, dtype=B.f32, device=device) if return_low else None
-    need = 0
-    if workspace is None:
-        need = B.adapters_workspace_bytes(M, K, N, R)
-        if not (p != abi.PATH_PREFILL and _fits_decode(M, K, N)):
-            need += B.forward_workspace_bytes(M, K)
+    need = 0 if workspace is not None else B.adapted_workspace_bytes(M, K, N, R)
     wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
     B.launch(B.adapted_forward, device, X.data_ptr(), dt, M, K, pk, N, gm, ids, A, R, dn, up, wdt, sc, Y.data_ptr(),
              T.data_ptr() if return_low else 0, p, wsp, ws_bytes)

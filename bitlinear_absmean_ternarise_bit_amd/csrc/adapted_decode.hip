@@ -1,13 +1,13 @@
-// A decode batch through a projection and its adapters (include/bitlinear_adapters.h):
-// the ternary product and the adapters' first product, which both read X alone,
-// in one launch.  What a small call costs is launches (about 4 us each on the
-// host, where the two kernels run 3 to 4 us), so this saves one of three.
-//
-// The first workgroups take the first product, the others the decode forward's
-// split form (one block of 16 weight rows each, decode_kernel.hpp).  Tokens whose
-// codes do not fit one workgroup's LDS go in up to four pieces, each through all
-// weight rows (16 x 4096 x 4096: 5.9 us instead of 23.6 for the quantiser and the
-// GEMM, which reads the weights once but has 32 workgroups).
+// A decode batch through a projection and its adapters (include/bitlinear_adapters.h)
+// in two launches.  What a small call costs is launches (about 4 us each on the
+// host) and kernels that wait for one memory access after another, so:
+//   1. what reads X alone: the adapters' first product, and the tokens' codes (one
+//      workgroup a token);
+//   2. the decode forward's split form (decode_kernel.hpp) on those codes, one
+//      block of 16 weight rows to a workgroup, which also forms the adapters'
+//      second product for its 16 columns while its first weights are on their way.
+// Tokens whose codes do not fit one workgroup's LDS go in up to four pieces, each
+// through all weight rows.
 #include "adapter_device.hpp"
 #include "decode_kernel.hpp"
 
@@ -15,50 +15,177 @@ namespace bitlinear {
 
 namespace {
 
+static_assert(kDecodeThreads == kAdapterThreads, "one launch for both");
+
+// The codes of one token by a workgroup: chunks of 8 values, up to 4 to a lane in
+// registers (8192 values), longer rows read twice.
+template <int DT>
+__device__ __forceinline__ void token_codes(const char* row, int K, int Kp, int8_t* dst, float* gamma_a,
+                                            int32_t* rowsum) {
+  __shared__ float s_max[kWaves];
+  __shared__ int s_sum[kWaves];
+  constexpr int RC = 4;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
+  float v[RC][8];
+  float mx = 0.0f;
+  auto load = [&](int c, float (&f)[8]) { chunk_f32<DT>(load_chunk<DT, false>(row, nullptr, K, c, chunk_values(K, c)), f); };
+  auto widen = [&](const float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(f[i]));
+  };
+#pragma unroll
+  for (int u = 0; u < RC; ++u) load(tid + u * kDecodeThreads, v[u]);
+#pragma unroll
+  for (int u = 0; u < RC; ++u) widen(v[u]);
+  for (int c = tid + RC * kDecodeThreads; 8 * c < K; c += kDecodeThreads) {
+    float f[8];
+    load(c, f);
+    widen(f);
+  }
+  mx = quant_wave_max(mx);
+  if (lane == 0) s_max[wave] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  const float s = __fdiv_rn(127.0f, __fadd_rn(mx, kEps));
+  int sum = 0;
+  auto store = [&](int c, const float (&f)[8]) {
+    if (8 * c >= Kp) return;
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int code = act_code(f[i], s);
+      sum += code;
+      w[i >> 2] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * (i & 3));
+    }
+    *reinterpret_cast<uint2*>(dst + 8 * c) = make_uint2(w[0], w[1]);
+  };
+#pragma unroll
+  for (int u = 0; u < RC; ++u) store(tid + u * kDecodeThreads, v[u]);
+  for (int c = tid + RC * kDecodeThreads; 8 * c < Kp; c += kDecodeThreads) {
+    float f[8];
+    load(c, f);
+    store(c, f);
+  }
+  sum = quant_wave_sum(sum);
+  if (lane == 0) s_sum[wave] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    *gamma_a = mx;
+    *rowsum = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  }
+}
+
+// tokens: workgroups of the codes (the first ones); the others: the first product
+template <int DT, int WT>
+__global__ __launch_bounds__(kDecodeThreads) void adapted_first_kernel(const char* X, int M, int K, int Kp, Adapters ad,
+                                                                       const char* down, float* parts, int nparts,
+                                                                       int spread, int8_t* Xq, float* gamma_a,
+                                                                       int32_t* rowsum) {
+  const int b = static_cast<int>(blockIdx.x);
+  if (b < M)
+    token_codes<DT>(X + static_cast<int64_t>(b) * K * kBytes<DT>, K, Kp, Xq + static_cast<int64_t>(b) * Kp, gamma_a + b,
+                    rowsum + b);
+  else
+    shrink_body<DT, WT, 1, 1>(X, M, K, ad, down, parts, 1, 0, 1, (b - M) % nparts, nparts, (b - M) / nparts, spread);
+}
+
 struct PartOfGrid {
   uint32_t index, count;
   __device__ uint32_t block() const { return index; }
   __device__ uint32_t blocks() const { return count; }
 };
 
-struct ShrinkArgs {
-  const char* W;
-  float* parts;
-  int nparts, spread;
+// The second product for 16 columns and up to 16 tokens: a thread to an output.
+// LDS: T of the tokens, scaled ([16][R] float32), then the 16 x 16 results.
+template <int WT>
+struct AddAdapters {
+  static constexpr bool kOn = true;
+  Adapters ad;
+  const char* up;
+  const float* parts;  // from the piece's first token
+  int nparts, stride;  // floats from part to part
+  float* T;            // NULL, or the piece's rows of T (written by the first block)
+  int m0, block;
+
+  __device__ __forceinline__ int adapter(int i) const {
+    const int id = ad.rows[m0 + i];
+    return id >= 0 && id < ad.A ? id : -1;
+  }
+  __device__ __forceinline__ float weight(int a, int r, uint32_t n, uint32_t N) const {
+    const int64_t at = (static_cast<int64_t>(a) * ad.R + r) * N + n;
+    if constexpr (WT == kF32) return reinterpret_cast<const float*>(up)[at];
+    else return bf16_to_f32(reinterpret_cast<const uint16_t*>(up)[at]);
+  }
+  __device__ __forceinline__ void prepare(int M, uint32_t n0, uint32_t N, int8_t* lds) const {
+    float* t = reinterpret_cast<float*>(lds);
+    float* d = t + 16 * ad.R;
+    const int Rp = (ad.R + 15) & ~15;
+    const int i = threadIdx.x >> 4;
+    const uint32_t n = n0 + (threadIdx.x & 15u);
+    const int a = i < M && n < N ? adapter(i) : -1;
+    // the first 16 ranks' weights are asked for before T's parts are added
+    float w[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) w[r] = a >= 0 && r < ad.R ? weight(a, r, n, N) : 0.0f;
+    for (int x = threadIdx.x; x < M * ad.R; x += kDecodeThreads) {
+      const int token = x / ad.R, r = x - token * ad.R, id = adapter(token);
+      float v = 0.0f;
+      if (id >= 0) {
+        const float* from = parts + token * Rp + r;
+        v = from[0];
+#pragma unroll 4
+        for (int s = 1; s < nparts; ++s) v += from[s * stride];
+      }
+      if (T != nullptr && block == 0) T[x] = v;
+      t[x] = id >= 0 ? __fmul_rn(v, ad.scales[id]) : 0.0f;
+    }
+    __syncthreads();
+    float sum = -0.0f;  // without an adapter: leaves every output as it is, its sign of zero too
+    if (a >= 0) {
+      const float* mine = t + i * ad.R;
+      sum = __fmul_rn(mine[0], w[0]);
+#pragma unroll
+      for (int r = 1; r < 16; ++r)
+        if (r < ad.R) sum = __fmaf_rn(mine[r], w[r], sum);
+#pragma unroll 8
+      for (int r = 16; r < ad.R; ++r) sum = __fmaf_rn(mine[r], weight(a, r, n, N), sum);
+    }
+    d[threadIdx.x] = sum;
+  }
+  // token i (0 to 15), row j of the block
+  __device__ __forceinline__ float add(int i, int j, float y, const int8_t* lds) const {
+    return __fadd_rn(y, reinterpret_cast<const float*>(lds)[16 * ad.R + 16 * i + j]);
+  }
 };
 
-// piece: tokens of a piece; row_blocks: blocks of 16 weight rows
-template <int DT, bool VEC, int SPLIT, int WT>
-__global__ __launch_bounds__(kDecodeThreads) void adapted_decode_kernel(const char* X, int M, int64_t K, int64_t Kp,
-                                                                        int64_t units, const uint32_t* packed, int64_t N,
+template <int SPLIT, int WT>
+__global__ __launch_bounds__(kDecodeThreads) void adapted_decode_kernel(const int8_t* Xq, const float* ga,
+                                                                        const int32_t* rs, int M, int64_t K, int64_t Kp,
+                                                                        const uint32_t* packed, int64_t N,
                                                                         const float* gamma, float* Y, int piece,
-                                                                        int row_blocks, Adapters ad, ShrinkArgs sh) {
-  static_assert(kDecodeThreads == kAdapterThreads, "one launch for both");
-  const int first = sh.nparts * sh.spread;
-  if (static_cast<int>(blockIdx.x) < first) {
-    const int b = static_cast<int>(blockIdx.x);
-    shrink_body<DT, WT, 1, 1>(X, M, K, ad, sh.W, sh.parts, 1, 0, 1, b % sh.nparts, sh.nparts, b / sh.nparts, sh.spread);
-    return;
-  }
-  const uint32_t b = blockIdx.x - static_cast<uint32_t>(first), which = b / static_cast<uint32_t>(row_blocks);
-  const int m0 = static_cast<int>(which) * piece;
-  decode_body<2, DT, VEC, kEpiY, SPLIT>(X + m0 * K * kBytes<DT>, min(piece, M - m0), K, Kp, units, packed, N, gamma,
-                                        Y + m0 * N, nullptr, row_blocks, 1, 0, nullptr, nullptr,
-                                        PartOfGrid{b - which * static_cast<uint32_t>(row_blocks), static_cast<uint32_t>(row_blocks)});
+                                                                        int row_blocks, Adapters ad, const char* up,
+                                                                        const float* parts, int nparts, float* T) {
+  const uint32_t which = blockIdx.x / static_cast<uint32_t>(row_blocks), b = blockIdx.x - which * row_blocks;
+  const int m0 = static_cast<int>(which) * piece, m = min(piece, M - m0), Rp = (ad.R + 15) & ~15;
+  const AddAdapters<WT> extra = {ad, up, parts + m0 * Rp, nparts, M * Rp, T ? T + m0 * ad.R : nullptr,
+                                 m0, static_cast<int>(b)};
+  decode_body<2, 2, true, kEpiY, SPLIT>(Xq + m0 * Kp, m, K, Kp, Kp / 64, packed, N, gamma, Y + m0 * N, nullptr,
+                                        row_blocks, 1, 0, ga + m0, rs + m0,
+                                        PartOfGrid{b, static_cast<uint32_t>(row_blocks)}, extra);
 }
 
-template <int DT, int WT>
-hipError_t launch_as(const void* X, int64_t M, int64_t K, const uint32_t* packed, int64_t N, const float* gamma,
-                     float* Y, const Adapters& ad, const ShrinkArgs& sh, int64_t piece, hipStream_t stream) {
-  const int64_t Kp = padded_k(K), units = Kp / 64, row_blocks = (N + 15) / 16, pieces = (M + piece - 1) / piece;
-  const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && (K * kBytes<DT>) % 16 == 0;
-  const bool two = ((units + 3) / 4 + 3) / 4 <= 8;  // loads a batch, as in the decode forward
-  auto kernel = vec ? (two ? adapted_decode_kernel<DT, true, 2, WT> : adapted_decode_kernel<DT, true, 4, WT>)
-                    : (two ? adapted_decode_kernel<DT, false, 2, WT> : adapted_decode_kernel<DT, false, 4, WT>);
-  const size_t lds = static_cast<size_t>(piece * (Kp + 16)) + kDecodeThreads * sizeof(v4i);
-  kernel<<<static_cast<unsigned>(sh.nparts * sh.spread + pieces * row_blocks), kDecodeThreads, lds, stream>>>(
-      static_cast<const char*>(X), static_cast<int>(M), K, Kp, units, packed, N, gamma, Y, static_cast<int>(piece),
-      static_cast<int>(row_blocks), ad, sh);
+template <int WT>
+hipError_t launch_second(int64_t M, int64_t K, const uint32_t* packed, int64_t N, const float* gamma, float* Y,
+                         const Adapters& ad, const void* up, const float* parts, int nparts, float* T, int64_t piece,
+                         const int8_t* Xq, const float* ga, const int32_t* rs, hipStream_t stream) {
+  const int64_t Kp = padded_k(K), row_blocks = (N + 15) / 16, pieces = (M + piece - 1) / piece;
+  // loads a batch as in the decode forward
+  auto kernel = ((Kp / 64 + 3) / 4 + 3) / 4 <= 8 ? adapted_decode_kernel<2, WT> : adapted_decode_kernel<4, WT>;
+  const size_t lds = static_cast<size_t>(piece * (Kp + 16)) + kDecodeThreads * sizeof(v4i) +
+                     static_cast<size_t>(16 * ad.R + 256) * 4;
+  kernel<<<static_cast<unsigned>(pieces * row_blocks), kDecodeThreads, lds, stream>>>(
+      Xq, ga, rs, static_cast<int>(M), K, Kp, packed, N, gamma, Y, static_cast<int>(piece),
+      static_cast<int>(row_blocks), ad, static_cast<const char*>(up), parts, nparts, T);
   return hipGetLastError();
 }
 
@@ -77,15 +204,22 @@ int64_t adapted_decode_piece(int64_t M, int64_t K, int64_t N) {
 }
 
 hipError_t launch_adapted_decode(const void* X, int x_dtype, int64_t M, int64_t K, const uint32_t* packed, int64_t N,
-                                 const float* gamma, float* Y, const Adapters& ad, const void* down, float* parts,
-                                 int64_t piece, hipStream_t stream) {
+                                 const float* gamma, float* Y, const Adapters& ad, const void* down, const void* up,
+                                 float* parts, float* T, int64_t piece, int8_t* Xq, float* ga, int32_t* rs,
+                                 hipStream_t stream) {
   const ShrinkPlan p = shrink_plan(M, K);
-  const ShrinkArgs sh = {static_cast<const char*>(down), parts, p.parts, p.spread};
-  if (x_dtype == kF32)
-    return ad.w_dtype == kF32 ? launch_as<kF32, kF32>(X, M, K, packed, N, gamma, Y, ad, sh, piece, stream)
-                              : launch_as<kF32, kBf16>(X, M, K, packed, N, gamma, Y, ad, sh, piece, stream);
-  return ad.w_dtype == kF32 ? launch_as<kBf16, kF32>(X, M, K, packed, N, gamma, Y, ad, sh, piece, stream)
-                            : launch_as<kBf16, kBf16>(X, M, K, packed, N, gamma, Y, ad, sh, piece, stream);
+  const unsigned grid = static_cast<unsigned>(M + p.parts * p.spread);
+  auto first = x_dtype == kF32
+                   ? (ad.w_dtype == kF32 ? adapted_first_kernel<kF32, kF32> : adapted_first_kernel<kF32, kBf16>)
+                   : (ad.w_dtype == kF32 ? adapted_first_kernel<kBf16, kF32> : adapted_first_kernel<kBf16, kBf16>);
+  first<<<grid, kDecodeThreads, 0, stream>>>(static_cast<const char*>(X), static_cast<int>(M), static_cast<int>(K),
+                                             static_cast<int>(padded_k(K)), ad, static_cast<const char*>(down), parts,
+                                             p.parts, p.spread, Xq, ga, rs);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return ad.w_dtype == kF32
+             ? launch_second<kF32>(M, K, packed, N, gamma, Y, ad, up, parts, p.parts, T, piece, Xq, ga, rs, stream)
+             : launch_second<kBf16>(M, K, packed, N, gamma, Y, ad, up, parts, p.parts, T, piece, Xq, ga, rs, stream);
 }
 
 }  // namespace bitlinear

@@ -67,7 +67,7 @@ int bitlinear_adapters_forward(const void* X, int x_dtype, int64_t M, int64_t K,
 size_t bitlinear_adapted_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R) {
   if (!size_args_ok(N)) return 0;
   const size_t low = adapters_ws_bytes(M, K, R);
-  return decode_fits(M, K, N) ? low : size_add(low, prefill_ws_bytes(M, K));
+  return size_add(low, prefill_ws_bytes(M, K));
 }
 
 int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, const uint32_t* packed, int64_t N,
@@ -81,7 +81,7 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
   st = check_forward_args(X, x_dtype, M, K, packed, N, gamma, Y, nullptr, path, &decode);
   if (st) return st;
   if (!aligned(T, 4)) return BITLINEAR_ERR_ALIGN;
-  const size_t low = adapters_ws_bytes(M, K, R), need = low + (decode ? 0 : prefill_ws_bytes(M, K));
+  const size_t low = adapters_ws_bytes(M, K, R), need = low + prefill_ws_bytes(M, K);
   if (!workspace || workspace_bytes < need) return BITLINEAR_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return BITLINEAR_ERR_ALIGN;
   const Range out[] = {floats(Y, M * N), floats(T, M * R), {workspace, need}};
@@ -97,15 +97,13 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
   const Adapters ad = {rows, scales, static_cast<int>(A), static_cast<int>(R), w_dtype};
   const int64_t piece = path == BITLINEAR_PATH_PREFILL ? 0 : adapted_decode_piece(M, K, N);
   hipError_t e;
-  if (piece) {
-    float* parts = static_cast<float*>(workspace);
-    e = launch_adapted_decode(X, x_dtype, M, K, packed, N, gamma, Y, ad, down, parts, piece, s);
-    return hip_status(e == hipSuccess ? launch_expand(parts, M, K, N, ad, up, Y, true, T, s) : e);
-  }
+  const PrefillWs c = prefill_ws(static_cast<char*>(workspace) + low, M, K);
+  if (piece)
+    return hip_status(launch_adapted_decode(X, x_dtype, M, K, packed, N, gamma, Y, ad, down, up,
+                                            static_cast<float*>(workspace), T, piece, c.xq, c.ga, c.rs, s));
   if (decode) {
     e = launch_decode(X, x_dtype, M, K, packed, N, gamma, Y, nullptr, 1, s);
   } else {
-    const PrefillWs c = prefill_ws(static_cast<char*>(workspace) + low, M, K);
     e = launch_act_quant(X, x_dtype, M, K, c.xq, c.ga, c.rs, s);
     if (e == hipSuccess) e = launch_prefill_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, nullptr, s);
   }

@@ -89,13 +89,15 @@ inline size_t adapters_backward_ws_bytes(int64_t M, int64_t K, int64_t N, int64_
   return size_add(size_add(shrink_ws_bytes(M, N, R), v), d > u ? d : u);
 }
 
-// Tokens of a piece where a decode batch's projection and first product go in one
-// launch, 0 where they do not (more than 16 tokens, weights of so many rows that
-// the decode forward streams them in another form, rows too long for its LDS).
+// Tokens of a piece where a decode batch goes through its projection and adapters
+// in two launches (adapted_decode.hip), 0 where it does not: more than 16 tokens,
+// weights of so many rows that the decode forward streams them in another form,
+// rows too long for its LDS.  Xq, ga, rs: as a prefill workspace holds them.
 int64_t adapted_decode_piece(int64_t M, int64_t K, int64_t N);
 hipError_t launch_adapted_decode(const void* X, int x_dtype, int64_t M, int64_t K, const uint32_t* packed, int64_t N,
-                                 const float* gamma, float* Y, const Adapters& ad, const void* down, float* parts,
-                                 int64_t piece, hipStream_t stream);
+                                 const float* gamma, float* Y, const Adapters& ad, const void* down, const void* up,
+                                 float* parts, float* T, int64_t piece, int8_t* Xq, float* ga, int32_t* rs,
+                                 hipStream_t stream);
 // parts of T = X W^T (rows without an adapter are not written)
 hipError_t launch_shrink(const void* X, int x_dtype, int64_t M, int64_t C, const Adapters& ad, const void* W,
                          float* parts, hipStream_t stream);

@@ -148,12 +148,17 @@ struct WholeGrid {
   __device__ uint32_t block() const { return blockIdx.x; }
   __device__ uint32_t blocks() const { return gridDim.x; }
 };
-template <int FMT, int DT, bool VEC, int EPI, int SPLIT, class At>
+// extra: something added to every output (split form): prepare() is called by
+// all threads before the workgroup's first barrier, add() for each output.
+struct NothingExtra {
+  static constexpr bool kOn = false;
+};
+template <int FMT, int DT, bool VEC, int EPI, int SPLIT, class At, class Extra = NothingExtra>
 __device__ __forceinline__ void decode_body(
     const void* X, int M, int64_t K, int64_t Kp, int64_t units,
     const uint32_t* packed, int64_t N, const float* gamma,
     float* Y, int32_t* acc, int blocks_per_layer, int groups, int interleave,
-    const float* ga_in, const int32_t* rs_in, const At& at) {
+    const float* ga_in, const int32_t* rs_in, const At& at, const Extra& extra = Extra{}) {
   extern __shared__ __align__(16) int8_t sxq[];
   __shared__ float s_ga[kDecodeMaxM];
   __shared__ int s_rs[kDecodeMaxM];
@@ -397,6 +402,10 @@ __device__ __forceinline__ void decode_body(
       keep(m, ga, rs);
     }
   }
+  if constexpr (Extra::kOn) {
+    static_assert(SPLIT != 0 && DT == 2, "the split form, from codes");
+    extra.prepare(M, static_cast<uint32_t>(n_base), N32, sxq + M * lds_stride + kDecodeThreads * sizeof(v4i));
+  }
   if (qtr) {
     // each wave reads only codes it wrote: one wave's LDS operations complete
     // in order.  (Slots past a row's end may pair with another wave's codes;
@@ -536,6 +545,7 @@ __device__ __forceinline__ void decode_body(
           const float rl = fmaxf(y, 0.0f);
           y = __fmul_rn(rl, rl) + 0.0f;  // + 0: no negative zero
         }
+        if constexpr (Extra::kOn) y = extra.add(i, j, y, sxq + M * lds_stride + kDecodeThreads * sizeof(v4i));
         const uint32_t off = (i < M && n < N32) ? (static_cast<uint32_t>(i) * N32 + n) * 4u : kOff;
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y), ysrc, off, 0, 0);
         if constexpr (EPI == kEpiAcc) __builtin_amdgcn_raw_buffer_store_b32(static_cast<uint32_t>(v), asrc, off, 0, 0);

@@ -78,8 +78,10 @@ int bitlinear_adapters_forward(const void* X, int x_dtype, int64_t M, int64_t K,
 /*
  * The projection and the adapters: Y = bitlinear_forward(X) and then the above
  * on it.  packed, gamma, path: as for bitlinear_forward_ex.  workspace: >=
- * bitlinear_adapted_workspace_bytes(M, K, N, R), 256-byte aligned (the prefill
- * path's codes among it).
+ * bitlinear_adapted_workspace_bytes(M, K, N, R), 256-byte aligned (activation
+ * codes among it).  Up to 16 tokens take two launches.  The adapters' sums may be
+ * formed in another order than by the two calls one after the other; both are
+ * within the accuracy above.
  */
 size_t bitlinear_adapted_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R);
 
