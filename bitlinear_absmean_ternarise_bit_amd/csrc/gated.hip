@@ -39,6 +39,7 @@ hipError_t launch_tile(const int8_t* Xq, const float* ga, const int32_t* rs, int
     const int64_t Mc = std::min(M - r0, chunk);
     const int tiles_m = static_cast<int>((Mc + BM - 1) / BM);
     const int tiles_n = static_cast<int>((N + BN / 2 - 1) / (BN / 2));
+    // persistent workgroups, one to a CU
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(int64_t(tiles_m) * tiles_n, kCUs));
     const int64_t at = r0 * ldy + n0;
     const GatedOut go = {w.up + words, w.gamma_up, moved(o.H, o.h_dtype, at), moved(o.G, o.gu_dtype, at),
@@ -295,25 +296,27 @@ hipError_t launch_decode_as(const void* X, const float* ga, const int32_t* rs, i
 hipError_t launch_gated_gemm(const int8_t* Xq, const float* ga, const int32_t* rs, int64_t M, int64_t D, int64_t F,
                              const GatedWeights& w, const GatedOutputs& o, hipStream_t stream) {
   const int64_t Kp = padded_k(D);
-  // The forward GEMM's choice of tiles, with half as many output columns to a
-  // tile: 256 tokens x 128 columns of both projections, smaller ones when those
-  // would leave more than a quarter of the CUs idle, and a short last round of a
-  // few given to 128 x 128 tiles.
+  // Tiles of 256 tokens x 128 columns (of both projections), 128 x 128 or 128 x 64.
+  // A round of the largest takes 1.75 times as long as one of the middle ones
+  // (4096 columns of X: 46 us and 27; K and the rest do not matter), and one of
+  // the smallest is no faster than the middle (25): those serve where even they
+  // are one round (17x2048x5632 12.7 us, middle 14.2).  Else the fewest rounds so
+  // weighed: 333x8192x28672 153 us with the middle tile, 172 with the largest;
+  // 300x4096x11008 54 and 50; 2048x4096x11008 183 and 165.  Whole rounds of the
+  // largest and then one round of middle tiles for the last columns are a third
+  // way (1024x4096x11008: 89, 94 and 102).
   auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((F + bn - 1) / bn); };
-  const int64_t big = tiles(256, 128), rounds = big / kCUs, rest = big - rounds * kCUs;
-  if (rounds >= 1 && rounds < 4 && rest > 0 && rest * 4 < 3 * kCUs) {
-    const int64_t tm_big = (M + 255) / 256, tm_half = (M + 127) / 128;
-    int64_t nA = rounds * kCUs / tm_big * 128;
-    while (nA > 0 && tm_half * ((F - nA + 127) / 128) > kCUs) nA -= 128;
-    if (nA > 0 && nA < F) {
-      const hipError_t e = launch_tile<256, 256, 4, 2>(Xq, ga, rs, M, Kp, w, 0, nA, F, o, stream);
-      if (e != hipSuccess) return e;
-      return launch_tile<128, 256, 2, 4>(Xq, ga, rs, M, Kp, w, nA, F - nA, F, o, stream);
-    }
+  auto rounds = [&](int64_t n) { return (n + kCUs - 1) / kCUs; };
+  if (tiles(128, 64) <= kCUs) return launch_tile<128, 128, 2, 2>(Xq, ga, rs, M, Kp, w, 0, F, F, o, stream);
+  const int64_t large = 7 * rounds(tiles(256, 128)), middle = 4 * rounds(tiles(128, 128));
+  const int64_t whole = tiles(256, 128) / kCUs, per_column = (M + 255) / 256;  // per column of tiles
+  const int64_t n = whole * kCUs / per_column * 128;  // columns of whole rounds of the largest
+  if (n > 0 && n < F && (M + 127) / 128 * ((F - n + 127) / 128) <= kCUs && 7 * whole + 4 < std::min(large, middle)) {
+    const hipError_t e = launch_tile<256, 256, 4, 2>(Xq, ga, rs, M, Kp, w, 0, n, F, o, stream);
+    return e != hipSuccess ? e : launch_tile<128, 256, 2, 4>(Xq, ga, rs, M, Kp, w, n, F - n, F, o, stream);
   }
-  if (big >= 192) return launch_tile<256, 256, 4, 2>(Xq, ga, rs, M, Kp, w, 0, F, F, o, stream);
-  if (tiles(128, 128) >= 192) return launch_tile<128, 256, 2, 4>(Xq, ga, rs, M, Kp, w, 0, F, F, o, stream);
-  return launch_tile<128, 128, 2, 2>(Xq, ga, rs, M, Kp, w, 0, F, F, o, stream);
+  if (middle < large) return launch_tile<128, 256, 2, 4>(Xq, ga, rs, M, Kp, w, 0, F, F, o, stream);
+  return launch_tile<256, 256, 4, 2>(Xq, ga, rs, M, Kp, w, 0, F, F, o, stream);
 }
 
 hipError_t launch_gated_decode(const void* X, int x_dtype, const int8_t* Xq, const float* ga, const int32_t* rs,
