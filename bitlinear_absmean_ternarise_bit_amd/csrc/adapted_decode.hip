@@ -8,86 +8,13 @@
 //      second product for its 16 columns while its first weights are on their way.
 // Tokens whose codes do not fit one workgroup's LDS go in up to four pieces, each
 // through all weight rows.
-#include "adapter_device.hpp"
+#include "adapter_ops.hpp"
+#include "block_device.hpp"
 #include "decode_kernel.hpp"
 
 namespace bitlinear {
 
 namespace {
-
-static_assert(kDecodeThreads == kAdapterThreads, "one launch for both");
-
-// The codes of one token by a workgroup: chunks of 8 values, up to 4 to a lane in
-// registers (8192 values), longer rows read twice.
-template <int DT>
-__device__ __forceinline__ void token_codes(const char* row, int K, int Kp, int8_t* dst, float* gamma_a,
-                                            int32_t* rowsum) {
-  __shared__ float s_max[kWaves];
-  __shared__ int s_sum[kWaves];
-  constexpr int RC = 4;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_id();
-  float v[RC][8];
-  float mx = 0.0f;
-  auto load = [&](int c, float (&f)[8]) { chunk_f32<DT>(load_chunk<DT, false>(row, nullptr, K, c, chunk_values(K, c)), f); };
-  auto widen = [&](const float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(f[i]));
-  };
-#pragma unroll
-  for (int u = 0; u < RC; ++u) load(tid + u * kDecodeThreads, v[u]);
-#pragma unroll
-  for (int u = 0; u < RC; ++u) widen(v[u]);
-  for (int c = tid + RC * kDecodeThreads; 8 * c < K; c += kDecodeThreads) {
-    float f[8];
-    load(c, f);
-    widen(f);
-  }
-  mx = quant_wave_max(mx);
-  if (lane == 0) s_max[wave] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-  const float s = __fdiv_rn(127.0f, __fadd_rn(mx, kEps));
-  int sum = 0;
-  auto store = [&](int c, const float (&f)[8]) {
-    if (8 * c >= Kp) return;
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int code = act_code(f[i], s);
-      sum += code;
-      w[i >> 2] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * (i & 3));
-    }
-    *reinterpret_cast<uint2*>(dst + 8 * c) = make_uint2(w[0], w[1]);
-  };
-#pragma unroll
-  for (int u = 0; u < RC; ++u) store(tid + u * kDecodeThreads, v[u]);
-  for (int c = tid + RC * kDecodeThreads; 8 * c < Kp; c += kDecodeThreads) {
-    float f[8];
-    load(c, f);
-    store(c, f);
-  }
-  sum = quant_wave_sum(sum);
-  if (lane == 0) s_sum[wave] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    *gamma_a = mx;
-    *rowsum = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-  }
-}
-
-// tokens: workgroups of the codes (the first ones); the others: the first product
-template <int DT, int WT>
-__global__ __launch_bounds__(kDecodeThreads) void adapted_first_kernel(const char* X, int M, int K, int Kp, Adapters ad,
-                                                                       const char* down, float* parts, int nparts,
-                                                                       int spread, int8_t* Xq, float* gamma_a,
-                                                                       int32_t* rowsum) {
-  const int b = static_cast<int>(blockIdx.x);
-  if (b < M)
-    token_codes<DT>(X + static_cast<int64_t>(b) * K * kBytes<DT>, K, Kp, Xq + static_cast<int64_t>(b) * Kp, gamma_a + b,
-                    rowsum + b);
-  else
-    shrink_body<DT, WT, 1, 1>(X, M, K, ad, down, parts, 1, 0, 1, (b - M) % nparts, nparts, (b - M) / nparts, spread);
-}
 
 struct PartOfGrid {
   uint32_t index, count;
@@ -208,14 +135,7 @@ hipError_t launch_adapted_decode(const void* X, int x_dtype, int64_t M, int64_t 
                                  float* parts, float* T, int64_t piece, int8_t* Xq, float* ga, int32_t* rs,
                                  hipStream_t stream) {
   const ShrinkPlan p = shrink_plan(M, K);
-  const unsigned grid = static_cast<unsigned>(M + p.parts * p.spread);
-  auto first = x_dtype == kF32
-                   ? (ad.w_dtype == kF32 ? adapted_first_kernel<kF32, kF32> : adapted_first_kernel<kF32, kBf16>)
-                   : (ad.w_dtype == kF32 ? adapted_first_kernel<kBf16, kF32> : adapted_first_kernel<kBf16, kBf16>);
-  first<<<grid, kDecodeThreads, 0, stream>>>(static_cast<const char*>(X), static_cast<int>(M), static_cast<int>(K),
-                                             static_cast<int>(padded_k(K)), ad, static_cast<const char*>(down), parts,
-                                             p.parts, p.spread, Xq, ga, rs);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = launch_adapted_first(X, x_dtype, M, K, ad, down, parts, Xq, ga, rs, stream);
   if (e != hipSuccess) return e;
   return ad.w_dtype == kF32
              ? launch_second<kF32>(M, K, packed, N, gamma, Y, ad, up, parts, p.parts, T, piece, Xq, ga, rs, stream)

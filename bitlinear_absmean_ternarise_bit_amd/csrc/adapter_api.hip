@@ -104,6 +104,14 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
   if (decode) {
     e = launch_decode(X, x_dtype, M, K, packed, N, gamma, Y, nullptr, 1, s);
   } else {
+    if (adapted_gemm_takes(K, N, R)) {
+      float* parts = static_cast<float*>(workspace);
+      uint16_t* planes = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + shrink_ws_bytes(M, K, R));
+      e = launch_adapted_first(X, x_dtype, M, K, ad, down, parts, c.xq, c.ga, c.rs, s);
+      if (e == hipSuccess) e = launch_join(parts, M, K, ad, T, planes, s);
+      if (e == hipSuccess) e = launch_adapted_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, planes, ad, up, s);
+      return hip_status(e);
+    }
     e = launch_act_quant(X, x_dtype, M, K, c.xq, c.ga, c.rs, s);
     if (e == hipSuccess) e = launch_prefill_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, nullptr, s);
   }
@@ -151,7 +159,7 @@ int bitlinear_adapters_backward(const void* dY, int dy_dtype, const void* X, int
     if (e == hipSuccess && dX)
       e = launch_expand(parts, M, N, K, ad, down, dX, accumulate != 0, ddown ? V : nullptr, s);
     else if (e == hipSuccess)
-      e = launch_join(parts, M, N, ad, V, s);
+      e = launch_join(parts, M, N, ad, V, nullptr, s);
   }
   if (e == hipSuccess && ddown) e = launch_adapter_grad(V, X, x_dtype, M, K, ad, ddown, grads, s);
   if (e == hipSuccess && dup) e = launch_adapter_grad(T, dY, dy_dtype, M, N, ad, dup, grads, s);

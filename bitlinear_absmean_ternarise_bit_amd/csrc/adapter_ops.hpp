@@ -33,7 +33,7 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t C) {
   ShrinkPlan p = {M >= 256 ? 4 : 1, 1, 1};
   const int64_t groups = (M + 16 * p.blocks - 1) / (16 * p.blocks);
   if (p.blocks == 1) p.spread = static_cast<int>(M < 16 ? M : 16);
-  int64_t parts = 512 / (groups * p.spread);
+  int64_t parts = (p.blocks == 4 ? 256 : 512) / (groups * p.spread);
   const int64_t most = (C + 255) / 256;  // at least 256 columns, 64 to a wave
   if (parts > most) parts = most;
   if (parts > 16) parts = 16;
@@ -77,7 +77,8 @@ inline size_t grad_ws_bytes(int64_t M, int64_t C, int64_t A, int64_t R) {
 }
 inline size_t adapters_ws_bytes(int64_t M, int64_t K, int64_t R) {
   if (!size_args_ok(M) || !size_args_ok(K) || !size_args_ok(R) || R > kAdapterMaxR) return 0;
-  return shrink_ws_bytes(M, K, R);
+  // (with up to 16 ranks also T's planes, for the GEMM with the adapters)
+  return size_add(shrink_ws_bytes(M, K, R), R <= 16 ? align256(size_mul(size_t(M), 96)) : 256);
 }
 inline size_t adapters_backward_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t A, int64_t R) {
   if (!size_args_ok(M) || !size_args_ok(K) || !size_args_ok(N) || !size_args_ok(R) || R > kAdapterMaxR || A < 1 ||
@@ -98,6 +99,17 @@ hipError_t launch_adapted_decode(const void* X, int x_dtype, int64_t M, int64_t 
                                  const float* gamma, float* Y, const Adapters& ad, const void* down, const void* up,
                                  float* parts, float* T, int64_t piece, int8_t* Xq, float* ga, int32_t* rs,
                                  hipStream_t stream);
+// The first product and the tokens' codes in one launch (K >= 8).
+hipError_t launch_adapted_first(const void* X, int x_dtype, int64_t M, int64_t K, const Adapters& ad, const void* down,
+                                float* parts, int8_t* Xq, float* ga, int32_t* rs, hipStream_t stream);
+// The prefill GEMM with the second product in its epilogue, where the ranks are
+// few (16) and its 32-bit offsets hold; planes: launch_join's.
+inline bool adapted_gemm_takes(int64_t K, int64_t N, int64_t R) {
+  return R <= 16 && K >= 8 && N >= 8 && N <= (int64_t(1) << 24);
+}
+hipError_t launch_adapted_gemm(const int8_t* Xq, const float* ga, const int32_t* rs, int64_t M, int64_t K,
+                               const uint32_t* packed, int64_t N, const float* gamma, float* Y, const uint16_t* planes,
+                               const Adapters& ad, const void* up, hipStream_t stream);
 // parts of T = X W^T (rows without an adapter are not written)
 hipError_t launch_shrink(const void* X, int x_dtype, int64_t M, int64_t C, const Adapters& ad, const void* W,
                          float* parts, hipStream_t stream);
@@ -105,8 +117,9 @@ hipError_t launch_shrink(const void* X, int x_dtype, int64_t M, int64_t C, const
 // or where the whole T goes ([M, R], zeros for rows without an adapter)
 hipError_t launch_expand(const float* parts, int64_t M, int64_t C0, int64_t C, const Adapters& ad, const void* W,
                          float* Y, bool accumulate, float* T, hipStream_t stream);
-// T alone
-hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, hipStream_t stream);
+// T alone, and (R <= 16) its scaled planes bf16 [3][M][16]; each may be NULL
+hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, uint16_t* planes,
+                       hipStream_t stream);
 // dW[a] = scale[a] V^T X, V [M, R]; ws: grad_ws_bytes
 hipError_t launch_adapter_grad(const float* V, const void* X, int x_dtype, int64_t M, int64_t C, const Adapters& ad,
                                float* dW, float* ws, hipStream_t stream);

@@ -185,19 +185,36 @@ __global__ __launch_bounds__(kAdapterThreads, 2) void expand_kernel(const float*
   }
 }
 
-// T[m, r] from its parts, zeros for rows without an adapter.
+// T [M, R] from its parts, and its planes, scaled, [3][M][Rp] (zeros for rows
+// without an adapter); either may be NULL.  Four ranks to a thread.
 __global__ __launch_bounds__(kAdapterThreads) void join_kernel(const float* __restrict__ parts, int nparts, int64_t M,
-                                                        Adapters ad, float* __restrict__ T) {
-  const int Rp = (ad.R + 15) & ~15;
-  const int64_t n = M * ad.R;
+                                                               Adapters ad, float* __restrict__ T,
+                                                               uint16_t* __restrict__ planes) {
+  const int Rp = (ad.R + 15) & ~15, quads = Rp / 4;
+  const int64_t n = M * quads;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAdapterThreads + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * kAdapterThreads) {
-    const int64_t m = i / ad.R;
-    const int id = ad.rows[m];
-    float v = 0.0f;
-    if (id >= 0 && id < ad.A)
-      for (int s = 0; s < nparts; ++s) v += parts[(s * M + m) * Rp + (i - m * ad.R)];
-    T[i] = v;
+    const int64_t m = i / quads;
+    const int r = 4 * static_cast<int>(i - m * quads), id = ad.rows[m];
+    const bool has = id >= 0 && id < ad.A;
+    f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (has) {
+      const float* from = parts + m * Rp + r;
+      t = *reinterpret_cast<const f32x4*>(from);
+#pragma unroll 4
+      for (int s = 1; s < nparts; ++s) t += *reinterpret_cast<const f32x4*>(from + static_cast<int64_t>(s) * M * Rp);
+    }
+    if (T != nullptr) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (r + k < ad.R) T[m * ad.R + r + k] = t[k];
+    }
+    if (planes != nullptr) {
+      s16x4 p[3];
+      value_planes(t * (has ? ad.scales[id] : 0.0f), p);
+#pragma unroll
+      for (int s = 0; s < 3; ++s) *reinterpret_cast<s16x4*>(planes + (s * M + m) * Rp + r) = p[s];
+    }
   }
 }
 
@@ -471,7 +488,7 @@ hipError_t expand_any(const float* parts, int64_t M, int64_t C0, int64_t C, cons
   if (few_or_many(C)) {
     expand_short_kernel<WT><<<flat_grid(M * C), kAdapterThreads, 0, s>>>(parts, p.parts, M, C, ad,
                                                                  static_cast<const char*>(W), Y, accumulate);
-    return T ? launch_join(parts, M, C0, ad, T, s) : hipGetLastError();
+    return T ? launch_join(parts, M, C0, ad, T, nullptr, s) : hipGetLastError();
   }
   return expand_blocks(M, C) == 2 ? expand_as<WT, 2>(parts, p.parts, 1, M, C, ad, W, Y, accumulate, T, s)
                                   : expand_as<WT, 1>(parts, p.parts, p.spread, M, C, ad, W, Y, accumulate, T, s);
@@ -517,8 +534,10 @@ hipError_t launch_expand(const float* parts, int64_t M, int64_t C0, int64_t C, c
                             : expand_any<kBf16>(parts, M, C0, C, ad, W, Y, accumulate, T, s);
 }
 
-hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, hipStream_t s) {
-  join_kernel<<<flat_grid(M * ad.R), kAdapterThreads, 0, s>>>(parts, shrink_plan(M, C0).parts, M, ad, T);
+hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, uint16_t* planes,
+                       hipStream_t s) {
+  join_kernel<<<flat_grid(M * (padded_r(ad.R) / 4)), kAdapterThreads, 0, s>>>(parts, shrink_plan(M, C0).parts, M, ad, T,
+                                                                              planes);
   return hipGetLastError();
 }
 

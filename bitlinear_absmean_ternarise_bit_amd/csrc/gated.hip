@@ -17,7 +17,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void gated_gemm_kernel(
     int64_t Kp, const uint32_t* __restrict__ packed_gate, int64_t N, int64_t ldy, const float* __restrict__ gamma_gate,
     int tiles_m, int tiles_n, int bytes_a, int bytes_b, GatedOut go) {
   prefill_gemm_body<BM, BN, WM, WN, 3>(Xq, gamma_a, rowsum, M, Kp, packed_gate, N, ldy, gamma_gate, nullptr, nullptr,
-                                       tiles_m, tiles_n, bytes_a, bytes_b, go);
+                                       tiles_m, tiles_n, bytes_a, bytes_b, go, AdapterOut{});
 }
 
 constexpr int64_t kCUs = 256;

@@ -13,7 +13,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void prefill_gemm_kernel(
     int64_t Kp, const uint32_t* __restrict__ packed, int64_t N, int64_t ldy, const float* __restrict__ gamma,
     float* __restrict__ Y, int32_t* __restrict__ acc, int tiles_m, int tiles_n, int bytes_a, int bytes_b) {
   prefill_gemm_body<BM, BN, WM, WN, EPI>(Xq, gamma_a, rowsum, M, Kp, packed, N, ldy, gamma, Y, acc, tiles_m, tiles_n,
-                                         bytes_a, bytes_b, GatedOut{});
+                                         bytes_a, bytes_b, GatedOut{}, AdapterOut{});
 }
 
 constexpr int64_t kCUs = 256;  // compute units of an MI355X: one workgroup each

@@ -42,6 +42,7 @@
 
 #include <type_traits>
 
+#include "adapter_device.hpp"
 #include "gated_device.hpp"
 #include "kernels.hpp"
 
@@ -70,8 +71,21 @@ struct GatedOut {
   int act, h_dtype, gu_dtype;
 };
 
+// Adapters of up to 16 ranks added to Y (EPI 4: bfloat16 weights, 5: float32):
+// the scaled first product as operand planes, and the second one's weights.
+// Pointers are those of the launch's first token and column.
+struct AdapterOut {
+  const uint16_t* planes;  // bf16 [3][tokens][16]
+  int64_t plane_stride;    // values from plane to plane
+  const int32_t* rows;
+  const char* up;          // [A][R][ld]
+  int64_t ld;
+  int A, R;
+};
+
 // EPI: 0 = Y, 1 = Y and the INT32 accumulators, 2 = ReLU^2 of Y (the hidden
-// activation of a BitNet FFN block), 3 = a gated hidden layer.
+// activation of a BitNet FFN block), 3 = a gated hidden layer, 4 = Y and the
+// adapters' part.
 // EPI 3: a tile is BM tokens x BN / 2 columns of both projections.  Of a wave's
 // NI blocks of 32 packed rows the first half are gate rows and the second half
 // the up rows of the same columns, so a lane holds both accumulators of every
@@ -83,7 +97,7 @@ __device__ __forceinline__ void prefill_gemm_body(
     const int32_t* __restrict__ rowsum, int64_t M, int64_t Kp, const uint32_t* __restrict__ packed,
     int64_t N, int64_t ldy, const float* __restrict__ gamma, float* __restrict__ Y,
     int32_t* __restrict__ acc,
-    int tiles_m, int tiles_n, int bytes_a, int bytes_b, const GatedOut& go) {
+    int tiles_m, int tiles_n, int bytes_a, int bytes_b, const GatedOut& go, const AdapterOut& ao) {
   constexpr int A_BYTES = BM * 128;
   constexpr int B_BYTES = BN * 32;
   constexpr int STAGE = A_BYTES + B_BYTES;
@@ -103,6 +117,8 @@ __device__ __forceinline__ void prefill_gemm_body(
   constexpr bool GATED = EPI == 3;
   constexpr int OUT_BN = GATED ? BN / 2 : BN;  // output columns of a tile
   __shared__ float row_scale_up[GATED ? BM : 1];
+  constexpr bool ADAPTED = EPI >= 4;
+  __shared__ int row_adapter[ADAPTED ? BM : 1];
   static_assert(!GATED || NI % 2 == 0, "gate and up blocks of a wave");
 
   const int tid = threadIdx.x;
@@ -158,6 +174,7 @@ __device__ __forceinline__ void prefill_gemm_body(
   bool b_ok = false;
   int row_rs = 0;
   float row_ga = 0.0f;
+  int row_id = -1;
   auto set_tile = [&](int t) {
     place(t);
     voff_a = static_cast<uint32_t>(m0 + a_r) * kp32 + 16u * a_c;
@@ -174,6 +191,9 @@ __device__ __forceinline__ void prefill_gemm_body(
     if (tid < BM && m < M) {
       row_rs = rowsum[m];
       row_ga = gamma_a[m];
+      if constexpr (ADAPTED) row_id = ao.rows[m];
+    } else if constexpr (ADAPTED) {
+      row_id = -1;
     }
   };
   // LDS destinations (swizzled)
@@ -290,6 +310,7 @@ __device__ __forceinline__ void prefill_gemm_body(
       row_scale[tid] = __fdiv_rn(__fmul_rn(gm, row_ga), 127.0f);
       if constexpr (GATED) row_scale_up[tid] = __fdiv_rn(__fmul_rn(gm_up, row_ga), 127.0f);
       row_sum[tid] = row_rs;
+      if constexpr (ADAPTED) row_adapter[tid] = row_id >= 0 && row_id < ao.A ? row_id : -1;
     }
     gload(min(2, niter - 1), S0());
 #pragma unroll
@@ -333,10 +354,13 @@ __device__ __forceinline__ void prefill_gemm_body(
     const int64_t em0 = m0, en0 = n0;
     const int tn = t + static_cast<int>(gridDim.x);
     const bool more = tn < num_tiles;
-    if (more) {
-      set_tile(tn);
-      gload(0, S0());
-    }
+    auto request_next = [&] {
+      if (more) {
+        set_tile(tn);
+        gload(0, S0());
+      }
+    };
+    if constexpr (!ADAPTED) request_next();  // (the adapters' products need its registers)
 
     // epilogue: lane holds rows 8*(r/4) + 4*(l/32) + r%4, column l%32 of each
     // 32x32 tile.  The lane's first row and column are made opaque to the
@@ -345,6 +369,108 @@ __device__ __forceinline__ void prefill_gemm_body(
     int lrow = wm * (BM / WM) + 4 * lh;
     int lcol = wn * (OUT_BN / WN) + lr;
     asm volatile("" : "+v"(lrow), "+v"(lcol));
+    if constexpr (ADAPTED) {
+      // The adapters of the wave's rows, one after another: T as the row operand
+      // (lane: row lr, ranks 8 lh .. + 7), the second product's weights as the columns
+      // (8 loads a lane and block of 32, one rank each), three planes of T against one
+      // or three of the weights (adapters.hip).  A block's product is formed apart and
+      // added to the rows that are the adapter's.
+      static_assert(MI == 2, "64 rows of a wave");
+      constexpr int WT = EPI == 4 ? kBf16 : kF32;
+      const int my_id = row_adapter[wm * (BM / WM) + lane];
+      uint64_t todo = __ballot(my_id >= 0);
+      f32x16 y[MI][NI];
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = lrow + mi * 32 + 8 * (r >> 2) + (r & 3);
+          const int rs = row_sum[row];
+          const float scale = row_scale[row];
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni) y[mi][ni][r] = __fmul_rn(static_cast<float>(c[mi][ni][r] - rs), scale);
+        }
+      bf16x8 tp[MI][3];
+      if (todo) {
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+          const int64_t m = min(em0 + wm * (BM / WM) + mi * 32 + lr, M - 1);
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            tp[mi][p] = *reinterpret_cast<const bf16x8*>(ao.planes + p * ao.plane_stride + m * 16 + 8 * lh);
+        }
+      }
+      while (todo) {
+        const int a = __builtin_amdgcn_readlane(my_id, __builtin_ctzll(todo));
+        const uint64_t mine = __ballot(my_id == a);
+        todo &= ~mine;
+        const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char*>(ao.up) + static_cast<int64_t>(a) * ao.R * ao.ld * kBytes<WT>, 0,
+            static_cast<int>(((ao.R - 1) * ao.ld + N) * kBytes<WT>), kBufferFlags);
+        const uint32_t step = static_cast<uint32_t>(ao.ld) * kBytes<WT>;
+        const uint32_t at = 8u * lh * step + static_cast<uint32_t>(en0 + lcol) * kBytes<WT>;
+        // a block's weights are asked for while the block before is multiplied; more
+        // in flight would not fit the registers
+        uint32_t raw[2][8];
+        auto load_w = [&](int ni, uint32_t (&to)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t off = 8 * lh + i < ao.R ? at + i * step + 32u * ni * kBytes<WT> : kNowhere;
+            if constexpr (WT == kF32) to[i] = __builtin_amdgcn_raw_buffer_load_b32(wres, off, 0, 0);
+            else to[i] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(wres, off, 0, 0));
+          }
+        };
+        load_w(0, raw[0]);
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) {
+          if (ni + 1 < NI) load_w(ni + 1, raw[(ni + 1) & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+          Some<WT, 8> w;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (WT == kF32) w.w[i] = raw[ni & 1][i];
+            else if (i % 2 == 0) w.w[i / 2] = lower(raw[ni & 1][i], raw[ni & 1][i + 1]);
+          }
+          bf16x8 wp[kPlanes<WT>];
+          row_planes<WT>(w, wp);
+#pragma unroll
+          for (int mi = 0; mi < MI; ++mi) {
+            const uint32_t own = static_cast<uint32_t>(mine >> (32 * mi));
+            if (own == 0u) continue;
+            f32x16 d = {};
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+              for (int q = 0; q < kPlanes<WT>; ++q)
+                if (p + q <= 2) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(tp[mi][p], wp[q], d, 0, 0, 0);
+            if (own == 0xffffffffu) {
+#pragma unroll
+              for (int r = 0; r < 16; ++r) y[mi][ni][r] = __fadd_rn(y[mi][ni][r], d[r]);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 16; ++r) {
+                const float sum = __fadd_rn(y[mi][ni][r], d[r]);
+                y[mi][ni][r] = own >> (8 * (r >> 2) + 4 * lh + (r & 3)) & 1u ? sum : y[mi][ni][r];
+              }
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      request_next();
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t m = em0 + lrow + mi * 32 + 8 * (r >> 2) + (r & 3);
+          if (m >= M) continue;
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni) {
+            const int64_t n = en0 + lcol + ni * 32;
+            if (n < N) __builtin_nontemporal_store(y[mi][ni][r], Y + m * ldy + n);
+          }
+        }
+    } else {
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
 #pragma unroll
@@ -390,6 +516,7 @@ __device__ __forceinline__ void prefill_gemm_body(
           }
         }
       }
+    }
     }
     if (!more) break;
     t = tn;
