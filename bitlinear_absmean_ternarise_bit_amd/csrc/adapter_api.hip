@@ -27,12 +27,18 @@ int check_adapters(int64_t M, int64_t K, int64_t N, int64_t A, int64_t R, const 
 Range weights(const void* p, int w_dtype, int64_t A, int64_t R, int64_t C) { return array(p, w_dtype, A * R, C); }
 Range ids(const int32_t* rows, int64_t M) { return {rows, 4 * static_cast<uint64_t>(M)}; }
 
+// The planes behind a first product's parts.
+uint16_t* planes_of(void* ws, int64_t M, int64_t C, int64_t R) {
+  return reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + parts_ws_bytes(M, C, R));
+}
+
 int add_adapters(const void* X, int x_dtype, int64_t M, int64_t K, int64_t N, const Adapters& ad, const void* down,
                  const void* up, float* Y, float* T, void* ws, hipStream_t s) {
   float* parts = static_cast<float*>(ws);
   const hipError_t e = launch_shrink(X, x_dtype, M, K, ad, down, parts, s);
   if (e != hipSuccess) return BITLINEAR_ERR_HIP;
-  return hip_status(launch_expand(parts, M, K, N, ad, up, Y, true, T, s));
+  uint16_t* planes = planes_of(ws, M, K, ad.R);
+  return hip_status(launch_expand(parts, planes, M, K, N, ad, up, Y, true, T, s));
 }
 
 }  // namespace
@@ -106,7 +112,7 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
   } else {
     if (adapted_gemm_takes(K, N, R)) {
       float* parts = static_cast<float*>(workspace);
-      uint16_t* planes = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + shrink_ws_bytes(M, K, R));
+      uint16_t* planes = planes_of(workspace, M, K, R);
       e = launch_adapted_first(X, x_dtype, M, K, ad, down, parts, c.xq, c.ga, c.rs, s);
       if (e == hipSuccess) e = launch_join(parts, M, K, ad, T, planes, s);
       if (e == hipSuccess) e = launch_adapted_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, planes, ad, up, s);
@@ -157,7 +163,8 @@ int bitlinear_adapters_backward(const void* dY, int dy_dtype, const void* X, int
   if (dX || ddown) {
     e = launch_shrink(dY, dy_dtype, M, N, ad, up, parts, s);
     if (e == hipSuccess && dX)
-      e = launch_expand(parts, M, N, K, ad, down, dX, accumulate != 0, ddown ? V : nullptr, s);
+      e = launch_expand(parts, planes_of(workspace, M, N, R), M, N, K, ad, down, dX, accumulate != 0,
+                        ddown ? V : nullptr, s);
     else if (e == hipSuccess)
       e = launch_join(parts, M, N, ad, V, nullptr, s);
   }

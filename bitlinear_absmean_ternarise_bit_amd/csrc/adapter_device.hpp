@@ -16,7 +16,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kAdapterThreads = 256, kAdapterWaves = 4;
 constexpr int kBlock = 16;      // tokens of a block
-constexpr int kTileCols = 128;  // columns of a wave in expand
+constexpr int kExpandCols = 4;  // columns of a lane in expand
 constexpr int kGradCols = 4;    // columns of a lane in grad
 constexpr int64_t kMaxGrid = int64_t(1) << 20;  // workgroups; each walks every gridDim.x-th item
 

@@ -42,9 +42,9 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t C) {
 }
 
 // The second product, Y += T W over C columns: 2 blocks of 16 tokens to a
-// workgroup of 512 columns where that makes two workgroups for every CU, else 1.
+// workgroup of 256 columns where that makes two workgroups for every CU, else 1.
 inline int expand_blocks(int64_t M, int64_t C) {
-  return (M + 31) / 32 * ((C + 511) / 512) >= 512 ? 2 : 1;
+  return (M + 31) / 32 * ((C + 255) / 256) >= 512 ? 2 : 1;
 }
 
 // The gradients dW[a] = V^T X over C columns: workgroups of 64 columns, one
@@ -65,11 +65,15 @@ inline GradPlan grad_plan(int64_t M, int64_t C, int64_t A, int64_t R) {
   return p;
 }
 
-// Workspaces: T's parts [parts, M, padded_r(R)] float32; for the backward V's
-// parts, V, and the parts of whichever gradient needs more.
-inline size_t shrink_ws_bytes(int64_t M, int64_t C, int64_t R) {
+// Workspaces: T's parts [parts, M, padded_r(R)] float32 and its planes, bf16 [3, M,
+// padded_r(R)]; for the backward those of V, V itself, and the parts of whichever
+// gradient needs more.
+inline size_t parts_ws_bytes(int64_t M, int64_t C, int64_t R) {
   const ShrinkPlan p = shrink_plan(M, C);
   return align256(size_mul(size_mul(size_t(p.parts) * 4, size_t(M)), size_t(padded_r(R))));
+}
+inline size_t shrink_ws_bytes(int64_t M, int64_t C, int64_t R) {
+  return size_add(parts_ws_bytes(M, C, R), align256(size_mul(size_mul(size_t(M), 6), size_t(padded_r(R)))));
 }
 inline size_t grad_ws_bytes(int64_t M, int64_t C, int64_t A, int64_t R) {
   const GradPlan p = grad_plan(M, C, A, R);
@@ -77,8 +81,7 @@ inline size_t grad_ws_bytes(int64_t M, int64_t C, int64_t A, int64_t R) {
 }
 inline size_t adapters_ws_bytes(int64_t M, int64_t K, int64_t R) {
   if (!size_args_ok(M) || !size_args_ok(K) || !size_args_ok(R) || R > kAdapterMaxR) return 0;
-  // (with up to 16 ranks also T's planes, for the GEMM with the adapters)
-  return size_add(shrink_ws_bytes(M, K, R), R <= 16 ? align256(size_mul(size_t(M), 96)) : 256);
+  return shrink_ws_bytes(M, K, R);
 }
 inline size_t adapters_backward_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t A, int64_t R) {
   if (!size_args_ok(M) || !size_args_ok(K) || !size_args_ok(N) || !size_args_ok(R) || R > kAdapterMaxR || A < 1 ||
@@ -113,11 +116,12 @@ hipError_t launch_adapted_gemm(const int8_t* Xq, const float* ga, const int32_t*
 // parts of T = X W^T (rows without an adapter are not written)
 hipError_t launch_shrink(const void* X, int x_dtype, int64_t M, int64_t C, const Adapters& ad, const void* W,
                          float* parts, hipStream_t stream);
-// Y[m] (+)= scale T[m] W from T's parts (of a shrink over C0 columns); T: NULL,
-// or where the whole T goes ([M, R], zeros for rows without an adapter)
-hipError_t launch_expand(const float* parts, int64_t M, int64_t C0, int64_t C, const Adapters& ad, const void* W,
-                         float* Y, bool accumulate, float* T, hipStream_t stream);
-// T alone, and (R <= 16) its scaled planes bf16 [3][M][16]; each may be NULL
+// Y[m] (+)= scale T[m] W from T's parts (of a shrink over C0 columns); planes: room
+// for T's; T: NULL, or where the whole T goes ([M, R], zeros for rows without an
+// adapter)
+hipError_t launch_expand(const float* parts, uint16_t* planes, int64_t M, int64_t C0, int64_t C, const Adapters& ad,
+                         const void* W, float* Y, bool accumulate, float* T, hipStream_t stream);
+// T and its scaled planes, bf16 [3, M, padded_r(R)]; each may be NULL
 hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, uint16_t* planes,
                        hipStream_t stream);
 // dW[a] = scale[a] V^T X, V [M, R]; ws: grad_ws_bytes

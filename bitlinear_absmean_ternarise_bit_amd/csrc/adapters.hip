@@ -36,55 +36,66 @@ __global__ __launch_bounds__(kAdapterThreads, 2) void shrink_kernel(const char* 
 }
 
 // ---- expand ---------------------------------------------------------------------
-// A workgroup takes RB blocks of 16 tokens and 512 columns, 128 to a wave.  T's
-// parts are added once, scaled and split into planes in LDS; T itself leaves from
-// the workgroups of the first columns, if the caller wants it.
+// A workgroup takes RB blocks of 16 tokens and 64 CW columns, 16 CW to a wave.
+// T's planes come into LDS, with many tokens as join_kernel wrote them; with few
+// the parts are added, scaled and split here, which saves a launch, and T itself
+// leaves from the workgroups of the first columns, if the caller wants it.  (With
+// many tokens each of a row's workgroups would read all parts again: at
+// 2048x4096 and 64 ranks as much as Y itself.)
 // v_mfma_f32_16x16x16_bf16 with T as the rows (lane l: token l % 16, ranks
-// 4 (l / 16) .. + 3) and W as the columns: lane l loads eight consecutive columns
-// of its four rank rows, 16 or 32 bytes a load, and column j of each lane's eight
+// 4 (l / 16) .. + 3) and W as the columns: lane l loads CW consecutive columns
+// of its four rank rows, 16 or 32 bytes a load, and column j of each lane's
 // is an operand of its own, so no transposition through LDS is needed and a lane
-// ends with eight consecutive columns of four tokens of each block, which it adds
+// ends with CW consecutive columns of four tokens of each block, which it adds
 // to Y.
-template <int WT, int RB>
-__global__ __launch_bounds__(kAdapterThreads, 2) void expand_kernel(const float* __restrict__ parts, int nparts, int64_t M,
-                                                          int64_t C, Adapters ad, const char* __restrict__ W, float* Y,
+template <int WT, int RB, int CW>
+__global__ __launch_bounds__(kAdapterThreads, 2) void expand_kernel(const float* __restrict__ parts, int nparts,
+                                                          const uint16_t* __restrict__ planes, int64_t M, int64_t C, Adapters ad, const char* __restrict__ W, float* Y,
                                                           int accumulate, float* __restrict__ T, int64_t items,
                                                           int64_t tiles) {
-  // Y is asked for ahead of the products where the registers hold it beside
-  // them (float32 weights with two blocks: they do not)
-  constexpr bool kAhead = WT == kBf16 || RB == 1;
   extern __shared__ __align__(16) short low[];  // [3 planes][RB * 16 tokens][Rp + 4]
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int Rp = (ad.R + 15) & ~15, stride = Rp + 4, plane = RB * kBlock * stride;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t group = item / tiles, tile = item - group * tiles, m0 = group * (RB * kBlock);
-    for (int i = threadIdx.x; i < RB * kBlock * (Rp / 4); i += kAdapterThreads) {
-      const int token = i / (Rp / 4), r = 4 * (i - token * (Rp / 4));
-      const int64_t m = m0 + token;
-      const int id = m < M ? ad.rows[m] : -1;
-      const bool has = id >= 0 && id < ad.A;
-      f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (has) {
-        const float* from = parts + m * Rp + r;
-        t = *reinterpret_cast<const f32x4*>(from);
+    if (planes != nullptr) {  // formed by join_kernel
+      const int per_row = Rp / 8, n = RB * kBlock * per_row;
+      for (int i = threadIdx.x; i < 3 * n; i += kAdapterThreads) {
+        const int s = i / n, token = (i - s * n) / per_row, r = 8 * (i - s * n - token * per_row);
+        const u32x2* from = reinterpret_cast<const u32x2*>(planes + (s * M + min(m0 + token, M - 1)) * Rp + r);
+        u32x2* to = reinterpret_cast<u32x2*>(low + s * plane + token * stride + r);
+        to[0] = from[0];
+        to[1] = from[1];
+      }
+    } else {
+      for (int i = threadIdx.x; i < RB * kBlock * (Rp / 4); i += kAdapterThreads) {
+        const int token = i / (Rp / 4), r = 4 * (i - token * (Rp / 4));
+        const int64_t m = m0 + token;
+        const int id = m < M ? ad.rows[m] : -1;
+        const bool has = id >= 0 && id < ad.A;
+        f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (has) {
+          const float* from = parts + m * Rp + r;
+          t = *reinterpret_cast<const f32x4*>(from);
 #pragma unroll 4
-        for (int s = 1; s < nparts; ++s) t += *reinterpret_cast<const f32x4*>(from + static_cast<int64_t>(s) * M * Rp);
-      }
-      if (T != nullptr && tile == 0 && blockIdx.y == 0 && m < M) {
+          for (int s = 1; s < nparts; ++s) t += *reinterpret_cast<const f32x4*>(from + static_cast<int64_t>(s) * M * Rp);
+        }
+        if (T != nullptr && tile == 0 && blockIdx.y == 0 && m < M) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (r + k < ad.R) T[m * ad.R + r + k] = t[k];
-      }
-      s16x4 p[3];
-      value_planes(t * (has ? ad.scales[id] : 0.0f), p);
+          for (int k = 0; k < 4; ++k)
+            if (r + k < ad.R) T[m * ad.R + r + k] = t[k];
+        }
+        s16x4 p[3];
+        value_planes(t * (has ? ad.scales[id] : 0.0f), p);
 #pragma unroll
-      for (int s = 0; s < 3; ++s) *reinterpret_cast<s16x4*>(low + s * plane + token * stride + r) = p[s];
+        for (int s = 0; s < 3; ++s) *reinterpret_cast<s16x4*>(low + s * plane + token * stride + r) = p[s];
+      }
     }
     __syncthreads();
-    const int64_t n0 = (tile * kAdapterWaves + wave) * kTileCols;
+    const int64_t n0 = (tile * kAdapterWaves + wave) * (16 * CW);
     if (n0 < C) {
-      const Columns at = lane_columns<8>(C, n0 / 8 + l);
-      const bool inside = n0 + kTileCols <= C;
+      const Columns at = lane_columns<CW>(C, n0 / CW + l);
+      const bool inside = n0 + 16 * CW <= C;
       const int id = token_adapter(ad, m0, M, RB * kBlock, lane);
       // The group's rows of Y as a buffer resource: rows and columns that are not
       // to be touched lie at an offset past it, where loads give zeros and stores
@@ -95,54 +106,55 @@ __global__ __launch_bounds__(kAdapterThreads, 2) void expand_kernel(const float*
       auto y_at = [&](int token, uint64_t rows) {
         return rows >> token & 1u ? static_cast<uint32_t>(token) * row_bytes + y_col : kNowhere;
       };
-      auto store_row = [&](uint32_t off, const float (&v)[8]) {
+      auto store_row = [&](uint32_t off, const float (&v)[CW]) {
         if (inside) {
-          __builtin_amdgcn_raw_buffer_store_b128(v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                     __float_as_uint(v[3])}, yres, off, 0, 0);
-          __builtin_amdgcn_raw_buffer_store_b128(v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                                                     __float_as_uint(v[7])}, yres, off + 16u, 0, 0);
+#pragma unroll
+          for (int h = 0; h < CW / 4; ++h)
+            __builtin_amdgcn_raw_buffer_store_b128(v4u{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                                                       __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])},
+                                                   yres, off + 16u * h, 0, 0);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < CW; ++j)
             __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), yres, j >= at.skip ? off + 4u * j : kNowhere, 0,
                                                   0);
         }
       };
-      auto load_w = [&](int a, int r0, Some<WT, 8> (&w)[4]) {
+      auto load_w = [&](int a, int r0, Some<WT, CW> (&w)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          w[i] = load_some<WT, 8>(W + ((static_cast<int64_t>(a) * ad.R + min(r0 + 4 * g + i, ad.R - 1)) * C + at.first) *
+          w[i] = load_some<WT, CW>(W + ((static_cast<int64_t>(a) * ad.R + min(r0 + 4 * g + i, ad.R - 1)) * C + at.first) *
                                           kBytes<WT>);
       };
       each_adapter(id, gridDim.y, blockIdx.y, [&](int a, uint64_t mine) {
-        Some<WT, 8> w[4];
+        Some<WT, CW> w[4];
         load_w(a, 0, w);
-        v4u y[kAhead ? RB : 1][4][2];
-        auto load_y = [&](int b, v4u (&v)[4][2]) {
+        v4u y[RB][4][CW / 4];  // asked for ahead of the products
+        auto load_y = [&](int b, v4u (&v)[4][CW / 4]) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t off = y_at(kBlock * b + 4 * g + i, mine);
-            v[i][0] = __builtin_amdgcn_raw_buffer_load_b128(yres, off, 0, 0);
-            v[i][1] = __builtin_amdgcn_raw_buffer_load_b128(yres, off + 16u, 0, 0);
+#pragma unroll
+            for (int h = 0; h < CW / 4; ++h) v[i][h] = __builtin_amdgcn_raw_buffer_load_b128(yres, off + 16u * h, 0, 0);
           }
         };
-        if (kAhead && accumulate) {
+        if (accumulate) {
 #pragma unroll
           for (int b = 0; b < RB; ++b) load_y(b, y[b]);
         }
-        f32x4 d[RB][8];
+        f32x4 d[RB][CW];
 #pragma unroll
         for (int b = 0; b < RB; ++b)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int j = 0; j < CW; ++j) d[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int r0 = 0; r0 < ad.R; r0 += 16) {
           if (r0 + 16 > ad.R) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (r0 + 4 * g + i >= ad.R) w[i] = Some<WT, 8>{};
+              if (r0 + 4 * g + i >= ad.R) w[i] = Some<WT, CW>{};
           }
-          s16x4 wp[kPlanes<WT>][8];
-          column_planes<WT, 8>(w, wp);
+          s16x4 wp[kPlanes<WT>][CW];
+          column_planes<WT, CW>(w, wp);
           if (r0 + 16 < ad.R) load_w(a, r0 + 16, w);
 #pragma unroll
           for (int b = 0; b < RB; ++b) {
@@ -156,27 +168,26 @@ __global__ __launch_bounds__(kAdapterThreads, 2) void expand_kernel(const float*
               for (int s = 0; s < kPlanes<WT>; ++s)
                 if (p + s <= 2) {
 #pragma unroll
-                  for (int j = 0; j < 8; ++j)
+                  for (int j = 0; j < CW; ++j)
                     d[b][j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(tp[p], wp[s][j], d[b][j], 0, 0, 0);
                 }
           }
         }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-          if (!kAhead && accumulate) load_y(b, y[0]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float v[8];
+            float v[CW];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              v[j] = accumulate ? __fadd_rn(__uint_as_float(y[kAhead ? b : 0][i][j >> 2][j & 3]), d[b][j][i]) : d[b][j][i];
+            for (int j = 0; j < CW; ++j)
+              v[j] = accumulate ? __fadd_rn(__uint_as_float(y[b][i][j >> 2][j & 3]), d[b][j][i]) : d[b][j][i];
             store_row(y_at(kBlock * b + 4 * g + i, mine), v);
           }
         }
       });
       if (!accumulate && blockIdx.y == 0) {  // tokens without an adapter (the resource ends with the last token)
         const uint64_t none = ~__ballot(id >= 0);
-        const float zero[8] = {};
+        const float zero[CW] = {};
         for (int b = 0; b < RB; ++b)
           for (int i = 0; i < 4; ++i) store_row(y_at(kBlock * b + 4 * g + i, none), zero);
       }
@@ -470,28 +481,41 @@ hipError_t shrink_any(const void* X, int64_t M, int64_t C, const Adapters& ad, c
 }
 
 template <int WT, int RB>
-hipError_t expand_as(const float* parts, int nparts, int spread, int64_t M, int64_t C, const Adapters& ad,
-                     const void* W, float* Y, bool accumulate, float* T, hipStream_t s) {
+hipError_t expand_as(const float* parts, const ShrinkPlan& p, const uint16_t* planes, int64_t M, int64_t C,
+                     const Adapters& ad, const void* W, float* Y, bool accumulate, float* T, hipStream_t s) {
+  constexpr int CW = kExpandCols;
   const int64_t groups = (M + RB * kBlock - 1) / (RB * kBlock);
-  const int64_t tiles = (C + kAdapterWaves * kTileCols - 1) / (kAdapterWaves * kTileCols), items = groups * tiles;
-  const dim3 grid(static_cast<unsigned>(std::min(items, kMaxGrid)), spread);
+  const int64_t tiles = (C + kAdapterWaves * 16 * CW - 1) / (kAdapterWaves * 16 * CW), items = groups * tiles;
+  const dim3 grid(static_cast<unsigned>(std::min(items, kMaxGrid)), planes ? 1 : p.spread);
   const size_t lds = size_t(3) * RB * kBlock * (padded_r(ad.R) + 4) * 2;
-  expand_kernel<WT, RB><<<grid, kAdapterThreads, lds, s>>>(parts, nparts, M, C, ad, static_cast<const char*>(W), Y, accumulate,
-                                                    T, items, tiles);
+  expand_kernel<WT, RB, CW><<<grid, kAdapterThreads, lds, s>>>(parts, p.parts, planes, M, C, ad,
+                                                               static_cast<const char*>(W), Y, accumulate, T, items,
+                                                               tiles);
   return hipGetLastError();
 }
 
 template <int WT>
-hipError_t expand_any(const float* parts, int64_t M, int64_t C0, int64_t C, const Adapters& ad, const void* W, float* Y,
-                      bool accumulate, float* T, hipStream_t s) {
+hipError_t expand_any(const float* parts, uint16_t* planes, int64_t M, int64_t C0, int64_t C, const Adapters& ad,
+                      const void* W, float* Y, bool accumulate, float* T, hipStream_t s) {
   const ShrinkPlan p = shrink_plan(M, C0);
   if (few_or_many(C)) {
     expand_short_kernel<WT><<<flat_grid(M * C), kAdapterThreads, 0, s>>>(parts, p.parts, M, C, ad,
                                                                  static_cast<const char*>(W), Y, accumulate);
     return T ? launch_join(parts, M, C0, ad, T, nullptr, s) : hipGetLastError();
   }
-  return expand_blocks(M, C) == 2 ? expand_as<WT, 2>(parts, p.parts, 1, M, C, ad, W, Y, accumulate, T, s)
-                                  : expand_as<WT, 1>(parts, p.parts, p.spread, M, C, ad, W, Y, accumulate, T, s);
+  // A launch of its own for the planes (5 us) where a workgroup's parts are at least
+  // half of the rows of Y that it reads and writes: 2048x4096, 64 ranks in 8 parts
+  // 31 us without it and 25 with; 700x4096, 16 ranks in 4 parts 8.4 either way.
+  if (p.blocks == 1 || padded_r(ad.R) * p.parts < 256) {
+    planes = nullptr;
+  } else {
+    const hipError_t e = launch_join(parts, M, C0, ad, T, planes, s);
+    if (e != hipSuccess) return e;
+    T = nullptr;
+  }
+  return p.blocks == 4 && expand_blocks(M, C) == 2
+             ? expand_as<WT, 2>(parts, p, planes, M, C, ad, W, Y, accumulate, T, s)
+             : expand_as<WT, 1>(parts, p, planes, M, C, ad, W, Y, accumulate, T, s);
 }
 
 template <int XT>
@@ -528,10 +552,10 @@ hipError_t launch_shrink(const void* X, int x_dtype, int64_t M, int64_t C, const
                             : shrink_any<kBf16, kBf16>(X, M, C, ad, W, parts, s);
 }
 
-hipError_t launch_expand(const float* parts, int64_t M, int64_t C0, int64_t C, const Adapters& ad, const void* W,
-                         float* Y, bool accumulate, float* T, hipStream_t s) {
-  return ad.w_dtype == kF32 ? expand_any<kF32>(parts, M, C0, C, ad, W, Y, accumulate, T, s)
-                            : expand_any<kBf16>(parts, M, C0, C, ad, W, Y, accumulate, T, s);
+hipError_t launch_expand(const float* parts, uint16_t* planes, int64_t M, int64_t C0, int64_t C, const Adapters& ad,
+                         const void* W, float* Y, bool accumulate, float* T, hipStream_t s) {
+  return ad.w_dtype == kF32 ? expand_any<kF32>(parts, planes, M, C0, C, ad, W, Y, accumulate, T, s)
+                            : expand_any<kBf16>(parts, planes, M, C0, C, ad, W, Y, accumulate, T, s);
 }
 
 hipError_t launch_join(const float* parts, int64_t M, int64_t C0, const Adapters& ad, float* T, uint16_t* planes,

@@ -59,7 +59,7 @@ def test_sizes(lib):
             assert h(*a) == 0
     assert f(40, 64, 64, 257) == 0 and h(40, 64, 64, 65536, 4) == 0
     for M, K, N, R in ((1, 1, 1, 1), (16, 4096, 4096, 16), (2048, 4096, 11008, 64), (8192, 8192, 28672, 256)):
-        assert f(M, K, N, R) % 256 == 0 and 4 * M * R <= f(M, K, N, R) <= 16 * 4 * M * (R + 15) + 96 * M + 512
+        assert f(M, K, N, R) % 256 == 0 and 4 * M * R <= f(M, K, N, R) <= 16 * 4 * M * (R + 15) + 6 * M * (R + 15) + 512
         assert h(M, K, N, 1, R) % 256 == 0 and h(M, K, N, 1, R) >= 8 * M * R
         assert g(M, K, N, R) == f(M, K, N, R) + lib.bitlinear_forward_workspace_bytes(M, K)
 
