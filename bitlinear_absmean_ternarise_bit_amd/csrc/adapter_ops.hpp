@@ -51,13 +51,14 @@ inline int expand_blocks(int64_t M, int64_t C) {
 // adapter and up to 64 of its R rows, cut along the tokens into parts that a
 // second launch adds.
 struct GradPlan {
-  int tiles, groups, parts;
+  int64_t tiles;
+  int groups, parts;
 };
 inline GradPlan grad_plan(int64_t M, int64_t C, int64_t A, int64_t R) {
   GradPlan p;
-  p.tiles = static_cast<int>((C + 63) / 64);
+  p.tiles = (C + 63) / 64;
   p.groups = static_cast<int>((R + 63) / 64);
-  int64_t parts = 512 / (int64_t(p.tiles) * p.groups * A);
+  int64_t parts = 512 / (p.tiles * p.groups * A);
   const int64_t most = (M + 255) / 256;  // at least 64 tokens to a wave
   if (parts > most) parts = most;
   if (parts > 16) parts = 16;

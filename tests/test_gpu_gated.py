@@ -101,7 +101,8 @@ def test_hidden_layer(M, D, F, dt):
 
 def test_tiles_of_every_kind():
     # 256 x 128 tiles alone, with a last round of 128 x 128 ones (two launches), and 128-token tiles
-    for M, D, F in ((2048, 64, 4096), (2048, 128, 5000), (1024, 192, 2900), (128, 64, 3200), (300, 64, 20000)):
+    for M, D, F in ((2048, 64, 4096), (2048, 128, 5000), (1024, 192, 2900), (128, 64, 3200), (300, 64, 20000),
+                    (1024, 64, 11008), (500, 64, 5632), (300, 64, 11008), (33, 64, 11008), (2300, 64, 11008)):
         print(f"tiles M={M} F={F}", flush=True)
         P = Problem(M, D, F, dt="bf16")
         h, g, u = bl.gated_forward(P.x, P.gate.gpu, P.up.gpu, save=torch.float32)
