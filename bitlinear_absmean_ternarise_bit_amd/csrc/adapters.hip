@@ -379,9 +379,9 @@ __global__ __launch_bounds__(kAdapterThreads) void grad_join_kernel(const float*
   }
 }
 
-// ---- fewer than 8 columns, or more than 2^24 ---------------------------------------
-// A lane's eight columns do not fit, or a group's rows of Y do not fit a buffer
-// resource: one thread to a value, float32 sums.
+// ---- fewer than 8 columns (expand: or more than 2^24) -------------------------------
+// A lane's eight columns do not fit (a group's rows of Y do not fit a buffer
+// resource): one thread to a value, float32 sums.
 template <int DT>
 __device__ __forceinline__ float value_at(const char* p, int64_t i) {
   if constexpr (DT == kF32) return reinterpret_cast<const float*>(p)[i];
@@ -453,7 +453,8 @@ unsigned flat_grid(int64_t n) {
   return static_cast<unsigned>(std::min<int64_t>((n + kAdapterThreads - 1) / kAdapterThreads, int64_t(1) << 16));
 }
 
-bool few_or_many(int64_t C) { return C < 8 || C > (int64_t(1) << 24); }
+// Columns for the short kernels.  (Such few columns are one part of a shrink.)
+bool few(int64_t C) { return C < 8; }
 
 template <int XT, int WT, int RB>
 hipError_t shrink_as(const void* X, int64_t M, int64_t C, const Adapters& ad, const void* W, float* parts,
@@ -471,7 +472,7 @@ template <int XT, int WT>
 hipError_t shrink_any(const void* X, int64_t M, int64_t C, const Adapters& ad, const void* W, float* parts,
                       hipStream_t s) {
   const ShrinkPlan p = shrink_plan(M, C);
-  if (few_or_many(C)) {
+  if (few(C)) {
     shrink_short_kernel<XT, WT><<<flat_grid(M * padded_r(ad.R)), kAdapterThreads, 0, s>>>(
         static_cast<const char*>(X), M, C, ad, static_cast<const char*>(W), parts);
     return hipGetLastError();
@@ -498,7 +499,7 @@ template <int WT>
 hipError_t expand_any(const float* parts, uint16_t* planes, int64_t M, int64_t C0, int64_t C, const Adapters& ad,
                       const void* W, float* Y, bool accumulate, float* T, hipStream_t s) {
   const ShrinkPlan p = shrink_plan(M, C0);
-  if (few_or_many(C)) {
+  if (few(C) || C > (int64_t(1) << 24)) {
     expand_short_kernel<WT><<<flat_grid(M * C), kAdapterThreads, 0, s>>>(parts, p.parts, M, C, ad,
                                                                  static_cast<const char*>(W), Y, accumulate);
     return T ? launch_join(parts, M, C0, ad, T, nullptr, s) : hipGetLastError();
@@ -521,7 +522,7 @@ hipError_t expand_any(const float* parts, uint16_t* planes, int64_t M, int64_t C
 template <int XT>
 hipError_t grad_as(const float* V, const void* X, int64_t M, int64_t C, const Adapters& ad, float* dW, float* ws,
                    hipStream_t s) {
-  if (few_or_many(C)) {
+  if (few(C)) {
     const int64_t n = int64_t(ad.A) * ad.R * C;
     grad_short_kernel<XT><<<static_cast<unsigned>(std::min(n, kMaxGrid)), kAdapterThreads, 0, s>>>(
         V, static_cast<const char*>(X), M, C, ad, dW, n);

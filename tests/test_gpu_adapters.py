@@ -253,6 +253,40 @@ def test_more_outputs_than_32_bits():
         assert (y[m].double() - ref).abs().max() <= 1e-4 * (1 if a < 2 else 0)  # 12 terms of at most 50, 2^-24 each
 
 
+@pytest.mark.parametrize("M", [5, 260])
+def test_gradients_of_very_long_outputs(M):
+    # more than 2^24 outputs, V's sums in several parts; positive values, so a part that is lost shows
+    K, N, R = 16, (1 << 24) + 12, 2
+    g = torch.Generator(device=DEV).manual_seed(M)
+    pos = lambda *s: torch.rand(*s, generator=g, device=DEV) + 0.5  # noqa: E731
+    dy = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    for m in range(M):
+        dy[m] = pos(N)
+    x, t, ads = pos(M, K), pos(M, R), (pos(2, R, K), pos(2, R, N), pos(2))
+    ids = (torch.arange(M, device=DEV) % 3).to(torch.int32)  # 2: none
+    need = bl.abi.load().bitlinear_adapters_backward_workspace_bytes(M, K, N, 2, R)
+    ws = torch.full((need // 4,), float("nan"), device=DEV)
+    dx, dd, du = bl.adapters_backward(dy, x, t, ads, ids, workspace=ws)
+    V = torch.zeros(M, R, dtype=torch.float64, device=DEV)
+    for m in range(M):
+        if m % 3 < 2:
+            V[m] = float(ads[2][m % 3]) * (ads[1][m % 3].double() @ dy[m].double())
+    # a term passes at most the 2^24 / 32 / 4 steps of a wave (M = 260 has one part), four roundings each,
+    # and fewer than 400 others
+    tol = (4 * 131073 + 400) * U24
+    for a in range(2):
+        at = torch.arange(a, M, 3, device=DEV)
+        ref = V[at] @ ads[0][a].double()
+        assert ((dx[at] - ref).abs() <= tol * ref).all()
+        ref = V[at].T @ x[at].double()
+        assert ((dd[a] - ref).abs() <= tol * ref).all()
+        for n0 in range(0, N, 1 << 22):
+            part = slice(n0, n0 + (1 << 22))
+            ref = float(ads[2][a]) * (t[at].double().T @ dy[at][:, part].double())
+            assert ((du[a][:, part] - ref).abs() <= (M + 72) * U24 * ref).all()
+    assert not dx[2::3].any()
+
+
 def test_refused_on_the_gpu():
     P = Problem(4, 64, 32, 2, 2)
     y = torch.zeros(4, 32, device=DEV)
