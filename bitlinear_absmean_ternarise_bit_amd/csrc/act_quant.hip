@@ -155,11 +155,12 @@ hipError_t launch_dt(const void* X, int64_t M, int64_t K, int8_t* Xq, float* gam
   const int64_t chunks_per_lane = (K * esize / 16 + kWave - 1) / kWave;
   const char* rows = static_cast<const char*>(X);
   const int k = static_cast<int>(K), kp = static_cast<int>(Kp);
+  const bool a_group_each = M < (int64_t(1) << 24);  // a launch holds fewer than 2^32 threads
   if (!vec && K >= 8 && Kp <= 2048)
     act_quant_any_kernel<DT, 4, 1><<<blocks, 256, 0, stream>>>(rows, M, k, kp, Xq, gamma_a, rowsum);
-  else if (!vec && K >= 8 && Kp <= 8192)
+  else if (!vec && K >= 8 && Kp <= 8192 && a_group_each)
     act_quant_any_kernel<DT, 4, 4><<<static_cast<unsigned>(M), 256, 0, stream>>>(rows, M, k, kp, Xq, gamma_a, rowsum);
-  else if (!vec && K >= 8 && Kp <= 28672)
+  else if (!vec && K >= 8 && Kp <= 28672 && a_group_each)
     act_quant_any_kernel<DT, 14, 4><<<static_cast<unsigned>(M), 256, 0, stream>>>(rows, M, k, kp, Xq, gamma_a, rowsum);
   else if (!vec)
     act_quant_kernel<DT, false, 4><<<blocks, 256, 0, stream>>>(X, M, K, Kp, Xq, gamma_a, rowsum);

@@ -276,6 +276,24 @@ def test_codes_of_rows_of_any_length(K, dt):
         assert same(np_of(ga), gA) and np.array_equal(rs.cpu().numpy(), r)
 
 
+def test_codes_of_more_rows_than_a_launch_has_groups():
+    M, K = 1 << 24, 2049  # 69 GB, in rows that are not aligned
+    if torch.cuda.mem_get_info()[0] < 140 << 30:
+        pytest.skip("needs 140 GB of GPU memory")
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    at = [0, 1, (1 << 23) + 3, M - 1]
+    X = to_type(np.random.default_rng(5).standard_normal((len(at), K)), "bf16")
+    for i, m in enumerate(at):
+        x[m] = on_gpu(X[i], "bf16")
+    Xq, ga, rs = bl.quantize_activations(x)
+    del x
+    gA, q, r = O.absmax_quantize(X)
+    assert np.array_equal(Xq[at].cpu().numpy()[:, :K], q) and same(np_of(ga[at]), gA)
+    assert np.array_equal(rs[at].cpu().numpy(), r) and int(ga.count_nonzero()) == len(at)
+    del Xq
+    torch.cuda.empty_cache()
+
+
 def test_refused_on_the_gpu():
     P = Problem(4, 64, 32)
     w = P.gate.gpu
