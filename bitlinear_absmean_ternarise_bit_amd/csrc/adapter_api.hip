@@ -107,17 +107,22 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
   if (piece)
     return hip_status(launch_adapted_decode(X, x_dtype, M, K, packed, N, gamma, Y, ad, down, up,
                                             static_cast<float*>(workspace), T, piece, c.xq, c.ga, c.rs, s));
+  if (!decode && K >= 8) {
+    float* parts = static_cast<float*>(workspace);
+    uint16_t* planes = planes_of(workspace, M, K, R);
+    e = launch_adapted_first(X, x_dtype, M, K, ad, down, parts, c.xq, c.ga, c.rs, s);
+    if (adapted_gemm_takes(M, N, R)) {
+      if (e == hipSuccess) e = launch_join(parts, M, K, ad, T, planes, s);
+      if (e == hipSuccess) e = launch_adapted_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, planes, ad, up, s);
+    } else {
+      if (e == hipSuccess) e = launch_prefill_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, nullptr, s);
+      if (e == hipSuccess) e = launch_expand(parts, planes, M, K, N, ad, up, Y, true, T, s);
+    }
+    return hip_status(e);
+  }
   if (decode) {
     e = launch_decode(X, x_dtype, M, K, packed, N, gamma, Y, nullptr, 1, s);
   } else {
-    if (adapted_gemm_takes(K, N, R)) {
-      float* parts = static_cast<float*>(workspace);
-      uint16_t* planes = planes_of(workspace, M, K, R);
-      e = launch_adapted_first(X, x_dtype, M, K, ad, down, parts, c.xq, c.ga, c.rs, s);
-      if (e == hipSuccess) e = launch_join(parts, M, K, ad, T, planes, s);
-      if (e == hipSuccess) e = launch_adapted_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, planes, ad, up, s);
-      return hip_status(e);
-    }
     e = launch_act_quant(X, x_dtype, M, K, c.xq, c.ga, c.rs, s);
     if (e == hipSuccess) e = launch_prefill_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, nullptr, s);
   }

@@ -24,8 +24,9 @@ inline int64_t padded_r(int64_t R) { return (R + 15) / 16 * 16; }
 // The first product, T = X W^T over C columns: `blocks` blocks of 16 tokens to a
 // workgroup (4 with 256 tokens or more, so that W is read once for 64), cut along
 // the columns where those are few, into parts that are added by whoever reads T.
-// `spread`: that many workgroups share the adapters of a block (each takes every
-// spread-th one).
+// `spread`: that many workgroups share the adapters of a group of tokens, each
+// taking every spread-th one, where there are fewer than one to a CU without it
+// (612x1280, 13 requests of 32 ranks: 17 us alone, 10 with 4).
 struct ShrinkPlan {
   int blocks, spread, parts;
 };
@@ -38,6 +39,10 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t C) {
   if (parts > most) parts = most;
   if (parts > 16) parts = 16;
   p.parts = static_cast<int>(parts < 1 ? 1 : parts);
+  if (p.blocks == 4) {
+    const int64_t room = 256 / (groups * p.parts);
+    p.spread = static_cast<int>(room < 1 ? 1 : room < 4 ? room : 4);
+  }
   return p;
 }
 
@@ -45,6 +50,14 @@ inline ShrinkPlan shrink_plan(int64_t M, int64_t C) {
 // workgroup of 256 columns where that makes two workgroups for every CU, else 1.
 inline int expand_blocks(int64_t M, int64_t C) {
   return (M + 31) / 32 * ((C + 255) / 256) >= 512 ? 2 : 1;
+}
+// How many workgroups share the adapters of such a group: as for the first product
+// while the GPU is not full (each of them adds up T's parts again): 128x11008, one
+// request to a group, 16 of them 19.6 us and 2 10.2; 200x5632, a request to a token,
+// 16 of them 31 us, one 28 and 3 20.
+inline int expand_spread(const ShrinkPlan& p, int64_t items) {
+  const int64_t room = (p.blocks == 4 ? 512 : 1024) / items;
+  return static_cast<int>(room < 1 ? 1 : room < p.spread ? room : p.spread);
 }
 
 // The gradients dW[a] = V^T X over C columns: workgroups of 64 columns, one
@@ -106,10 +119,13 @@ hipError_t launch_adapted_decode(const void* X, int x_dtype, int64_t M, int64_t 
 // The first product and the tokens' codes in one launch (K >= 8).
 hipError_t launch_adapted_first(const void* X, int x_dtype, int64_t M, int64_t K, const Adapters& ad, const void* down,
                                 float* parts, int8_t* Xq, float* ga, int32_t* rs, hipStream_t stream);
-// The prefill GEMM with the second product in its epilogue, where the ranks are
-// few (16) and its 32-bit offsets hold; planes: launch_join's.
-inline bool adapted_gemm_takes(int64_t K, int64_t N, int64_t R) {
-  return R <= 16 && K >= 8 && N >= 8 && N <= (int64_t(1) << 24);
+// The prefill GEMM with the second product in its epilogue: where the ranks are few
+// (16), its 32-bit offsets hold, and the tokens are so many that those of a tile's
+// wave, 64, are likely of few adapters, which it takes one after another (4096x4096:
+// 128 tokens of 4 requests 32 us, as a pass of its own 34; 64 of 16 requests 41 and
+// 34); planes: launch_join's.
+inline bool adapted_gemm_takes(int64_t M, int64_t N, int64_t R) {
+  return M >= 128 && R <= 16 && N >= 8 && N <= (int64_t(1) << 24);
 }
 hipError_t launch_adapted_gemm(const int8_t* Xq, const float* ga, const int32_t* rs, int64_t M, int64_t K,
                                const uint32_t* packed, int64_t N, const float* gamma, float* Y, const uint16_t* planes,

@@ -233,7 +233,8 @@ __global__ __launch_bounds__(kAdapterThreads) void join_kernel(const float* __re
 // A workgroup takes 64 columns, one adapter, RT tiles of 16 ranks and one part
 // of the tokens; each of its four waves a quarter of those, 16 tokens at a time
 // (blocks without one of the adapter's are passed over), with the next block's
-// loads on their way.  V is the row operand (lane l: rank l % 16, tokens
+// loads on their way.  Parts and waves take blocks in turn, so that a request's
+// tokens, which lie together, are shared by all of them.  V is the row operand (lane l: rank l % 16, tokens
 // 4 (l / 16) .. + 3), X the columns as in expand.  The waves' sums meet in LDS,
 // and each wave then writes one of every four ranks.
 template <int XT, int RT>
@@ -255,21 +256,21 @@ __global__ __launch_bounds__(kAdapterThreads, 2) void grad_kernel(const float* _
     const int r0 = group * 16 * RT;
     const Columns at = lane_columns<CW>(C, tile * 16 + l);
     const int64_t q = static_cast<int64_t>(part) * kAdapterWaves + wave, Q = static_cast<int64_t>(nparts) * kAdapterWaves;
-    const int64_t lo = q * blocks / Q, hi = (q + 1) * blocks / Q;
     f32x4 acc[RT][CW];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int j = 0; j < CW; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // The adapter's tokens, 64 at a time, the ids of the next 64 already loaded.
-    auto ids_at = [&](int64_t b) {
-      const int64_t m = b * kBlock + lane;
-      return m < min(hi * kBlock, M) ? ad.rows[m] : -1;
+    // The adapter's tokens in blocks q, q + Q, q + 2 Q ..., four blocks at a time, the
+    // ids of the next four already loaded.
+    auto ids_at = [&](int64_t i) {
+      const int64_t m = (q + Q * (i + g)) * kBlock + l;
+      return m < M ? ad.rows[m] : -1;
     };
-    int64_t base = lo;
+    int64_t base = 0;
     int sub = 0;
-    uint64_t here = __ballot(ids_at(lo) == a);
-    int ids_next = ids_at(lo + 4);
+    uint64_t here = __ballot(ids_at(0) == a);
+    int ids_next = ids_at(4);
     auto next = [&](uint32_t& mine) -> int64_t {  // the next block that holds one of them, -1 at the end
       for (;;) {
         if (sub == 4) {
@@ -278,9 +279,10 @@ __global__ __launch_bounds__(kAdapterThreads, 2) void grad_kernel(const float* _
           here = __ballot(ids_next == a);
           ids_next = ids_at(base + 4);
         }
-        if (base + sub >= hi) return -1;
+        const int64_t b = q + Q * (base + sub);
+        if (b >= blocks) return -1;
         mine = static_cast<uint32_t>(here >> (16 * sub)) & 0xffffu;
-        const int64_t b = base + sub++;
+        ++sub;
         if (mine) return b;
       }
     };
@@ -487,7 +489,7 @@ hipError_t expand_as(const float* parts, const ShrinkPlan& p, const uint16_t* pl
   constexpr int CW = kExpandCols;
   const int64_t groups = (M + RB * kBlock - 1) / (RB * kBlock);
   const int64_t tiles = (C + kAdapterWaves * 16 * CW - 1) / (kAdapterWaves * 16 * CW), items = groups * tiles;
-  const dim3 grid(static_cast<unsigned>(std::min(items, kMaxGrid)), planes ? 1 : p.spread);
+  const dim3 grid(static_cast<unsigned>(std::min(items, kMaxGrid)), planes ? 1 : expand_spread(p, items));
   const size_t lds = size_t(3) * RB * kBlock * (padded_r(ad.R) + 4) * 2;
   expand_kernel<WT, RB, CW><<<grid, kAdapterThreads, lds, s>>>(parts, p.parts, planes, M, C, ad,
                                                                static_cast<const char*>(W), Y, accumulate, T, items,

@@ -381,10 +381,11 @@ int main() {
     g_piece = 4;
     CHECK(c.whole(4, 100, 8, 4, 9) == BITLINEAR_OK && launched(0, "adapted_decode "));
     c.path = BITLINEAR_PATH_PREFILL;
-    CHECK(c.whole(4, 100, 8, 4, 9) == BITLINEAR_OK && launched(0, "first join adapted_gemm "));
-    CHECK(c.whole(4, 100, 8, 4, 17) == BITLINEAR_OK && launched(2, "shrink expand "));
-    CHECK(c.whole(4, 7, 8, 4, 9) == BITLINEAR_OK && launched(2, "shrink expand "));
-    CHECK(c.whole(4, 8, 7, 4, 9) == BITLINEAR_OK && launched(2, "shrink expand "));
+    CHECK(c.whole(128, 100, 8, 4, 9) == BITLINEAR_OK && launched(0, "first join adapted_gemm "));
+    CHECK(c.whole(127, 100, 8, 4, 9) == BITLINEAR_OK && launched(1, "first expand "));
+    CHECK(c.whole(128, 100, 8, 4, 17) == BITLINEAR_OK && launched(1, "first expand "));
+    CHECK(c.whole(128, 7, 8, 4, 9) == BITLINEAR_OK && launched(2, "shrink expand "));
+    CHECK(c.whole(128, 8, 7, 4, 9) == BITLINEAR_OK && launched(1, "first expand "));
     g_piece = 0;
     CHECK(l.back(5, 100, 9, 4, 8, dX, nullptr, nullptr, 1) == BITLINEAR_OK && launched(0, "shrink expand "));
     CHECK(l.back(5, 100, 9, 4, 8, nullptr, dd, nullptr) == BITLINEAR_OK && launched(0, "shrink join grad "));
@@ -408,7 +409,7 @@ int main() {
   stub_reset(0);
   CHECK(g.block(2, 8, 8, 8) == BITLINEAR_ERR_HIP && launched(1, "gated_decode "));
   stub_reset(0);
-  CHECK(l.whole(300, 8, 8, 4, 17) == BITLINEAR_ERR_HIP && launched(1, ""));
+  CHECK(l.whole(300, 8, 8, 4, 17) == BITLINEAR_ERR_HIP && launched(1, "first "));
 
   // size queries saturate to 0
   for (int64_t v : {int64_t(0), int64_t(-1), I64MAX, I64MIN, (int64_t(1) << 40) + 1}) {
