@@ -944,8 +944,9 @@ def gated_input_backward(dG, dU, gateT, upT, K: int, out=None, workspace=None):
     up_, ug, _ = _ternary(B, upT, F, K, device.index, "upT")
     dX = _output(B, out, M, K, B.f32, device)
     need = 0
-    if workspace is None and (F % 8 or dG.data_ptr() % 16 or dU.data_ptr() % 16):
-        need = B.gated_input_backward_workspace_bytes(M, F)
+    if workspace is None:
+        copies = bool(F % 8 or dG.data_ptr() % 16 or dU.data_ptr() % 16)
+        need = B.gated_input_backward_workspace_bytes(M, F, K, copies)
     wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
     B.launch(B.gated_input_backward, device, dG.data_ptr(), dU.data_ptr(), M, F, K, gp, gg, up_, ug, dX.data_ptr(),
              wsp, ws_bytes)

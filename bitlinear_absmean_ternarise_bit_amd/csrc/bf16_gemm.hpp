@@ -80,7 +80,8 @@ __device__ __forceinline__ void store_masked(const f32x16 (&acc)[MI][NI], char* 
 // EPI 2: the sum of two products of the same shapes, gamma (A B^T) + gamma2
 // (A2 B2^T): the stages of the second follow those of the first without a
 // break, and the first one's accumulators are scaled and put by in between (64
-// more registers a lane with 256 x 128 tiles).
+// more registers a lane with 256 x 128 tiles).  Of each product the stages
+// first .. first + count - 1 are taken.
 // EPI 0: C * gamma;  EPI 1: C where bit q of row p of the range mask is set
 // (mask: rows of kw 32-bit words, bit q % 32 of word q / 32), else 0.
 //
@@ -96,6 +97,7 @@ struct SecondProduct {
   const uint16_t* A;
   const void* B;
   const float* gamma;
+  int first, count;
 };
 
 template <int BM, int BN, int WM, int WN, int BMODE, int EPI>
@@ -135,7 +137,7 @@ __device__ __forceinline__ void bf16_gemm_nt_body(
   const int64_t p0 = static_cast<int64_t>(first_p + in_group % gsize) * BM;
   const int64_t q0 = static_cast<int64_t>(in_group / gsize) * BN;
 
-  const int half = static_cast<int>(Rp / BK);  // stages of a product
+  const int half = EPI == 2 ? second.count : static_cast<int>(Rp / BK);  // stages of a product
   const int niter = EPI == 2 ? 2 * half : half;
   const uint32_t rowbytes = static_cast<uint32_t>(Rp) * 2u;
   const uint32_t rowbytes_a = static_cast<uint32_t>(lda) * 2u;
@@ -195,7 +197,7 @@ __device__ __forceinline__ void bf16_gemm_nt_body(
       const bool two = it >= half;
       gload_from(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(two ? second.A : A), 0, bytes_a, 0x00020000),
                  __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(two ? second.B : B), 0, bytes_b, 0x00020000),
-                 two ? it - half : it, set_tag);
+                 second.first + (two ? it - half : it), set_tag);
     } else {
       gload_from(rsrc_a, rsrc_b, it, set_tag);
     }

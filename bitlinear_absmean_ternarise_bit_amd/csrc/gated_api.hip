@@ -162,8 +162,8 @@ int bitlinear_gated_backward(const void* dH, int dh_dtype, const void* G, const 
                                           static_cast<hipStream_t>(stream)));
 }
 
-size_t bitlinear_gated_input_backward_workspace_bytes(int64_t M, int64_t F) {
-  return gated_input_backward_ws_bytes(M, F);
+size_t bitlinear_gated_input_backward_workspace_bytes(int64_t M, int64_t F, int64_t D, int copies) {
+  return gated_input_backward_ws_bytes(M, F, D, copies != 0);
 }
 
 int bitlinear_gated_input_backward(const uint16_t* dG, const uint16_t* dU, int64_t M, int64_t F, int64_t D,
@@ -181,7 +181,7 @@ int bitlinear_gated_input_backward(const uint16_t* dG, const uint16_t* dU, int64
       !aligned(gamma_gate, 4) || !aligned(gamma_up, 4) || !aligned(dX, 4))
     return BITLINEAR_ERR_ALIGN;
   const bool direct = F % 8 == 0 && aligned(dG, 16) && aligned(dU, 16);
-  const size_t need = direct ? 0 : gated_input_backward_ws_bytes(M, F);
+  const size_t need = gated_input_backward_ws_bytes(M, F, D, !direct), sums = gated_dx_parts_bytes(M, F, D);
   if (need) {
     if (!workspace || workspace_bytes < need) return BITLINEAR_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return BITLINEAR_ERR_ALIGN;
@@ -191,8 +191,10 @@ int bitlinear_gated_input_backward(const uint16_t* dG, const uint16_t* dU, int64
                       packed_range(packedT_gate, D, F),   packed_range(packedT_up, D, F),
                       floats(gamma_gate, 1),              floats(gamma_up, 1)};
   if (any_overlap(out, in)) return BITLINEAR_ERR_ARG;
+  void* copies = direct ? nullptr : static_cast<char*>(workspace) + sums;
   return hip_status(launch_gated_input_backward(dG, dU, M, F, D, packedT_gate, gamma_gate, packedT_up, gamma_up, dX,
-                                                need ? workspace : nullptr, static_cast<hipStream_t>(stream)));
+                                                static_cast<float*>(workspace), copies,
+                                                static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

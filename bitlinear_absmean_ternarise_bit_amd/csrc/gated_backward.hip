@@ -59,14 +59,30 @@ hipError_t launch_to(const void* dH, const void* G, const void* U, int64_t n, in
                          : launch_as<HT, GT, kBf16>(dH, G, U, n, act, dG, dU, s);
 }
 
-// C[p, q] = gamma A B^T + gamma2 A2 B2^T (bf16_gemm.hpp, EPI 2)
+// C[p, q] = gamma A B^T + gamma2 A2 B2^T (bf16_gemm.hpp, EPI 2); part blockIdx.y of
+// the contraction, each with a C of its own
 template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_two_products_kernel(
     const uint16_t* __restrict__ A, int64_t P, int64_t lda, const void* __restrict__ B, int64_t Q, int64_t Rp,
     float* __restrict__ C, const float* __restrict__ gamma, int bytes_a, int bytes_b, int tiles_p, int tiles_q,
     SecondProduct second) {
-  bf16_gemm_nt_body<BM, BN, WM, WN, 1, 2>(A, P, lda, B, Q, Rp, C, Q, gamma, nullptr, 0, bytes_a, bytes_b, tiles_p,
-                                          tiles_q, second);
+  const int stages = static_cast<int>(Rp / 64), part = blockIdx.y, parts = gridDim.y;
+  second.first = static_cast<int>(static_cast<int64_t>(part) * stages / parts);
+  second.count = static_cast<int>(static_cast<int64_t>(part + 1) * stages / parts) - second.first;
+  bf16_gemm_nt_body<BM, BN, WM, WN, 1, 2>(A, P, lda, B, Q, Rp, C + part * P * Q, Q, gamma, nullptr, 0, bytes_a, bytes_b,
+                                          tiles_p, tiles_q, second);
+}
+
+// dX = the sum of its parts, in order
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict__ parts, int nparts, int64_t n,
+                                                        float* __restrict__ dX) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    float v = parts[i];
+#pragma unroll 8
+    for (int s = 1; s < nparts; ++s) v += parts[s * n + i];
+    dX[i] = v;
+  }
 }
 
 }  // namespace
@@ -83,8 +99,8 @@ hipError_t launch_gated_backward(const void* dH, int dh_dtype, const void* G, co
 
 hipError_t launch_gated_input_backward(const uint16_t* dG, const uint16_t* dU, int64_t M, int64_t F, int64_t D,
                                        const uint32_t* packedT_gate, const float* gamma_gate,
-                                       const uint32_t* packedT_up, const float* gamma_up, float* dX, void* copies,
-                                       hipStream_t stream) {
+                                       const uint32_t* packedT_up, const float* gamma_up, float* dX, float* parts,
+                                       void* copies, hipStream_t stream) {
   const int64_t Fp = padded_k(F);
   int64_t lda = F;
   if (copies) {
@@ -99,17 +115,22 @@ hipError_t launch_gated_input_backward(const uint16_t* dG, const uint16_t* dU, i
     lda = Fp;
   }
   const int bytes_a = static_cast<int>(M * lda * 2), bytes_b = static_cast<int>(D * (Fp / 4));
-  const SecondProduct second = {dU, packedT_up, gamma_up};
-  // the largest tile that still makes a workgroup for most CUs
-  auto tiles = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((D + bn - 1) / bn); };
+  const SecondProduct second = {dU, packedT_up, gamma_up, 0, 0};
+  const GatedDxPlan plan = gated_dx_plan(M, F, D);
   auto go = [&](auto kernel, int bm, int bn, int threads) {
     const int tiles_p = static_cast<int>((M + bm - 1) / bm), tiles_q = static_cast<int>((D + bn - 1) / bn);
-    kernel<<<static_cast<unsigned>(tiles_p * tiles_q), threads, 0, stream>>>(
-        dG, M, lda, packedT_gate, D, Fp, dX, gamma_gate, bytes_a, bytes_b, tiles_p, tiles_q, second);
+    kernel<<<dim3(static_cast<unsigned>(tiles_p * tiles_q), plan.parts), threads, 0, stream>>>(
+        dG, M, lda, packedT_gate, D, Fp, plan.parts > 1 ? parts : dX, gamma_gate, bytes_a, bytes_b, tiles_p, tiles_q,
+        second);
   };
-  if (tiles(256, 128) >= 192) go(bf16_two_products_kernel<256, 128, 4, 2>, 256, 128, 512);
-  else if (tiles(128, 128) >= 128) go(bf16_two_products_kernel<128, 128, 2, 2>, 128, 128, 256);
+  if (plan.bm == 256) go(bf16_two_products_kernel<256, 128, 4, 2>, 256, 128, 512);
+  else if (plan.bm == 128) go(bf16_two_products_kernel<128, 128, 2, 2>, 128, 128, 256);
   else go(bf16_two_products_kernel<64, 64, 1, 2>, 64, 64, 128);
+  if (plan.parts > 1) {
+    const int64_t blocks = (M * D + 255) / 256;
+    sum_parts_kernel<<<static_cast<unsigned>(blocks < 65536 ? blocks : 65536), 256, 0, stream>>>(parts, plan.parts, M * D,
+                                                                                             dX);
+  }
   return hipGetLastError();
 }
 

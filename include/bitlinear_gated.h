@@ -120,16 +120,18 @@ int bitlinear_gated_backward(const void* dH, int dh_dtype, const void* G, const 
 /* ---- backward: the input's gradient ----------------------------------------- */
 /*
  * dX = gamma_gate (dG W_gate) + gamma_up (dU W_up), W the ternary codes: both
- * products in one launch, float32 accumulation, each scaled once and then
- * added (the activation clip never binds, as for bitlinear_backward).
+ * products in one launch, float32 accumulation, each scaled and then added; with
+ * few rows in parts of F, which a second launch adds in order (the activation
+ * clip never binds, as for bitlinear_backward).
  * dG, dU: device bfloat16 [M, F] (bit patterns).  packedT_gate, packedT_up:
  * [D, F] matrices as bitlinear_pack_transposed writes them.  dX: device float32
- * [M, D].  workspace: >= bitlinear_gated_input_backward_workspace_bytes(M, F)
- * where F % 8 != 0 or dG or dU is not 16-byte aligned (padded copies), 256-byte
- * aligned; else it may be NULL/0.  Requires M * padded_k(F) < 2^30.
+ * [M, D].  workspace: >= bitlinear_gated_input_backward_workspace_bytes(M, F, D,
+ * copies), 256-byte aligned, NULL/0 where that is 0.  copies: nonzero where F % 8 != 0
+ * or dG or dU is not 16-byte aligned (padded copies of both are made).  Requires
+ * M * padded_k(F) < 2^30.
  * Errors: BITLINEAR_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _ARG, _HIP.
  */
-size_t bitlinear_gated_input_backward_workspace_bytes(int64_t M, int64_t F);
+size_t bitlinear_gated_input_backward_workspace_bytes(int64_t M, int64_t F, int64_t D, int copies);
 
 int bitlinear_gated_input_backward(const uint16_t* dG, const uint16_t* dU, int64_t M, int64_t F, int64_t D,
                                    const uint32_t* packedT_gate, const float* gamma_gate,

@@ -51,7 +51,7 @@ hipError_t launch_gated_backward(const void*, int, const void*, const void*, int
   return record("gated_backward");
 }
 hipError_t launch_gated_input_backward(const uint16_t*, const uint16_t*, int64_t, int64_t, int64_t, const uint32_t*,
-                                       const float*, const uint32_t*, const float*, float*, void* copies, hipStream_t) {
+                                       const float*, const uint32_t*, const float*, float*, float*, void* copies, hipStream_t) {
   return record(copies ? "dx_copies" : "dx");
 }
 int64_t adapted_decode_piece(int64_t, int64_t, int64_t) { return g_piece; }
@@ -357,11 +357,14 @@ int main() {
   exact(l, bitlinear_adapters_backward_workspace_bytes(300, 100, 70, 4, 9),
         [=](const Low& b) { return b.back(300, 100, 70, 4, 9, dX, dd, du); });
   CHECK(launched(0, "shrink expand first join adapted_gemm shrink expand grad grad "));
-  const size_t need = bitlinear_gated_input_backward_workspace_bytes(33, 70);
+  const size_t need = bitlinear_gated_input_backward_workspace_bytes(33, 70, 8, 1);
   CHECK(dx(33, 70, 8, 0, at(8), need - 1) == BITLINEAR_ERR_WORKSPACE);
   CHECK(dx(33, 70, 8, 0, at(8), need) == BITLINEAR_OK && launched(0, "dx_copies "));
   CHECK(dx(33, 72, 8, 0, nullptr, 0) == BITLINEAR_OK && launched(0, "dx "));
   CHECK(dx(33, 72, 8, 1, nullptr, 0) == BITLINEAR_ERR_WORKSPACE && none());
+  const size_t sums = bitlinear_gated_input_backward_workspace_bytes(33, 1024, 8, 0);
+  CHECK(sums > 0 && dx(33, 1024, 8, 0, at(8), sums - 1) == BITLINEAR_ERR_WORKSPACE && none());
+  CHECK(dx(33, 1024, 8, 0, at(8), sums) == BITLINEAR_OK && launched(0, "dx "));
 
   // which launches: paths, sizes and what is asked for
   {
@@ -415,8 +418,10 @@ int main() {
   for (int64_t v : {int64_t(0), int64_t(-1), I64MAX, I64MIN, (int64_t(1) << 40) + 1}) {
     CHECK(bitlinear_gated_ffn_workspace_bytes(v, 8, 8) == 0 && bitlinear_gated_ffn_workspace_bytes(8, v, 8) == 0 &&
           bitlinear_gated_ffn_workspace_bytes(8, 8, v) == 0);
-    CHECK(bitlinear_gated_input_backward_workspace_bytes(v, 8) == 0 &&
-          bitlinear_gated_input_backward_workspace_bytes(8, v) == 0);
+    for (int copies : {0, 1})
+      CHECK(bitlinear_gated_input_backward_workspace_bytes(v, 8, 8, copies) == 0 &&
+            bitlinear_gated_input_backward_workspace_bytes(8, v, 8, copies) == 0 &&
+            bitlinear_gated_input_backward_workspace_bytes(8, 8, v, copies) == 0);
     CHECK(bitlinear_adapters_workspace_bytes(v, 8, 8, 8) == 0 && bitlinear_adapters_workspace_bytes(8, v, 8, 8) == 0 &&
           bitlinear_adapters_workspace_bytes(8, 8, v, 8) == 0 && bitlinear_adapters_workspace_bytes(8, 8, 8, v) == 0);
     CHECK(bitlinear_adapted_workspace_bytes(v, 8, 8, 8) == 0 && bitlinear_adapted_workspace_bytes(8, v, 8, 8) == 0 &&
@@ -429,7 +434,15 @@ int main() {
   }
   const int64_t huge = int64_t(1) << 40;
   CHECK(bitlinear_gated_ffn_workspace_bytes(huge, huge, huge) == 0);
-  CHECK(bitlinear_gated_input_backward_workspace_bytes(huge, huge) == 0);
+  CHECK(bitlinear_gated_input_backward_workspace_bytes(huge, huge, huge, 1) == 0);
+  for (int64_t M : {int64_t(1), int64_t(55), int64_t(64), int64_t(300), int64_t(5000)})
+    for (int64_t D : {int64_t(1), int64_t(64), int64_t(238), int64_t(4096), int64_t(70000)})
+      for (int64_t F : {int64_t(1), int64_t(64), int64_t(255), int64_t(256), int64_t(10688), K20}) {
+        const bitlinear::GatedDxPlan p = bitlinear::gated_dx_plan(M, F, D);
+        CHECK(p.parts >= 1 && p.parts <= 64 && (p.parts == 1 || int64_t(p.parts) * 256 <= bitlinear::padded_k(F)));
+        CHECK(bitlinear_gated_input_backward_workspace_bytes(M, F, D, 0) >=
+              (p.parts == 1 ? 0 : size_t(4) * p.parts * M * D));
+      }
   CHECK(bitlinear_adapted_workspace_bytes(huge, huge, 8, 256) == 0);
   CHECK(bitlinear_adapters_backward_workspace_bytes(huge, huge, huge, 65535, 256) > size_t(huge) * 256 * 8);
 

@@ -46,10 +46,12 @@ def test_exports_every_declared_function(lib):
 def test_sizes(lib):
     f, g = lib.bitlinear_gated_ffn_workspace_bytes, lib.bitlinear_gated_input_backward_workspace_bytes
     for bad in (0, -1, (1 << 40) + 1, (1 << 63) - 1, -(1 << 63)):
-        assert f(bad, 8, 8) == f(8, bad, 8) == f(8, 8, bad) == g(bad, 8) == g(8, bad) == 0
+        assert f(bad, 8, 8) == f(8, bad, 8) == f(8, 8, bad) == g(bad, 8, 8, 1) == g(8, bad, 8, 1) == g(8, 8, bad, 1) == g(8, 8, bad, 0) == 0
     assert f(8, 2048, 5632) == 8 * 5632 * 4 + lib.bitlinear_forward_workspace_bytes(8, 5632)
     assert f(8, 8192, 64) == 8 * 64 * 4 + lib.bitlinear_forward_workspace_bytes(8, 8192)
-    assert g(3, 65) == 2 * 768 and f(1 << 40, 1 << 40, 1 << 40) == 0
+    assert g(3, 65, 8, 1) == 2 * 768 and g(3, 65, 8, 0) == 0
+    assert g(55, 10688, 238, 0) == 34 * 55 * 238 * 4 + 240  # 34 parts; to a multiple of 256
+    assert g(2048, 11008, 4096, 0) == 0 and f(1 << 40, 1 << 40, 1 << 40) == 0
 
 
 FORWARD = ["X", "dt", "M", "D", "F", "pg", "gg", "pu", "gu", "act", "H", "hdt", "G", "U", "sdt", "path", "ws", "wsb", "s"]
@@ -100,7 +102,7 @@ def test_forward_refusals(lib, make):
     assert call(X=at(0) + 1) == call(X=at(0) + 2, dt=abi.F32) == abi.ERR_ALIGN
     assert call(path=3) == call(path=-1) == abi.ERR_ARG
     assert call(path=abi.PATH_DECODE) == abi.ERR_SHAPE                  # 40 tokens
-    need = lib.bitlinear_forward_workspace_bytes(40, 100)
+    need = lib.bitlinear_forward_workspace_bytes(40, 100, 50, 1)
     assert call(ws=None) == call(wsb=need - 1) == abi.ERR_WORKSPACE
     assert call(ws=at(8) + 128) == abi.ERR_ALIGN
     assert call(ws=at(5) + 256, wsb=need) == call(ws=at(0) - 256, wsb=need) == abi.ERR_ARG
@@ -142,7 +144,7 @@ def test_backward_refusals(lib):
     assert call(act=2) == abi.ERR_ARG
     assert call(dG=at(1)) == call(dU=at(0) + 1996) == call(dG=at(4) + 998) == call(dU=at(2)) == abi.ERR_ARG
     names = ["dG", "dU", "M", "F", "D", "pg", "gg", "pu", "gu", "dX", "ws", "wsb", "s"]
-    need = lib.bitlinear_gated_input_backward_workspace_bytes(40, 100)
+    need = lib.bitlinear_gated_input_backward_workspace_bytes(40, 100, 50, 1)
     call = caller(lib.bitlinear_gated_input_backward, names,
                   [at(0), at(1), 40, 100, 50, at(2), at(3), at(4), at(5), at(6), at(7), need, None])
     for nm in ("dG", "dU", "pg", "gg", "pu", "gu", "dX"):
@@ -154,6 +156,8 @@ def test_backward_refusals(lib):
     assert call(ws=None) == call(wsb=need - 1) == abi.ERR_WORKSPACE      # F % 8 != 0
     assert call(F=104, dU=at(1) + 8, ws=None) == abi.ERR_WORKSPACE       # rows that start off 16 bytes
     assert call(ws=at(7) + 64) == abi.ERR_ALIGN
+    parts = lib.bitlinear_gated_input_backward_workspace_bytes(40, 1024, 50, 0)
+    assert parts > 0 and call(F=1024, wsb=parts - 1) == call(F=1024, ws=None) == abi.ERR_WORKSPACE
     assert call(dX=at(0)) == call(dX=at(2)) == call(ws=at(6)) == call(dX=at(1) - 4) == abi.ERR_ARG
 
 

@@ -169,7 +169,8 @@ def test_activation_backward_special_values():
     assert np.isnan(sG[0, [0, 3, 7]]).all() and np.isnan(sU[0, [0, 2, 7]]).all() and sU[0, 1] == i
 
 
-@pytest.mark.parametrize("M,D,F", [(1, 1, 1), (3, 70, 33), (40, 200, 136), (257, 129, 200), (300, 300, 1000), (64, 4100, 64)])
+@pytest.mark.parametrize("M,D,F", [(1, 1, 1), (3, 70, 33), (40, 200, 136), (257, 129, 200), (300, 300, 1000), (64, 4100, 64), (5, 30, 2000),
+                                   (70, 65, 4099)])
 def test_products_backward(M, D, F):
     print(f"products M={M} D={D} F={F}", flush=True)
     P = Problem(M, D, F, dt="bf16", backward=True)
