@@ -1,8 +1,8 @@
 // Prefill through a projection and its adapters (include/bitlinear_adapters.h): the
 // INT8-MFMA GEMM with the adapters' second product in its epilogue
-// (prefill_gemm.hpp, EPI 4), for up to 16 ranks.  Y is written once; as a pass of
-// its own the second product reads and writes it again, 180 MB for 2048 tokens of
-// 11008 outputs.
+// (prefill_gemm.hpp, EPI 4 to 7), for up to 64 ranks.  Y is written once; as a pass
+// of its own the second product reads and writes it again, 180 MB for 2048 tokens
+// of 11008 outputs.
 #include <algorithm>
 
 #include "prefill_gemm.hpp"
@@ -35,9 +35,12 @@ hipError_t launch_tile(const int8_t* Xq, const float* ga, const int32_t* rs, int
     const int tiles_m = static_cast<int>((Mc + BM - 1) / BM), tiles_n = static_cast<int>((N + BN - 1) / BN);
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(int64_t(tiles_m) * tiles_n, kCUs));
     AdapterOut at = ao;
-    at.planes += r0 * 16;
+    at.planes += r0 * padded_r(ao.R);
     at.rows += r0;
-    auto kernel = w_dtype == kF32 ? adapted_gemm_kernel<BM, BN, WM, WN, 5> : adapted_gemm_kernel<BM, BN, WM, WN, 4>;
+    const bool f32 = w_dtype == kF32;
+    auto kernel = ao.R <= 16
+                      ? (f32 ? adapted_gemm_kernel<BM, BN, WM, WN, 5> : adapted_gemm_kernel<BM, BN, WM, WN, 4>)
+                      : (f32 ? adapted_gemm_kernel<BM, BN, WM, WN, 7> : adapted_gemm_kernel<BM, BN, WM, WN, 6>);
     kernel<<<blocks, 64 * WM * WN, 0, stream>>>(
         Xq + r0 * Kp, ga + r0, rs + r0, Mc, Kp, packed + n0 * (Kp / 16), N, ldy, gamma, Y + r0 * ldy + n0, tiles_m,
         tiles_n, static_cast<int>(Mc * Kp), static_cast<int>(N * (Kp / 4)), at);
@@ -53,7 +56,7 @@ hipError_t launch_adapted_gemm(const int8_t* Xq, const float* ga, const int32_t*
                                const uint32_t* packed, int64_t N, const float* gamma, float* Y, const uint16_t* planes,
                                const Adapters& ad, const void* up, hipStream_t stream) {
   const int64_t Kp = padded_k(K);
-  const AdapterOut ao = {planes, M * 16, ad.rows, static_cast<const char*>(up), N, ad.A, ad.R};
+  const AdapterOut ao = {planes, M * padded_r(ad.R), ad.rows, static_cast<const char*>(up), N, ad.A, ad.R};
   const int wt = ad.w_dtype;
   // Tiles of 256 tokens x 256 columns, 128 x 256 or 128 x 128 by weighed rounds, as
   // for the gated GEMM (gated.hip, where the weights and what they decide stand).

@@ -71,11 +71,11 @@ struct GatedOut {
   int act, h_dtype, gu_dtype;
 };
 
-// Adapters of up to 16 ranks added to Y (EPI 4: bfloat16 weights, 5: float32):
-// the scaled first product as operand planes, and the second one's weights.
-// Pointers are those of the launch's first token and column.
+// Adapters added to Y (EPI 4: up to 16 ranks, bfloat16 weights, 5: float32; 6 and
+// 7: more ranks): the scaled first product as operand planes, and the second one's
+// weights.  Pointers are those of the launch's first token and column.
 struct AdapterOut {
-  const uint16_t* planes;  // bf16 [3][tokens][16]
+  const uint16_t* planes;  // bf16 [3][tokens][R to a multiple of 16]
   int64_t plane_stride;    // values from plane to plane
   const int32_t* rows;
   const char* up;          // [A][R][ld]
@@ -375,8 +375,10 @@ __device__ __forceinline__ void prefill_gemm_body(
       // (8 loads a lane and block of 32, one rank each), three planes of T against one
       // or three of the weights (adapters.hip).  A block's product is formed apart and
       // added to the rows that are the adapter's.
-      static_assert(MI == 2, "64 rows of a wave");
-      constexpr int WT = EPI == 4 ? kBf16 : kF32;
+      static_assert(MI == 2 && NI % 2 == 0, "64 rows of a wave, weights in two sets of registers");
+      constexpr int WT = EPI % 2 == 0 ? kBf16 : kF32;
+      constexpr bool MANY = EPI >= 6;  // more than 16 ranks: 16 at a time
+      const int Rp = MANY ? (ao.R + 15) & ~15 : 16;
       const int my_id = row_adapter[wm * (BM / WM) + lane];
       uint64_t todo = __ballot(my_id >= 0);
       f32x16 y[MI][NI];
@@ -391,15 +393,16 @@ __device__ __forceinline__ void prefill_gemm_body(
           for (int ni = 0; ni < NI; ++ni) y[mi][ni][r] = __fmul_rn(static_cast<float>(c[mi][ni][r] - rs), scale);
         }
       bf16x8 tp[MI][3];
-      if (todo) {
+      auto load_t = [&](int r0) {
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
           const int64_t m = min(em0 + wm * (BM / WM) + mi * 32 + lr, M - 1);
 #pragma unroll
           for (int p = 0; p < 3; ++p)
-            tp[mi][p] = *reinterpret_cast<const bf16x8*>(ao.planes + p * ao.plane_stride + m * 16 + 8 * lh);
+            tp[mi][p] = *reinterpret_cast<const bf16x8*>(ao.planes + p * ao.plane_stride + m * Rp + r0 + 8 * lh);
         }
-      }
+      };
+      if (!MANY && todo) load_t(0);
       while (todo) {
         const int a = __builtin_amdgcn_readlane(my_id, __builtin_ctzll(todo));
         const uint64_t mine = __ballot(my_id == a);
@@ -412,49 +415,54 @@ __device__ __forceinline__ void prefill_gemm_body(
         // a block's weights are asked for while the block before is multiplied; more
         // in flight would not fit the registers
         uint32_t raw[2][8];
-        auto load_w = [&](int ni, uint32_t (&to)[8]) {
+        auto load_w = [&](int r0, int ni, uint32_t (&to)[8]) {
+          const uint32_t from = at + static_cast<uint32_t>(r0) * step;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t off = 8 * lh + i < ao.R ? at + i * step + 32u * ni * kBytes<WT> : kNowhere;
+            const uint32_t off = r0 + 8 * lh + i < ao.R ? from + i * step + 32u * ni * kBytes<WT> : kNowhere;
             if constexpr (WT == kF32) to[i] = __builtin_amdgcn_raw_buffer_load_b32(wres, off, 0, 0);
             else to[i] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(wres, off, 0, 0));
           }
         };
-        load_w(0, raw[0]);
+        load_w(0, 0, raw[0]);
+        for (int r0 = 0; r0 < (MANY ? ao.R : 1); r0 += 16) {
+          if constexpr (MANY) load_t(r0);
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-          if (ni + 1 < NI) load_w(ni + 1, raw[(ni + 1) & 1]);
-          __builtin_amdgcn_sched_barrier(0);
-          Some<WT, 8> w;
+          for (int ni = 0; ni < NI; ++ni) {
+            if (ni + 1 < NI) load_w(r0, ni + 1, raw[(ni + 1) & 1]);
+            else if (MANY && r0 + 16 < ao.R) load_w(r0 + 16, 0, raw[0]);
+            __builtin_amdgcn_sched_barrier(0);
+            Some<WT, 8> w;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if constexpr (WT == kF32) w.w[i] = raw[ni & 1][i];
-            else if (i % 2 == 0) w.w[i / 2] = lower(raw[ni & 1][i], raw[ni & 1][i + 1]);
-          }
-          bf16x8 wp[kPlanes<WT>];
-          row_planes<WT>(w, wp);
+            for (int i = 0; i < 8; ++i) {
+              if constexpr (WT == kF32) w.w[i] = raw[ni & 1][i];
+              else if (i % 2 == 0) w.w[i / 2] = lower(raw[ni & 1][i], raw[ni & 1][i + 1]);
+            }
+            bf16x8 wp[kPlanes<WT>];
+            row_planes<WT>(w, wp);
 #pragma unroll
-          for (int mi = 0; mi < MI; ++mi) {
-            const uint32_t own = static_cast<uint32_t>(mine >> (32 * mi));
-            if (own == 0u) continue;
-            f32x16 d = {};
+            for (int mi = 0; mi < MI; ++mi) {
+              const uint32_t own = static_cast<uint32_t>(mine >> (32 * mi));
+              if (own == 0u) continue;
+              f32x16 d = {};
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
+              for (int p = 0; p < 3; ++p)
 #pragma unroll
-              for (int q = 0; q < kPlanes<WT>; ++q)
-                if (p + q <= 2) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(tp[mi][p], wp[q], d, 0, 0, 0);
-            if (own == 0xffffffffu) {
+                for (int q = 0; q < kPlanes<WT>; ++q)
+                  if (p + q <= 2) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(tp[mi][p], wp[q], d, 0, 0, 0);
+              if (own == 0xffffffffu) {
 #pragma unroll
-              for (int r = 0; r < 16; ++r) y[mi][ni][r] = __fadd_rn(y[mi][ni][r], d[r]);
-            } else {
+                for (int r = 0; r < 16; ++r) y[mi][ni][r] = __fadd_rn(y[mi][ni][r], d[r]);
+              } else {
 #pragma unroll
-              for (int r = 0; r < 16; ++r) {
-                const float sum = __fadd_rn(y[mi][ni][r], d[r]);
-                y[mi][ni][r] = own >> (8 * (r >> 2) + 4 * lh + (r & 3)) & 1u ? sum : y[mi][ni][r];
+                for (int r = 0; r < 16; ++r) {
+                  const float sum = __fadd_rn(y[mi][ni][r], d[r]);
+                  y[mi][ni][r] = own >> (8 * (r >> 2) + 4 * lh + (r & 3)) & 1u ? sum : y[mi][ni][r];
+                }
               }
             }
+            __builtin_amdgcn_sched_barrier(0);
           }
-          __builtin_amdgcn_sched_barrier(0);
         }
       }
       request_next();

@@ -148,6 +148,26 @@ def test_beside_the_projection(M, K, N):
 
 
 @pytest.mark.parametrize("xt,wt", TYPES)
+@pytest.mark.parametrize("M,K,N,R,A,order", [(129, 72, 300, 16, 3, "mixed"), (200, 2050, 8, 5, 20, "requests"),
+                                             (1500, 72, 2900, 17, 4, "requests"), (1447, 9, 2905, 64, 3, "mixed"),
+                                             (2300, 130, 4500, 40, 5, "requests"), (1447, 40, 2905, 65, 3, "requests")])
+def test_in_the_projections_epilogue(M, K, N, R, A, order, xt, wt):
+    P = Problem(M, K, N, R, A, xt, wt, order)
+    packed, gamma = bl.quantize_weights(on_gpu(P.rng.standard_normal((N, K)) * 0.02))
+    base = bl.forward(P.x, packed, gamma, K)
+    y, t = bl.adapted_forward(P.x, packed, gamma, P.ads, P.ids, return_low=True)
+    P.check_forward(y, t, np_of(base))
+    # a request's infinities and NaN stay with it
+    bad = torch.from_numpy(P.rows == 1).to(DEV)
+    for v in (float("nan"), float("inf")):
+        x = P.x.clone()
+        down, up, scales = (w.clone() for w in P.ads)
+        x[bad], down[1], up[1], scales[1] = v, v, v, v
+        y2, t2 = bl.adapted_forward(x, packed, gamma, (down, up, scales), P.ids, return_low=True)
+        assert torch.equal(y2[~bad], y[~bad]) and torch.equal(t2[~bad], t[~bad]) and not torch.isfinite(y2[bad]).any()
+
+
+@pytest.mark.parametrize("xt,wt", TYPES)
 def test_requests_do_not_reach_each_other(xt, wt):
     M, K, N, R, A = 50, 70, 90, 12, 6
     P = Problem(M, K, N, R, A, xt, wt)
