@@ -16,7 +16,7 @@ namespace {
 
 // dYp[m, n] = dY[m, n] for n < N, 0 for N <= n < Np (bf16 bit patterns; Np a
 // multiple of 64): a thread to 8 columns, read at any address (2048x4097: value
-// by value 20 us, this 9).
+// by value 20 us, this 7.8).
 __global__ __launch_bounds__(256) void pad_rows_bf16_kernel(const uint16_t* __restrict__ src, int64_t M, int64_t N,
                                                             uint16_t* __restrict__ dst, int64_t Np) {
   const int64_t per_row = Np >> 3, total = M * per_row;

