@@ -88,8 +88,8 @@ TRAFFIC = {
     "decode_ffn_up_m8_k2048_n5632/radix3": {"sources_sha": "30f652cd416104ec", "fetch_bytes": 1091142656, "write_bytes": 82722816},
     "decode_m1_k2048_n2048/lut": {"sources_sha": "6d4398590ebb1f5f", "fetch_bytes": 1076063744, "write_bytes": 8388608},
     "decode_ffn_up_m8_k2048_n5632/lut": {"sources_sha": "6d4398590ebb1f5f", "fetch_bytes": 1082523392, "write_bytes": 67223552},
-    "prefill_ffn_m2048_k4096_n11008": {"sources_sha": "8266ce6d2f033581", "fetch_bytes": 117062656, "write_bytes": 90282880},
-    "prefill_ffn_m8192_k8192_n28672": {"sources_sha": "8266ce6d2f033581", "fetch_bytes": 2116055040, "write_bytes": 939632192},
+    "prefill_ffn_m2048_k4096_n11008": {"sources_sha": "f196e66478b99f95", "fetch_bytes": 117062656, "write_bytes": 90279168},
+    "prefill_ffn_m8192_k8192_n28672": {"sources_sha": "f196e66478b99f95", "fetch_bytes": 2116055040, "write_bytes": 939638656},
 }
 
 KERNEL_SOURCES = {

@@ -894,7 +894,7 @@ def gated_ffn_forward(X, gate, up, down, act: str = "relu2", path: str = "auto",
     dp, dg, Do = _ternary(B, down, F, None, device.index, "down")
     Y = _output(B, out, M, Do, B.f32, device)
     H = B.empty(M, F, dtype=B.f32, device=device) if return_hidden else None
-    need = 0 if workspace is not None else B.gated_ffn_workspace_bytes(M, D, F)
+    need = 0 if workspace is not None else B.gated_ffn_workspace_bytes(M, D, F, Do)
     wsp, ws_bytes, keep = _workspace(B, workspace, need, device)
     B.launch(B.gated_ffn_forward, device, X.data_ptr(), dt, M, D, F, Do, gp, gg, up_, ug, a, dp, dg, Y.data_ptr(),
              H.data_ptr() if return_hidden else 0, p, wsp, ws_bytes)

@@ -89,7 +89,7 @@ GATED_SIGNATURES = {
                                        _p, _sz, _p]),
     "bitlinear_gated_forward_quantized": (_int, [_p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _int, _p, _int, _p, _p,
                                                  _int, _p]),
-    "bitlinear_gated_ffn_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "bitlinear_gated_ffn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "bitlinear_gated_ffn_forward": (_int, [_p, _int, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _int, _p, _p, _p, _p,
                                            _int, _p, _sz, _p]),
     "bitlinear_gated_backward": (_int, [_p, _int, _p, _p, _int, _i64, _i64, _int, _p, _p, _int, _p]),

@@ -5,6 +5,7 @@
 #include "../../include/bitlinear_adapters.h"
 #include "abi_common.hpp"
 #include "adapter_ops.hpp"
+#include "prefill_parts.hpp"
 
 using namespace bitlinear;
 
@@ -72,8 +73,8 @@ int bitlinear_adapters_forward(const void* X, int x_dtype, int64_t M, int64_t K,
 
 size_t bitlinear_adapted_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R) {
   if (!size_args_ok(N)) return 0;
-  const size_t low = adapters_ws_bytes(M, K, R);
-  return size_add(low, prefill_ws_bytes(M, K));
+  const size_t all = size_add(adapters_ws_bytes(M, K, R), prefill_ws_bytes(M, K)), sums = prefill_parts_bytes(M, N, K);
+  return sums ? size_add(all, sums) : all;
 }
 
 int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, const uint32_t* packed, int64_t N,
@@ -87,7 +88,8 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
   st = check_forward_args(X, x_dtype, M, K, packed, N, gamma, Y, nullptr, path, &decode);
   if (st) return st;
   if (!aligned(T, 4)) return BITLINEAR_ERR_ALIGN;
-  const size_t low = adapters_ws_bytes(M, K, R), need = low + prefill_ws_bytes(M, K);
+  const size_t low = adapters_ws_bytes(M, K, R), codes = prefill_ws_bytes(M, K), sums = prefill_parts_bytes(M, N, K);
+  const size_t need = low + codes + sums;
   if (!workspace || workspace_bytes < need) return BITLINEAR_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return BITLINEAR_ERR_ALIGN;
   const Range out[] = {floats(Y, M * N), floats(T, M * R), {workspace, need}};
@@ -111,11 +113,18 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
     float* parts = static_cast<float*>(workspace);
     uint16_t* planes = planes_of(workspace, M, K, R);
     e = launch_adapted_first(X, x_dtype, M, K, ad, down, parts, c.xq, c.ga, c.rs, s);
-    if (adapted_gemm_takes(M, N, R)) {
+    // the second product in the GEMM's epilogue, unless parts of K save more than its
+    // own pass over Y costs (128x4096x4096, 16 ranks: 32 us and 29; 256x4096x4096 33
+    // and 36; 1024x8192x1024 58 and 45)
+    if (adapted_gemm_takes(M, N, R) && prefill_parts(M, N, K).saved <= 4000 + M * N / 300) {
       if (e == hipSuccess) e = launch_join(parts, M, K, ad, T, planes, s);
       if (e == hipSuccess) e = launch_adapted_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, planes, ad, up, s);
     } else {
-      if (e == hipSuccess) e = launch_prefill_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, nullptr, s);
+      if (e == hipSuccess && sums)
+        e = launch_prefill_parts(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y,
+                                 reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + low + codes), s);
+      else if (e == hipSuccess)
+        e = launch_prefill_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, nullptr, s);
       if (e == hipSuccess) e = launch_expand(parts, planes, M, K, N, ad, up, Y, true, T, s);
     }
     return hip_status(e);

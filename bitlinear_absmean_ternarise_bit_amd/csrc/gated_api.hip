@@ -5,6 +5,7 @@
 #include "../../include/bitlinear_gated.h"
 #include "abi_common.hpp"
 #include "gated_ops.hpp"
+#include "prefill_parts.hpp"
 
 using namespace bitlinear;
 
@@ -88,11 +89,13 @@ int bitlinear_gated_forward_quantized(const int8_t* Xq, const float* gamma_a, co
   return hip_status(launch_gated_gemm(Xq, gamma_a, rowsum, M, D, F, w, o, s));
 }
 
-size_t bitlinear_gated_ffn_workspace_bytes(int64_t M, int64_t D, int64_t F) {
-  if (!size_args_ok(M) || !size_args_ok(D) || !size_args_ok(F)) return 0;
+size_t bitlinear_gated_ffn_workspace_bytes(int64_t M, int64_t D, int64_t F, int64_t D_out) {
+  if (!size_args_ok(M) || !size_args_ok(D) || !size_args_ok(F) || !size_args_ok(D_out)) return 0;
   const size_t one = prefill_ws_bytes(M, D), two = prefill_ws_bytes(M, F);
   if (one == 0 || two == 0) return 0;
-  return size_add(align256(size_mul(size_mul(size_t(M), size_t(F)), 4)), one > two ? one : two);
+  const size_t all = size_add(align256(size_mul(size_mul(size_t(M), size_t(F)), 4)), one > two ? one : two);
+  const size_t parts = prefill_parts_bytes(M, D_out, F);
+  return parts ? size_add(all, parts) : all;
 }
 
 int bitlinear_gated_ffn_forward(const void* X, int x_dtype, int64_t M, int64_t D, int64_t F, int64_t D_out,
@@ -117,7 +120,8 @@ int bitlinear_gated_ffn_forward(const void* X, int x_dtype, int64_t M, int64_t D
   const bool decode = fits && path != BITLINEAR_PATH_PREFILL;
   const size_t hidden_bytes = hidden ? 0 : align256(static_cast<size_t>(M) * static_cast<size_t>(F) * 4);
   const size_t first = decode ? 0 : prefill_ws_bytes(M, D), second = prefill_ws_bytes(M, F);
-  const size_t need = hidden_bytes + (first > second ? first : second);
+  const size_t codes = first > second ? first : second, parts = decode ? 0 : prefill_parts_bytes(M, D_out, F);
+  const size_t need = hidden_bytes + codes + parts;
   if (!workspace || workspace_bytes < need) return BITLINEAR_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return BITLINEAR_ERR_ALIGN;
   const Range out[] = {floats(Y, M * D_out), floats(hidden, M * F), {workspace, need}};
@@ -142,6 +146,9 @@ int bitlinear_gated_ffn_forward(const void* X, int x_dtype, int64_t M, int64_t D
   if (e != hipSuccess) return BITLINEAR_ERR_HIP;
   if (decode)
     return hip_status(launch_decode_codes(c.xq, c.ga, c.rs, M, F, packed_down, D_out, gamma_down, Y, 1, s));
+  if (parts)
+    return hip_status(launch_prefill_parts(c.xq, c.ga, c.rs, M, F, packed_down, D_out, gamma_down, Y,
+                                           reinterpret_cast<int32_t*>(ws + hidden_bytes + codes), s));
   return hip_status(launch_prefill_gemm(c.xq, c.ga, c.rs, M, F, packed_down, D_out, gamma_down, Y, nullptr, s));
 }
 

@@ -84,8 +84,9 @@ struct AdapterOut {
 };
 
 // EPI: 0 = Y, 1 = Y and the INT32 accumulators, 2 = ReLU^2 of Y (the hidden
-// activation of a BitNet FFN block), 3 = a gated hidden layer, 4 = Y and the
-// adapters' part.
+// activation of a BitNet FFN block), 3 = a gated hidden layer, 4 to 7 = Y and the
+// adapters' part, 8 = the INT32 sums of the stages first .. first + count - 1 alone
+// (without the tokens' code sums).
 // EPI 3: a tile is BM tokens x BN / 2 columns of both projections.  Of a wave's
 // NI blocks of 32 packed rows the first half are gate rows and the second half
 // the up rows of the same columns, so a lane holds both accumulators of every
@@ -97,7 +98,8 @@ __device__ __forceinline__ void prefill_gemm_body(
     const int32_t* __restrict__ rowsum, int64_t M, int64_t Kp, const uint32_t* __restrict__ packed,
     int64_t N, int64_t ldy, const float* __restrict__ gamma, float* __restrict__ Y,
     int32_t* __restrict__ acc,
-    int tiles_m, int tiles_n, int bytes_a, int bytes_b, const GatedOut& go, const AdapterOut& ao) {
+    int tiles_m, int tiles_n, int bytes_a, int bytes_b, const GatedOut& go, const AdapterOut& ao,
+    int first = 0, int count = 0) {
   constexpr int A_BYTES = BM * 128;
   constexpr int B_BYTES = BN * 32;
   constexpr int STAGE = A_BYTES + B_BYTES;
@@ -117,7 +119,7 @@ __device__ __forceinline__ void prefill_gemm_body(
   constexpr bool GATED = EPI == 3;
   constexpr int OUT_BN = GATED ? BN / 2 : BN;  // output columns of a tile
   __shared__ float row_scale_up[GATED ? BM : 1];
-  constexpr bool ADAPTED = EPI >= 4;
+  constexpr bool ADAPTED = EPI >= 4 && EPI < 8, PART = EPI == 8;
   __shared__ int row_adapter[ADAPTED ? BM : 1];
   static_assert(!GATED || NI % 2 == 0, "gate and up blocks of a wave");
 
@@ -212,6 +214,7 @@ __device__ __forceinline__ void prefill_gemm_body(
   v4u ra[2][A_LOADS], rb[2][B_LOADS];
   auto gload = [&](int it, auto set_tag) {
     constexpr int S = decltype(set_tag)::value;
+    if constexpr (PART) it += first;
     const uint32_t k0 = static_cast<uint32_t>(it) * BK;
     const uint32_t a_adj = (k0 + 16u * a_c >= kp32) ? 64u : 0u;
     // unit 2 it + b_c of the row; past Kp (final half stage) the unit before it
@@ -289,8 +292,8 @@ __device__ __forceinline__ void prefill_gemm_body(
     }
   };
 
-  const int nfull = static_cast<int>(Kp / BK);
-  const int niter = static_cast<int>((Kp + BK - 1) / BK);
+  const int nfull = PART ? min(static_cast<int>(Kp / BK) - first, count) : static_cast<int>(Kp / BK);
+  const int niter = PART ? count : static_cast<int>((Kp + BK - 1) / BK);
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
 
@@ -508,6 +511,10 @@ __device__ __forceinline__ void prefill_gemm_body(
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) {
           const int64_t n = en0 + lcol + ni * 32;
+          if constexpr (PART) {
+            if (n < N) acc[m * ldy + n] = c[mi][ni][r];
+            continue;
+          }
           if (n < N) {
             const int v = c[mi][ni][r] - rs;
             if constexpr (EPI == 1) acc[m * ldy + n] = v;

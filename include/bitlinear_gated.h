@@ -90,12 +90,12 @@ int bitlinear_gated_forward_quantized(const int8_t* Xq, const float* gamma_a, co
 /*
  * Y = BitLinear_down(act(G) * U).  packed_down: [D_out, F] ternary; Y: device
  * float32 [M, D_out]; hidden: NULL, or device float32 [M, F], 16-byte aligned,
- * receiving H.  workspace: >= bitlinear_gated_ffn_workspace_bytes(M, D, F),
- * 256-byte aligned (the hidden layer when `hidden` is NULL, and activation
- * codes).  Three launches on the decode path (both its products fit it), four
+ * receiving H.  workspace: >= bitlinear_gated_ffn_workspace_bytes(M, D, F, D_out),
+ * 256-byte aligned (the hidden layer when `hidden` is NULL, activation
+ * codes, and parts of the down product where its tiles are few).  Three launches on the decode path (both its products fit it), four
  * or more on the prefill path.  Errors as above.
  */
-size_t bitlinear_gated_ffn_workspace_bytes(int64_t M, int64_t D, int64_t F);
+size_t bitlinear_gated_ffn_workspace_bytes(int64_t M, int64_t D, int64_t F, int64_t D_out);
 
 int bitlinear_gated_ffn_forward(const void* X, int x_dtype, int64_t M, int64_t D, int64_t F, int64_t D_out,
                                 const uint32_t* packed_gate, const float* gamma_gate, const uint32_t* packed_up,

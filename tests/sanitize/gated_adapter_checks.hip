@@ -11,6 +11,7 @@
 
 #include "../../bitlinear_absmean_ternarise_bit_amd/csrc/adapter_ops.hpp"
 #include "../../bitlinear_absmean_ternarise_bit_amd/csrc/gated_ops.hpp"
+#include "../../bitlinear_absmean_ternarise_bit_amd/csrc/prefill_parts.hpp"
 #include "../../include/bitlinear_adapters.h"
 #include "../../include/bitlinear_gated.h"
 #include "stub.h"
@@ -45,6 +46,10 @@ hipError_t launch_gated_decode(const void*, int, const int8_t*, const float*, co
 hipError_t launch_gated_gemm(const int8_t*, const float*, const int32_t*, int64_t, int64_t, int64_t, const GatedWeights&,
                              const GatedOutputs&, hipStream_t) {
   return record("gated_gemm");
+}
+hipError_t launch_prefill_parts(const int8_t*, const float*, const int32_t*, int64_t, int64_t, const uint32_t*, int64_t,
+                                const float*, float*, int32_t*, hipStream_t) {
+  return record("parts");
 }
 hipError_t launch_gated_backward(const void*, int, const void*, const void*, int, int64_t, int64_t, int, void*, void*,
                                  int, hipStream_t) {
@@ -350,7 +355,7 @@ int main() {
   exact(g, bitlinear_forward_workspace_bytes(20, 100), [](const Gated& b) { return b.run(20, 100, 8); });
   CHECK(launched(1, "gated_gemm "));
   for (int64_t F : {8, 900})  // the hidden layer's codes, or the input's
-    exact(g, bitlinear_gated_ffn_workspace_bytes(20, 100, F), [F](const Gated& b) { return b.block(20, 100, F, 8); });
+    exact(g, bitlinear_gated_ffn_workspace_bytes(20, 100, F, 8), [F](const Gated& b) { return b.block(20, 100, F, 8); });
   CHECK(launched(6, "gated_gemm gated_gemm "));
   exact(l, bitlinear_adapters_workspace_bytes(300, 100, 8, 9), [](const Low& b) { return b.run(300, 100, 8, 4, 9); });
   exact(l, bitlinear_adapted_workspace_bytes(300, 100, 8, 9), [](const Low& b) { return b.whole(300, 100, 8, 4, 9); });
@@ -365,6 +370,19 @@ int main() {
   const size_t sums = bitlinear_gated_input_backward_workspace_bytes(33, 1024, 8, 0);
   CHECK(sums > 0 && dx(33, 1024, 8, 0, at(8), sums - 1) == BITLINEAR_ERR_WORKSPACE && none());
   CHECK(dx(33, 1024, 8, 0, at(8), sums) == BITLINEAR_OK && launched(0, "dx "));
+
+  // the product of few tiles in parts of K
+  exact(g, bitlinear_gated_ffn_workspace_bytes(64, 100, 11008, 8), [](const Gated& b) { return b.block(64, 100, 11008, 8); });
+  CHECK(launched(2, "gated_gemm parts "));
+  exact(l, bitlinear_adapted_workspace_bytes(64, 11008, 8, 9), [](const Low& b) { return b.whole(64, 11008, 8, 4, 9); });
+  CHECK(launched(0, "first parts expand "));
+  for (int64_t M : {int64_t(1), int64_t(16), int64_t(17), int64_t(64), int64_t(777), int64_t(100000), M31, I64MAX / 2})
+    for (int64_t N : {int64_t(1), int64_t(128), int64_t(4096), int64_t(70000), M31, I64MAX / 2})
+      for (int64_t K : {int64_t(1), int64_t(128), int64_t(255), int64_t(4096), int64_t(11008), K20, I64MAX / 2}) {
+        const int p = bitlinear::prefill_parts(M, N, K).parts;
+        CHECK(p >= 1 && p <= 16 && (p == 1 || (M > 16 && 2 * p <= (K + 127) / 128)));
+        CHECK(p == 1 || bitlinear::prefill_parts_bytes(M, N, K) >= size_t(4) * p * M * N);
+      }
 
   // which launches: paths, sizes and what is asked for
   {
@@ -418,8 +436,8 @@ int main() {
 
   // size queries saturate to 0
   for (int64_t v : {int64_t(0), int64_t(-1), I64MAX, I64MIN, (int64_t(1) << 40) + 1}) {
-    CHECK(bitlinear_gated_ffn_workspace_bytes(v, 8, 8) == 0 && bitlinear_gated_ffn_workspace_bytes(8, v, 8) == 0 &&
-          bitlinear_gated_ffn_workspace_bytes(8, 8, v) == 0);
+    CHECK(bitlinear_gated_ffn_workspace_bytes(v, 8, 8, 8) == 0 && bitlinear_gated_ffn_workspace_bytes(8, v, 8, 8) == 0 &&
+          bitlinear_gated_ffn_workspace_bytes(8, 8, v, 8) == 0 && bitlinear_gated_ffn_workspace_bytes(8, 8, 8, v) == 0);
     for (int copies : {0, 1})
       CHECK(bitlinear_gated_input_backward_workspace_bytes(v, 8, 8, copies) == 0 &&
             bitlinear_gated_input_backward_workspace_bytes(8, v, 8, copies) == 0 &&
@@ -435,7 +453,7 @@ int main() {
           bitlinear_adapters_backward_workspace_bytes(8, 8, 8, 4, v) == 0);
   }
   const int64_t huge = int64_t(1) << 40;
-  CHECK(bitlinear_gated_ffn_workspace_bytes(huge, huge, huge) == 0);
+  CHECK(bitlinear_gated_ffn_workspace_bytes(huge, huge, huge, huge) == 0);
   CHECK(bitlinear_gated_input_backward_workspace_bytes(huge, huge, huge, 1) == 0);
   for (int64_t M : {int64_t(1), int64_t(55), int64_t(64), int64_t(300), int64_t(5000)})
     for (int64_t D : {int64_t(1), int64_t(64), int64_t(238), int64_t(4096), int64_t(70000)})

@@ -46,12 +46,15 @@ def test_exports_every_declared_function(lib):
 def test_sizes(lib):
     f, g = lib.bitlinear_gated_ffn_workspace_bytes, lib.bitlinear_gated_input_backward_workspace_bytes
     for bad in (0, -1, (1 << 40) + 1, (1 << 63) - 1, -(1 << 63)):
-        assert f(bad, 8, 8) == f(8, bad, 8) == f(8, 8, bad) == g(bad, 8, 8, 1) == g(8, bad, 8, 1) == g(8, 8, bad, 1) == g(8, 8, bad, 0) == 0
-    assert f(8, 2048, 5632) == 8 * 5632 * 4 + lib.bitlinear_forward_workspace_bytes(8, 5632)
-    assert f(8, 8192, 64) == 8 * 64 * 4 + lib.bitlinear_forward_workspace_bytes(8, 8192)
+        assert f(bad, 8, 8, 8) == f(8, bad, 8, 8) == f(8, 8, bad, 8) == f(8, 8, 8, bad) == \
+            g(bad, 8, 8, 1) == g(8, bad, 8, 1) == g(8, 8, bad, 1) == g(8, 8, bad, 0) == 0
+    assert f(8, 2048, 5632, 2048) == 8 * 5632 * 4 + lib.bitlinear_forward_workspace_bytes(8, 5632)
+    assert f(8, 8192, 64, 8192) == 8 * 64 * 4 + lib.bitlinear_forward_workspace_bytes(8, 8192)
     assert g(3, 65, 8, 1) == 2 * 768 and g(3, 65, 8, 0) == 0
     assert g(55, 10688, 238, 0) == 34 * 55 * 238 * 4 + 240  # 34 parts; to a multiple of 256
-    assert g(2048, 11008, 4096, 0) == 0 and f(1 << 40, 1 << 40, 1 << 40) == 0
+    assert g(2048, 11008, 4096, 0) == 0 and f(1 << 40, 1 << 40, 1 << 40, 1 << 40) == 0
+    # the down product in 15 parts of INT32 sums
+    assert f(64, 64, 11008, 128) == 64 * 11008 * 4 + lib.bitlinear_forward_workspace_bytes(64, 11008) + 15 * 64 * 128 * 4
 
 
 FORWARD = ["X", "dt", "M", "D", "F", "pg", "gg", "pu", "gu", "act", "H", "hdt", "G", "U", "sdt", "path", "ws", "wsb", "s"]
@@ -110,7 +113,7 @@ def test_forward_refusals(lib, make):
 
 def test_block_refusals(lib):
     names = ["X", "dt", "M", "D", "F", "Do", "pg", "gg", "pu", "gu", "act", "pd", "gd", "Y", "hid", "path", "ws", "wsb", "s"]
-    need = lib.bitlinear_gated_ffn_workspace_bytes(40, 100, 50)
+    need = lib.bitlinear_gated_ffn_workspace_bytes(40, 100, 50, 30)
     call = caller(lib.bitlinear_gated_ffn_forward, names,
                   [at(0), abi.F32, 40, 100, 50, 30, at(1), at(2), at(3), at(4), 0, at(5), at(6), at(7), None, 0, at(8),
                    need, None])

@@ -133,7 +133,7 @@ def test_nothing_is_rounded_to_fewer_bits(xt, wt):
 
 
 @pytest.mark.parametrize("M,K,N", [(1, 256, 192), (16, 300, 70), (40, 128, 300), (300, 512, 256), (1, 2050, 33),
-                                   (16, 4096, 130), (11, 12000, 64), (16, 16400, 50), (16, 40, 20000), (5, 7, 40)])
+                                   (40, 4090, 300), (150, 3001, 130), (16, 4096, 130), (11, 12000, 64), (16, 16400, 50), (16, 40, 20000), (5, 7, 40)])
 def test_beside_the_projection(M, K, N):
     P = Problem(M, K, N, 16, 5, "bf16", "bf16", "requests")
     packed, gamma = bl.quantize_weights(on_gpu(P.rng.standard_normal((N, K)) * 0.02))

@@ -110,7 +110,9 @@ def test_tiles_of_every_kind():
 
 
 @pytest.mark.parametrize("M,D,F,Do,dt", [(1, 64, 48, 64, "f32"), (8, 300, 129, 70, "bf16"), (16, 500, 333, 40, "f32"),
-                                         (33, 257, 190, 257, "bf16"), (300, 130, 450, 64, "f32"), (4, 16200, 20, 30, "bf16")])
+                                         (33, 257, 190, 257, "bf16"), (300, 130, 450, 64, "f32"), (4, 16200, 20, 30, "bf16"),
+                                         (17, 64, 2000, 130, "f32"), (64, 100, 4095, 40, "bf16"),
+                                         (200, 70, 1400, 300, "f32")])
 def test_block(M, D, F, Do, dt):
     P = Problem(M, D, F, dt=dt)
     down = Matrix(P.rng, Do, F)
