@@ -114,8 +114,8 @@ int bitlinear_adapted_forward(const void* X, int x_dtype, int64_t M, int64_t K, 
     uint16_t* planes = planes_of(workspace, M, K, R);
     e = launch_adapted_first(X, x_dtype, M, K, ad, down, parts, c.xq, c.ga, c.rs, s);
     // the second product in the GEMM's epilogue, unless parts of K save more than its
-    // own pass over Y costs (128x4096x4096, 16 ranks: 32 us and 29; 256x4096x4096 33
-    // and 36; 1024x8192x1024 58 and 45)
+    // own pass over Y costs (16 ranks: 256x4096x4096 33 us and 36, 1024x8192x1024 58
+    // and 45)
     if (adapted_gemm_takes(M, N, R) && prefill_parts(M, N, K).saved <= 4000 + M * N / 300) {
       if (e == hipSuccess) e = launch_join(parts, M, K, ad, T, planes, s);
       if (e == hipSuccess) e = launch_adapted_gemm(c.xq, c.ga, c.rs, M, K, packed, N, gamma, Y, planes, ad, up, s);

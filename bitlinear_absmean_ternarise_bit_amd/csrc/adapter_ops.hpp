@@ -121,13 +121,14 @@ hipError_t launch_adapted_first(const void* X, int x_dtype, int64_t M, int64_t K
                                 float* parts, int8_t* Xq, float* ga, int32_t* rs, hipStream_t stream);
 // The prefill GEMM with the second product in its epilogue: where its 32-bit offsets
 // hold and the tokens are so many that those of a tile's wave, 64, are likely of few
-// adapters, which it takes one after another (4096x4096, 16 ranks: 128 tokens of 4
-// requests 32 us, as a pass of its own 34; 64 of 16 requests 41 and 34).  More ranks
-// take longer there; what is saved is the pass over Y, so that has to be large
-// (64 ranks: 2048x4096x4096 67 and 79, 512x4096x4096 44 and 45, 6852x487x128 36 and
-// 33; more than 64 ranks were not measured); planes: launch_join's.
+// adapters, which it takes one after another (16 ranks: 256x4096x4096 of 1 request 33
+// us, as a pass of its own 38; a request for each of its tokens 89 and 75, for each of
+// 200x2048x5632 65 and 38).  More ranks take longer there; what is saved is the pass
+// over Y, so that has to be large (64 ranks: 2048x4096x4096 67 and 79, 512x4096x4096 44
+// and 45, 6852x487x128 36 and 33; more than 64 ranks were not measured); planes:
+// launch_join's.
 inline bool adapted_gemm_takes(int64_t M, int64_t N, int64_t R) {
-  return M >= 128 && N >= 8 && N <= (int64_t(1) << 24) && (R <= 16 || (R <= 64 && M * N >= (int64_t(1) << 22)));
+  return M >= 256 && N >= 8 && N <= (int64_t(1) << 24) && (R <= 16 || (R <= 64 && M * N >= (int64_t(1) << 22)));
 }
 hipError_t launch_adapted_gemm(const int8_t* Xq, const float* ga, const int32_t* rs, int64_t M, int64_t K,
                                const uint32_t* packed, int64_t N, const float* gamma, float* Y, const uint16_t* planes,

@@ -79,7 +79,9 @@ int bitlinear_adapters_forward(const void* X, int x_dtype, int64_t M, int64_t K,
  * The projection and the adapters: Y = bitlinear_forward(X) and then the above
  * on it.  packed, gamma, path: as for bitlinear_forward_ex.  workspace: >=
  * bitlinear_adapted_workspace_bytes(M, K, N, R), 256-byte aligned (activation
- * codes among it).  Up to 16 tokens take two launches.  The adapters' sums may be
+ * codes among it, and parts of the product where its tiles are few).  Up to 16 tokens
+ * take two launches, except of weights with so many rows that the decode path streams
+ * them (then three), more take three to five.  The adapters' sums may be
  * formed in another order than by the two calls one after the other; both are
  * within the accuracy above.
  */

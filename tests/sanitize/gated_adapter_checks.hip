@@ -402,8 +402,8 @@ int main() {
     g_piece = 4;
     CHECK(c.whole(4, 100, 8, 4, 9) == BITLINEAR_OK && launched(0, "adapted_decode "));
     c.path = BITLINEAR_PATH_PREFILL;
-    CHECK(c.whole(128, 100, 8, 4, 9) == BITLINEAR_OK && launched(0, "first join adapted_gemm "));
-    CHECK(c.whole(127, 100, 8, 4, 9) == BITLINEAR_OK && launched(1, "first expand "));
+    CHECK(c.whole(256, 100, 8, 4, 9) == BITLINEAR_OK && launched(0, "first join adapted_gemm "));
+    CHECK(c.whole(255, 100, 8, 4, 9) == BITLINEAR_OK && launched(1, "first expand "));
     CHECK(c.whole(2048, 100, 2048, 4, 64) == BITLINEAR_OK && launched(0, "first join adapted_gemm "));
     CHECK(c.whole(2048, 100, 2048, 4, 65) == BITLINEAR_OK && launched(1, "first expand "));
     CHECK(c.whole(128, 100, 8, 4, 17) == BITLINEAR_OK && launched(1, "first expand "));

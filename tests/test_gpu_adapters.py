@@ -149,6 +149,7 @@ def test_beside_the_projection(M, K, N):
 
 @pytest.mark.parametrize("xt,wt", TYPES)
 @pytest.mark.parametrize("M,K,N,R,A,order", [(129, 72, 300, 16, 3, "mixed"), (200, 2050, 8, 5, 20, "requests"),
+                                             (257, 72, 300, 16, 3, "mixed"), (300, 250, 8, 5, 20, "requests"),
                                              (1500, 72, 2900, 17, 4, "requests"), (1447, 9, 2905, 64, 3, "mixed"),
                                              (2300, 130, 4500, 40, 5, "requests"), (1447, 40, 2905, 65, 3, "requests")])
 def test_in_the_projections_epilogue(M, K, N, R, A, order, xt, wt):
