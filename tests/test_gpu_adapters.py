@@ -151,7 +151,9 @@ def test_beside_the_projection(M, K, N):
 @pytest.mark.parametrize("M,K,N,R,A,order", [(129, 72, 300, 16, 3, "mixed"), (200, 2050, 8, 5, 20, "requests"),
                                              (257, 72, 300, 16, 3, "mixed"), (300, 250, 8, 5, 20, "requests"),
                                              (1500, 72, 2900, 17, 4, "requests"), (1447, 9, 2905, 64, 3, "mixed"),
-                                             (2300, 130, 4500, 40, 5, "requests"), (1447, 40, 2905, 65, 3, "requests")])
+                                             (2300, 130, 4500, 40, 5, "requests"), (1447, 40, 2905, 65, 3, "requests"),
+                                             (2048, 40, 2048, 33, 3, "requests"), (2048, 24, 9000, 16, 3, "requests"),
+                                             (2048, 24, 9000, 20, 2, "requests")])
 def test_in_the_projections_epilogue(M, K, N, R, A, order, xt, wt):
     P = Problem(M, K, N, R, A, xt, wt, order)
     packed, gamma = bl.quantize_weights(on_gpu(P.rng.standard_normal((N, K)) * 0.02))
@@ -260,6 +262,27 @@ def test_streams_and_graph():
         assert same(out, eager)
 
 
+@pytest.mark.parametrize("M,K,N,R", [(64, 4090, 130, 16), (300, 300, 260, 16), (40, 70, 90, 33)])
+def test_projection_in_a_graph(M, K, N, R):
+    # K in parts, the GEMM's epilogue, and a pass of its own
+    P = Problem(M, K, N, R, 4, order="requests")
+    packed, gamma = bl.quantize_weights(on_gpu(P.rng.standard_normal((N, K)) * 0.02))
+    call = lambda x, ids: bl.adapted_forward(x, packed, gamma, P.ads, ids, return_low=True)  # noqa: E731
+    x, ids = P.x.clone(), P.ids.clone()
+    call(x, ids)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(x, ids)
+    for k in range(4):
+        x.copy_(torch.roll(P.x, k, 0))
+        ids.copy_(torch.roll(P.ids, 3 * k, 0))
+        graph.replay()
+        eager = call(torch.roll(P.x, k, 0), torch.roll(P.ids, 3 * k, 0))
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], eager[0]) and torch.equal(out[1], eager[1])
+
+
 def test_more_outputs_than_32_bits():
     M, K, N, R = 70000, 8, 40000, 4  # 2.8e9 outputs
     g = torch.Generator(device=DEV).manual_seed(1)
@@ -272,6 +295,25 @@ def test_more_outputs_than_32_bits():
         a = int(ids[m])
         ref = (x[m].double() @ ads[0][a].double().T) @ ads[1][a].double() if a < 2 else torch.zeros(N, dtype=torch.float64, device=DEV)
         assert (y[m].double() - ref).abs().max() <= 1e-4 * (1 if a < 2 else 0)  # 12 terms of at most 50, 2^-24 each
+
+
+def test_more_codes_than_32_bits():
+    # the GEMM goes through the tokens in chunks of less than 2^31 codes
+    M, K, N, R = 2100, 1 << 20, 8, 16
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(M, K, generator=g, device=DEV).bfloat16()
+    packed, gamma = bl.quantize_weights(torch.randn(N, K, generator=g, device=DEV) * 0.02)
+    ads = (torch.randn(2, R, K, generator=g, device=DEV), torch.randn(2, R, N, generator=g, device=DEV), torch.ones(2, device=DEV))
+    ids = (torch.arange(M, device=DEV) // 300 % 3).to(torch.int32)  # 2: none
+    base = bl.forward(x, packed, gamma, K)
+    y, t = bl.adapted_forward(x, packed, gamma, ads, ids, return_low=True)
+    two, t2 = bl.adapters_forward(x, ads, ids, base.clone(), return_low=True)
+    assert torch.equal(t, t2) and torch.equal(y[ids == 2], base[ids == 2])
+    up = torch.cat([ads[1], torch.zeros_like(ads[1][:1])])[ids.long()].double()
+    terms = base.double().abs() + (t.double().abs()[:, :, None] * up.abs()).sum(1)
+    ref = base.double() + (t.double()[:, :, None] * up).sum(1)
+    for out in (y, two):  # 16 terms of three planes' products, their sum with the projection
+        assert ((out.double() - ref).abs() <= terms * (R + 72) * U24).all()
 
 
 @pytest.mark.parametrize("M", [5, 260])

@@ -265,6 +265,30 @@ def test_streams_and_graph():
         assert torch.equal(h1, bl.gated_forward(new[:1].contiguous(), P.gate.gpu, P.up.gpu))
 
 
+def test_parts_in_a_graph():
+    # the down product in parts of K, the input's gradient in parts of F
+    M, D, F = 40, 100, 4095
+    P = Problem(M, D, F, dt="bf16", backward=True)
+    down = Matrix(P.rng, 60, F).gpu
+    gateT, upT = (P.gate.T, P.gate.gpu[1]), (P.up.T, P.up.gpu[1])
+    dG, dU = (torch.randn(M, F, device=DEV).to(torch.bfloat16) for _ in range(2))
+    call = lambda x, a, b: (bl.gated_ffn_forward(x, P.gate.gpu, P.up.gpu, down),  # noqa: E731
+                            bl.gated_input_backward(a, b, gateT, upT, D))
+    x, a, b = P.x.clone(), dG.clone(), dU.clone()
+    call(x, a, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(x, a, b)
+    for k in range(4):
+        for to, src in ((x, P.x), (a, dG), (b, dU)):
+            to.copy_(torch.roll(src, k, 0))
+        graph.replay()
+        eager = call(*(torch.roll(t, k, 0) for t in (P.x, dG, dU)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, eager))
+
+
 @pytest.mark.parametrize("K", [1, 7, 8, 9, 63, 2041, 2049, 8191, 8193, 28671, 28673])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_codes_of_rows_of_any_length(K, dt):
