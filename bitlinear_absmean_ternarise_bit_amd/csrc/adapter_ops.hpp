@@ -126,9 +126,12 @@ hipError_t launch_adapted_first(const void* X, int x_dtype, int64_t M, int64_t K
 // 200x2048x5632 65 and 38).  More ranks take longer there; what is saved is the pass
 // over Y, so that has to be large (64 ranks: 2048x4096x4096 67 and 79, 512x4096x4096 44
 // and 45, 6852x487x128 36 and 33; more than 64 ranks were not measured); planes:
-// launch_join's.
+// launch_join's.  An adapter's R rows of `up` are one buffer resource there: below 2^31
+// bytes even of float32, or its size would not fit 32 bits and the offset that stands
+// for "nowhere" would lie inside it.
 inline bool adapted_gemm_takes(int64_t M, int64_t N, int64_t R) {
-  return M >= 256 && N >= 8 && N <= (int64_t(1) << 24) && (R <= 16 || (R <= 64 && M * N >= (int64_t(1) << 22)));
+  return M >= 256 && N >= 8 && N <= (int64_t(1) << 24) && R * N < (int64_t(1) << 29) &&
+         (R <= 16 || (R <= 64 && M * N >= (int64_t(1) << 22)));
 }
 hipError_t launch_adapted_gemm(const int8_t* Xq, const float* ga, const int32_t* rs, int64_t M, int64_t K,
                                const uint32_t* packed, int64_t N, const float* gamma, float* Y, const uint16_t* planes,
