@@ -72,9 +72,10 @@ __device__ __forceinline__ void store_masked(const f32x16 (&acc)[MI][NI], char* 
 }
 
 // bf16 MFMA GEMM, C[p, q] = sum_r A[p, r] B[q, r] over r < Rp (a multiple of 64).
-// A: bf16 [P, Rp] with row stride lda >= Rp, or, when B is packed, lda >= the
-// number of real columns (padding codes are zero weights, so whatever A holds
-// past a row's end only meets zeros); rows 16-byte aligned.  B: bf16 [Q, Rp]
+// A: bf16 [P, Rp] with row stride lda >= Rp, or, when B is packed, lda = the
+// number of real columns (what lies past a row's end is read as zeros: there it
+// meets padding codes, zero weights, but another row's infinities and NaN must
+// not); rows 16-byte aligned.  B: bf16 [Q, Rp]
 // (BMODE 0) or the 2-bit ternary codes of a [Q, Rp] matrix in the packed
 // format (BMODE 1), expanded to bf16 c - 1.
 // EPI 2: the sum of two products of the same shapes, gamma (A B^T) + gamma2
@@ -156,6 +157,7 @@ __device__ __forceinline__ void bf16_gemm_nt_body(
     a_off[i] = (p0 + r < P) ? static_cast<uint32_t>(p0 + r) * rowbytes_a + 16u * c : kOff;
     a_dst[i] = r * ROWB + 16 * (c ^ ((r >> 1) & 7));
   }
+  const int a_end = static_cast<int>(rowbytes_a) - 16 * (tid & 7);  // offsets within a row end here
   uint32_t b_off[B_LOADS], b_dst[B_LOADS];
   if constexpr (BMODE == 0) {
 #pragma unroll
@@ -173,9 +175,12 @@ __device__ __forceinline__ void bf16_gemm_nt_body(
   v4u ra[2][A_LOADS], rb[2][BMODE == 0 ? B_LOADS : 1];  // packed B: word i in element i
   auto gload_from = [&](__amdgpu_buffer_rsrc_t rsrc_a, __amdgpu_buffer_rsrc_t rsrc_b, int it, auto set_tag) {
     constexpr int S = decltype(set_tag)::value;
+    // (a thread's slots are the same 8 columns of different rows; sums of two offsets
+    // past the resource stay past it)
+    const uint32_t at = 128u * it, to = BMODE == 1 && static_cast<int>(at) >= a_end ? kOff : at;
 #pragma unroll
     for (int i = 0; i < A_LOADS; ++i)
-      ra[S][i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_a, a_off[i] == kOff ? kOff : a_off[i] + 128u * it, 0, 0);
+      ra[S][i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_a, __builtin_elementwise_add_sat(a_off[i], to), 0, 0);
     if constexpr (BMODE == 0) {
 #pragma unroll
       for (int i = 0; i < B_LOADS; ++i)

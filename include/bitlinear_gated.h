@@ -122,7 +122,8 @@ int bitlinear_gated_backward(const void* dH, int dh_dtype, const void* G, const 
  * dX = gamma_gate (dG W_gate) + gamma_up (dU W_up), W the ternary codes: both
  * products in one launch, float32 accumulation, each scaled and then added; with
  * few rows in parts of F, which a second launch adds in order (the activation
- * clip never binds, as for bitlinear_backward).
+ * clip never binds, as for bitlinear_backward).  A row of dX depends on that row of
+ * dG and dU alone: infinities and NaN in others do not reach it.
  * dG, dU: device bfloat16 [M, F] (bit patterns).  packedT_gate, packedT_up:
  * [D, F] matrices as bitlinear_pack_transposed writes them.  dX: device float32
  * [M, D].  workspace: >= bitlinear_gated_input_backward_workspace_bytes(M, F, D,
