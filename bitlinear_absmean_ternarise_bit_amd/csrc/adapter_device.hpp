@@ -27,15 +27,18 @@ constexpr int kPlanes = DT == kF32 ? 3 : 1;
 __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 __device__ __forceinline__ uint32_t lower(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 
-// Planes of two float32: what truncation leaves is exact each time, and the third
-// plane holds the last 8 bits.
+// Planes of two float32, each rounded half to even: what a plane leaves is exact (15
+// bits of the value, then 7), at most 2^-8 and 2^-17 of the value's power of two, and
+// the third plane holds all of it.  The first one stays finite where the value is.
 __device__ __forceinline__ void split(float a, float b, uint32_t (&p)[3]) {
+  constexpr float kTop = 338953138925153547590470800371487866880.0f;  // the largest bfloat16
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    p[i] = upper(ua, ub);
-    a = __fsub_rn(a, __uint_as_float(ua & 0xffff0000u));
-    b = __fsub_rn(b, __uint_as_float(ub & 0xffff0000u));
+    p[i] = i == 0 ? bf16_pair(__builtin_amdgcn_fmed3f(a, -kTop, kTop), __builtin_amdgcn_fmed3f(b, -kTop, kTop))
+                  : bf16_pair(a, b);
+    if (i == 2) break;
+    a = __fsub_rn(a, __uint_as_float(p[i] << 16));
+    b = __fsub_rn(b, __uint_as_float(p[i] & 0xffff0000u));
   }
 }
 

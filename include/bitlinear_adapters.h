@@ -27,9 +27,10 @@
  *         those of bitlinear_forward for M, N and K.
  *
  * Arithmetic: products and sums in float32 accuracy whatever the types.
- * float32 values go to the bf16 matrix cores as exact sums of three bfloat16
- * numbers, and only products below 2^-24 of the largest are left out; sums are
- * float32.  T is float32 and is not rounded to fewer bits.  Every sum is over
+ * float32 values go to the bf16 matrix cores as sums of three bfloat16 numbers,
+ * exact for values of 2^-110 and more (smaller ones to 2^-134), and at most
+ * 2^-24 (1 + 2^-10) of a product of two of them is left out, with either sign;
+ * products with bfloat16 weights or inputs are whole.  Sums are float32.  T is float32 and is not rounded to fewer bits.  Every sum is over
  * fixed parts in a fixed order (no atomics): results do not depend on
  * scheduling, and the same call gives the same bits.
  * A token's outputs depend on its own row of X (or dY) and its own adapter
