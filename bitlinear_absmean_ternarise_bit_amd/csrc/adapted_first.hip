@@ -2,7 +2,9 @@
 // (include/bitlinear_adapters.h): the adapters' first product and the tokens'
 // codes.  Either leaves most of the GPU waiting for its loads; together they read X
 // from memory once and are one launch (2048x4096 bf16, 16 ranks: 16.5 us, apart 11
-// and 8.2; one token of 2048 columns 4.8).
+// and 8.2; one token of 2048 columns 4.8).  With more than 32 ranks of float32 for 64
+// tokens a workgroup, 12 of a lane's registers go to scratch memory, 26 with X of
+// float32.
 #include <algorithm>
 
 #include "adapter_device.hpp"

@@ -2,7 +2,11 @@
 // INT8-MFMA GEMM with the adapters' second product in its epilogue
 // (prefill_gemm.hpp, EPI 4 to 7), for up to 64 ranks.  Y is written once; as a pass
 // of its own the second product reads and writes it again, 180 MB for 2048 tokens
-// of 11008 outputs (4096 inputs, 16 ranks: 106 us, the GEMM alone 88).
+// of 11008 outputs (4096 inputs, 16 ranks: 106 us, the GEMM alone 88).  Part of the
+// difference is scratch memory: Y's tile, T's planes, two sets of weights and a block's
+// product exceed a lane's 256 registers with 256 x 256 tiles, by 59 with 16 ranks of
+// bfloat16, 76 of float32, 136 and 150 with more ranks (128 x 256 tiles: none, none, 2
+// and 11; 128 x 128 none).  The main loop has none of it.
 #include <algorithm>
 
 #include "prefill_gemm.hpp"

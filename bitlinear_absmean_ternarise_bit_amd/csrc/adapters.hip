@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kAdapterThreads, 2) void shrink_kernel(const char* 
 // 2048x4096 and 64 ranks as much as Y itself.)
 // v_mfma_f32_16x16x16_bf16 with T as the rows (lane l: token l % 16, ranks
 // 4 (l / 16) .. + 3) and W as the columns: lane l loads CW consecutive columns
-// of its four rank rows, 16 or 32 bytes a load, and column j of each lane's
+// of its four rank rows, 8 or 16 bytes a load, and column j of each lane's
 // is an operand of its own, so no transposition through LDS is needed and a lane
 // ends with CW consecutive columns of four tokens of each block, which it adds
 // to Y.  2048x4096, 64 ranks of float32: 25 us for 67 MB of Y, of which a copy takes
@@ -243,7 +243,9 @@ __global__ __launch_bounds__(kAdapterThreads) void join_kernel(const float* __re
 // ranks, both gradients: 83 us with consecutive blocks to a wave, 53 in turn).  V is
 // the row operand (lane l: rank l % 16, tokens 4 (l / 16) .. + 3), X the columns as in
 // expand.  The waves' sums meet in LDS, and each wave then writes one of every four
-// ranks.
+// ranks.  With more than 32 ranks (RT = 4) two blocks of X and V beside 64 sums exceed a
+// lane's 256 registers: 24 of them go to scratch memory in the token loop, 69 with X of
+// float32.
 template <int XT, int RT>
 __global__ __launch_bounds__(kAdapterThreads, 2) void grad_kernel(const float* __restrict__ V, const char* __restrict__ X,
                                                         int64_t M, int64_t C, Adapters ad, float* __restrict__ out,
@@ -389,8 +391,10 @@ __global__ __launch_bounds__(kAdapterThreads) void grad_join_kernel(const float*
 }
 
 // ---- fewer than 8 columns (expand: or more than 2^24) -------------------------------
-// A lane's eight columns do not fit (a group's rows of Y do not fit a buffer
-// resource): one thread to a value, float32 sums.
+// A lane of shrink takes eight columns, and a row has to hold that many (a group's rows
+// of Y have to fit a buffer resource); else one thread to a value, float32 sums.  Lanes
+// of expand and grad take four: they could do with rows of 4 to 7, which go the same way
+// as in shrink so that there is one cut (no projection is that narrow).
 template <int DT>
 __device__ __forceinline__ float value_at(const char* p, int64_t i) {
   if constexpr (DT == kF32) return reinterpret_cast<const float*>(p)[i];

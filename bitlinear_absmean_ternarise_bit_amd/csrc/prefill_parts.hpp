@@ -14,6 +14,9 @@ namespace bitlinear {
 // the tile, while the others idle; parts are INT32 sums, exact in any order, and cost
 // a launch and their bytes.  64x4096 over 11008: 47 us in one part, 17 in 8; 43x251
 // over 10432: 43 and 12; 777x1003 over 2701 17 either way, so little gain is left out.
+// Up to 16 tokens stay in one part: the decode kernel takes them, but for rows too long
+// for its LDS (a gated block of 4096 x 11008: 72 us for 6 to 16 tokens, 41 for 17, 24
+// for 5).
 struct PrefillParts {
   int parts;
   int64_t saved;

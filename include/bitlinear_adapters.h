@@ -81,10 +81,11 @@ int bitlinear_adapters_forward(const void* X, int x_dtype, int64_t M, int64_t K,
  * on it.  packed, gamma, path: as for bitlinear_forward_ex.  workspace: >=
  * bitlinear_adapted_workspace_bytes(M, K, N, R), 256-byte aligned (activation
  * codes among it, and parts of the product where its tiles are few).  Up to 16 tokens
- * take two launches, except of weights with so many rows that the decode path streams
- * them (then three), more take three to five.  The adapters' sums may be
- * formed in another order than by the two calls one after the other; both are
- * within the accuracy above.
+ * take two launches, with three exceptions: weights with so many rows that the decode
+ * path streams them, tokens whose codes do not fit the decode kernel's LDS in four
+ * pieces, fewer than 8 inputs.  Those, more tokens and the prefill path take three or
+ * more.  The adapters' sums may be formed in another order than by the two calls one
+ * after the other; both are within the accuracy above.
  */
 size_t bitlinear_adapted_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t R);
 
