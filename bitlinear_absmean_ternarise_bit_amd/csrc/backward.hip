@@ -416,9 +416,12 @@ hipError_t launch_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, 
       pad_rows_bf16_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(dY, M, N, dYp, Np);
     }
     // 256 x 128 tiles: a 2048-token, 4096-column dX is 256 tiles, one per CU
-    launch_gemm<256, 128, 4, 2, 1, 0>(direct ? dY : dYp, M, direct ? N : Np, packedT, K, Np, dX, K, gamma,
-                                      nullptr, 0, static_cast<int>(M * (direct ? N : Np) * 2),
-                                      static_cast<int>(K * (Np / 4)), stream);
+    const int bytes_a = static_cast<int>(M * (direct ? N : Np) * 2), bytes_b = static_cast<int>(K * (Np / 4));
+    if (direct && N != Np)
+      launch_gemm<256, 128, 4, 2, 2, 0>(dY, M, N, packedT, K, Np, dX, K, gamma, nullptr, 0, bytes_a, bytes_b, stream);
+    else
+      launch_gemm<256, 128, 4, 2, 1, 0>(direct ? dY : dYp, M, Np, packedT, K, Np, dX, K, gamma, nullptr, 0, bytes_a,
+                                        bytes_b, stream);
   }
   if (dW && N % 8 == 0 && reinterpret_cast<uintptr_t>(dY) % 16 == 0 && reinterpret_cast<uintptr_t>(Xq) % 16 == 0) {
     // operands as they are: no transposed copies

@@ -72,12 +72,13 @@ __device__ __forceinline__ void store_masked(const f32x16 (&acc)[MI][NI], char* 
 }
 
 // bf16 MFMA GEMM, C[p, q] = sum_r A[p, r] B[q, r] over r < Rp (a multiple of 64).
-// A: bf16 [P, Rp] with row stride lda >= Rp, or, when B is packed, lda = the
-// number of real columns (what lies past a row's end is read as zeros: there it
-// meets padding codes, zero weights, but another row's infinities and NaN must
-// not); rows 16-byte aligned.  B: bf16 [Q, Rp]
+// A: bf16 [P, Rp] with row stride lda >= Rp; rows 16-byte aligned.  B: bf16 [Q, Rp]
 // (BMODE 0) or the 2-bit ternary codes of a [Q, Rp] matrix in the packed
-// format (BMODE 1), expanded to bf16 c - 1.
+// format (BMODE 1), expanded to bf16 c - 1.  BMODE 2: packed, and A's rows hold
+// lda < Rp columns (a multiple of 8): what lies past a row's end is read as
+// zeros, since the next row's infinities and NaN must not meet the padding
+// codes' zero weights.  (In the same kernel the comparison cost whole rows 1 to
+// 2%: 17x2048 over 5632 68.2 us and 69.5.)
 // EPI 2: the sum of two products of the same shapes, gamma (A B^T) + gamma2
 // (A2 B2^T): the stages of the second follow those of the first without a
 // break, and the first one's accumulators are scaled and put by in between (64
@@ -157,7 +158,7 @@ __device__ __forceinline__ void bf16_gemm_nt_body(
     a_off[i] = (p0 + r < P) ? static_cast<uint32_t>(p0 + r) * rowbytes_a + 16u * c : kOff;
     a_dst[i] = r * ROWB + 16 * (c ^ ((r >> 1) & 7));
   }
-  const int a_end = static_cast<int>(rowbytes_a) - 16 * (tid & 7);  // offsets within a row end here
+  const int a_end = static_cast<int>(rowbytes_a) - 16 * (tid & 7);  // (BMODE 2) offsets within a row end here
   uint32_t b_off[B_LOADS], b_dst[B_LOADS];
   if constexpr (BMODE == 0) {
 #pragma unroll
@@ -177,10 +178,12 @@ __device__ __forceinline__ void bf16_gemm_nt_body(
     constexpr int S = decltype(set_tag)::value;
     // (a thread's slots are the same 8 columns of different rows; sums of two offsets
     // past the resource stay past it)
-    const uint32_t at = 128u * it, to = BMODE == 1 && static_cast<int>(at) >= a_end ? kOff : at;
+    const uint32_t at = 128u * it, to = static_cast<int>(at) >= a_end ? kOff : at;
 #pragma unroll
-    for (int i = 0; i < A_LOADS; ++i)
-      ra[S][i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_a, __builtin_elementwise_add_sat(a_off[i], to), 0, 0);
+    for (int i = 0; i < A_LOADS; ++i) {
+      const uint32_t off = BMODE == 2 ? __builtin_elementwise_add_sat(a_off[i], to) : a_off[i] == kOff ? kOff : a_off[i] + at;
+      ra[S][i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_a, off, 0, 0);
+    }
     if constexpr (BMODE == 0) {
 #pragma unroll
       for (int i = 0; i < B_LOADS; ++i)

@@ -64,7 +64,7 @@ hipError_t launch_to(const void* dH, const void* G, const void* U, int64_t n, in
 // 310 to 330 us, 1.12 to 1.19 PFLOP/s, where the library's large bfloat16 product
 // reaches 1.4; one launch for both saves writing and reading dX between.  Part blockIdx.y of
 // the contraction, each with a C of its own
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int BMODE>
 __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_two_products_kernel(
     const uint16_t* __restrict__ A, int64_t P, int64_t lda, const void* __restrict__ B, int64_t Q, int64_t Rp,
     float* __restrict__ C, const float* __restrict__ gamma, int bytes_a, int bytes_b, int tiles_p, int tiles_q,
@@ -72,8 +72,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void bf16_two_products_kernel(
   const int stages = static_cast<int>(Rp / 64), part = blockIdx.y, parts = gridDim.y;
   second.first = static_cast<int>(static_cast<int64_t>(part) * stages / parts);
   second.count = static_cast<int>(static_cast<int64_t>(part + 1) * stages / parts) - second.first;
-  bf16_gemm_nt_body<BM, BN, WM, WN, 1, 2>(A, P, lda, B, Q, Rp, C + part * P * Q, Q, gamma, nullptr, 0, bytes_a, bytes_b,
-                                          tiles_p, tiles_q, second);
+  bf16_gemm_nt_body<BM, BN, WM, WN, BMODE, 2>(A, P, lda, B, Q, Rp, C + part * P * Q, Q, gamma, nullptr, 0, bytes_a,
+                                              bytes_b, tiles_p, tiles_q, second);
 }
 
 // dX = the sum of its parts, in order
@@ -126,9 +126,13 @@ hipError_t launch_gated_input_backward(const uint16_t* dG, const uint16_t* dU, i
         dG, M, lda, packedT_gate, D, Fp, plan.parts > 1 ? parts : dX, gamma_gate, bytes_a, bytes_b, tiles_p, tiles_q,
         second);
   };
-  if (plan.bm == 256) go(bf16_two_products_kernel<256, 128, 4, 2>, 256, 128, 512);
-  else if (plan.bm == 128) go(bf16_two_products_kernel<128, 128, 2, 2>, 128, 128, 256);
-  else go(bf16_two_products_kernel<64, 64, 1, 2>, 64, 64, 128);
+  const bool whole = lda == Fp;
+  if (plan.bm == 256)
+    go(whole ? bf16_two_products_kernel<256, 128, 4, 2, 1> : bf16_two_products_kernel<256, 128, 4, 2, 2>, 256, 128, 512);
+  else if (plan.bm == 128)
+    go(whole ? bf16_two_products_kernel<128, 128, 2, 2, 1> : bf16_two_products_kernel<128, 128, 2, 2, 2>, 128, 128, 256);
+  else
+    go(whole ? bf16_two_products_kernel<64, 64, 1, 2, 1> : bf16_two_products_kernel<64, 64, 1, 2, 2>, 64, 64, 128);
   if (plan.parts > 1) {
     const int64_t blocks = (M * D + 255) / 256;
     sum_parts_kernel<<<static_cast<unsigned>(blocks < 65536 ? blocks : 65536), 256, 0, stream>>>(parts, plan.parts, M * D,
