@@ -30,9 +30,11 @@
  * float32 values go to the bf16 matrix cores as sums of three bfloat16 numbers,
  * exact for values of 2^-110 and more (smaller ones to 2^-134), and at most
  * 2^-24 (1 + 2^-10) of a product of two of them is left out, with either sign;
- * products with bfloat16 weights or inputs are whole.  Sums are float32.  T is float32 and is not rounded to fewer bits.  Every sum is over
- * fixed parts in a fixed order (no atomics): results do not depend on
- * scheduling, and the same call gives the same bits.
+ * products with bfloat16 weights or inputs are whole.  Sums are float32; those
+ * that come within 2^-8 of the largest float32 on the way may overflow.  T is
+ * float32 and is not rounded to fewer bits.  Every sum is over fixed parts in a
+ * fixed order (no atomics): results do not depend on scheduling, and the same
+ * call gives the same bits.
  * A token's outputs depend on its own row of X (or dY) and its own adapter
  * only: infinities and NaN elsewhere do not reach it.  In a token's own row or
  * adapter they make its outputs non-finite, not always with the same value as
